@@ -414,7 +414,7 @@ def _plain_plan(s):
     need = (n + m + PAGE - 1) // PAGE
     grow = torch.where(fits, (need - pages).clamp(min=0), 0).reshape(-1)
     before = torch.cumsum(grow, 0) - grow
-    given = (before + grow <= count).reshape(b, hkv) & fits
+    given = ((grow == 0) | (before + grow <= count)).reshape(b, hkv) & fits
     grow = torch.where(given.reshape(-1), grow, 0)
     back = torch.where(given, (pages - need).clamp(min=0), 0).reshape(-1) if s["release"] \
         else torch.zeros_like(grow)
