@@ -10,6 +10,11 @@
  *   - H2O heavy-hitter scores and eviction    -- kvc_h2o_accumulate, kvc_h2o_evict
  *   - whole decode steps in one launch        -- kvc_h2o_decode_step,
  *                                                kvc_stream_decode_step
+ *   - attention of whole prompts and of chunks of new tokens over the slot cache
+ *                                             -- kvc_prompt_attend, kvc_chunk_attend
+ *   - ragged appends: page tables, slot map and lengths of a batch whose
+ *     sequences bring different numbers of tokens, and the rows themselves
+ *                                             -- kvc_append_plan, kvc_append_packed
  *   - StreamingLLM sink + recent window       -- kvc_stream_evict, kvc_stream_append
  *   - per-head uniform random eviction with the prompt locked
  *                                             -- kvc_random_evict
@@ -501,6 +506,144 @@ KVC_API kvc_status kvc_stream_decode_step(const kvc_slot_cache *cache, int Hq, c
  */
 KVC_API kvc_status kvc_random_evict(const kvc_slot_cache *cache, int prompt_len, double keep_ratio,
                             uint64_t seed, uint32_t epoch, cudaStream_t stream);
+
+/*
+ * kvc_prompt_attend -- causal attention over whole prompts, with grouped heads.
+ * Token i of a sequence attends the tokens j <= i of the same sequence:
+ *   o = sum_j softmax_j(scale q_i . k_j) v_j,   lse = log sum_j exp(scale q_i . k_j)
+ * Two layouts:
+ *   packed   cu_seqlens [B + 1] int32 (device): sequence b is the tokens
+ *            [cu_seqlens[b], cu_seqlens[b+1]) of q, k, v and o, which hold L
+ *            tokens in all; tokens outside every sequence are left as they were.
+ *   padded   cu_seqlens NULL: every sequence has room for L tokens of which the
+ *            first lens[b] (device int32 [B]; NULL: L) count; o and lse of the
+ *            others are left as they were and q, k, v of the others may hold
+ *            anything.
+ * q, k, v, o are binary16 with D adjacent channels per row; *_stride give the
+ * distance in elements between sequences (padded only), heads and tokens, each
+ * a positive multiple of 8, so q, k and v may be column ranges of one projection's
+ * output.  lse (optional) is fp32 with adjacent tokens: [B, Hq, L] padded,
+ * [Hq, L] packed.  The padded lse is what kvc_h2o_accumulate(KVC_H2O_PREFILL) takes
+ * as the rows' normalisers, so a prompt's heavy-hitter scores cost one more pass.
+ * A non-finite key or value row affects the rows that attend it and no others.
+ * A sequence whose range leaves [0, L] counts as empty and sets KVC_DEV_CAPACITY.
+ * No workspace.  Source: "Rethinking KV Cache Compression" guide, §16 "Prefill、decode、TP 的
+ * 性能账" (the prefill computes the prompt's attention in one pass) and "局限与
+ * 最终结论" (flash attention never materialises the probabilities).
+ */
+typedef struct kvc_prompt_args {
+    int B, Hq, Hkv, D;
+    int L;
+    const uint16_t *q, *k, *v;
+    uint16_t *o;
+    float *lse;
+    const int32_t *cu_seqlens;
+    const int32_t *lens;
+    int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3]; /* sequence, head, token */
+    float softmax_scale; /* 0 for 1/sqrt(D) */
+} kvc_prompt_args;
+
+KVC_API kvc_status kvc_prompt_attend(const kvc_prompt_args *args, cudaStream_t stream);
+
+/*
+ * kvc_chunk_attend -- attention of a chunk of new tokens per sequence over the
+ * slot cache (dense or paged): the pieces of a prompt that is taken in chunks, or
+ * drafted tokens that are checked together.  The chunk's K/V rows are already in
+ * the cache, in the last m_b of each unit's n slots and in order, as kvc_append and
+ * kvc_append_plan + kvc_append_packed leave them (evict after the attention, as in a
+ * decode step).  Query token i of sequence b's m_b attends the slots
+ *   j < n[b,hk] - m_b + i + 1,
+ * so every older slot and, of the chunk, the tokens up to itself.  With m_b = 1 this
+ * is kvc_decode_attend; m_b = 0 leaves the sequence out.
+ *   q, o     the T new tokens of all sequences, packed: sequence b's are
+ *            [cu_new[b], cu_new[b+1]) (device int32 [B + 1]); strides in elements
+ *            between heads and between tokens, positive multiples of 8
+ *   lse      optional [Hq, T] fp32
+ *   workspace  kvc_chunk_workspace_size(args) bytes (16-byte aligned; may be NULL
+ *            when that is 0); calls that may overlap on the GPU need one each
+ *   num_splits  0: chosen from the sizes; otherwise ranges per unit that are
+ *            computed apart and merged
+ * A row that sees no slot gives o = 0 and lse = -inf.  A unit whose n leaves [0, C]
+ * counts as empty and sets KVC_DEV_CAPACITY; so does a sequence whose range leaves
+ * [0, T]; a read through a page outside the pool yields no data and sets it too.
+ * Rows of the cache behind n may hold anything.
+ * Source: "Rethinking KV Cache Compression" guide, §16 "Prefill、decode、TP 的性能账"
+ * and "前置背景、复现方法与结论边界" (the paged cache of continuous batching).
+ */
+typedef struct kvc_chunk_args {
+    int Hq;
+    int T;
+    const kvc_slot_cache *cache;
+    const uint16_t *q;
+    uint16_t *o;
+    const int32_t *cu_new;
+    float *lse;
+    int64_t q_stride[2], o_stride[2]; /* head, token */
+    void *workspace;
+    size_t workspace_bytes;
+    int num_splits;
+    float softmax_scale; /* 0 for 1/sqrt(D) */
+} kvc_chunk_args;
+
+KVC_API size_t kvc_chunk_workspace_size(const kvc_chunk_args *args);
+KVC_API kvc_status kvc_chunk_attend(const kvc_chunk_args *args, cudaStream_t stream);
+
+/*
+ * kvc_append_plan -- where the new tokens of a ragged batch go.  Sequence b brings
+ * m_b = cu_new[b+1] - cu_new[b] tokens (0 allowed); per unit (b, h) they take the
+ * slots n .. n + m_b - 1.  The call writes
+ *   slot_map [T, Hkv]  the row of the cache's K / V arrays that token t's K/V of
+ *                      head h go to (b h C + slot dense, page 64 + slot % 64 paged),
+ *                      or -1: a token of a refused unit, or behind cu_new[B]
+ *   next->pos          the new slots' positions seqlen[b] + i
+ *   next->n, seqlen    n + m_b and seqlen + m_b
+ * and, in the paged layout, gives every unit the pages it needs.  Unit (b, h) holds
+ * its first pages[b,h] table entries; free_list[0 .. count) is a stack of the pages
+ * that nobody holds.  With need = ceil((n + m_b) / 64), a unit that holds fewer pages
+ * takes the missing ones from the top of the stack, the units in order; with
+ * release != 0 a unit that holds more (an eviction compacted it) gives the pages
+ * behind `need` back: their entries become -1 and, after all takes, they go on the
+ * stack in unit order, each unit's lowest entry first.  Entries of the stack at and
+ * behind the new count are unspecified.
+ * A unit is refused, sets KVC_DEV_CAPACITY and keeps its n and pages when n + m_b
+ * exceeds C or the stack cannot serve it in full (its sequence's seqlen still
+ * advances, as in kvc_append).  A sequence whose range leaves [0, T] counts as
+ * bringing none and sets the same bit.
+ * `next` gives the arrays to write: the cache itself and the same pool (the step in
+ * place), or others of the same sizes, so that the next step can be planned while
+ * this one's attention still reads the old state; then table, counts and stack are
+ * written in full.  An output array is either the same as its input or does not
+ * overlap any input.  next->K and next->V are not used.  B * Hkv is at most
+ * KVC_PLAN_MAX_UNITS.  One launch, no workspace, deterministic.
+ * Source: "Rethinking KV Cache Compression" guide, §16 "前置背景、复现方法与结论边界"
+ * (blocks allocated non-contiguously, batched continuously); "Practical Online KV
+ * Cache Compaction for LLM Agents", §4.2 (compaction frees the tail).
+ */
+#define KVC_PLAN_MAX_UNITS 65536
+typedef struct kvc_page_pool {
+    int32_t *pages;     /* [B, Hkv] pages held by each unit */
+    int32_t *free_list; /* [num_pages] */
+    int32_t *count;     /* [1] pages on the stack */
+} kvc_page_pool;
+
+KVC_API kvc_status kvc_append_plan(const kvc_slot_cache *cache, const kvc_page_pool *pool,
+                                   const int32_t *cu_new, int T, int release,
+                                   const kvc_slot_cache *next, const kvc_page_pool *next_pool,
+                                   int32_t *slot_map, cudaStream_t stream);
+
+/*
+ * kvc_append_packed -- write the packed new tokens' K/V rows (T tokens, Hkv heads, D
+ * adjacent channels; strides in elements between tokens and between heads, positive
+ * multiples of 8) to the rows of the cache that slot_map [T, Hkv] names, as
+ * kvc_append_plan wrote it.  Entries of -1 are skipped; any other entry outside the
+ * cache's rows is skipped and sets KVC_DEV_CAPACITY.  The rows named must differ.
+ * n, pos, seqlen and the page table are not touched.
+ * Source: as kvc_append.
+ */
+KVC_API kvc_status kvc_append_packed(const kvc_slot_cache *cache, const uint16_t *k_new,
+                                     const int64_t k_stride[2], const uint16_t *v_new,
+                                     const int64_t v_stride[2], int T, const int32_t *slot_map,
+                                     cudaStream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 KVC_API const char *kvc_status_string(kvc_status status);

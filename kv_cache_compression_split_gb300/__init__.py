@@ -30,6 +30,7 @@ KIVI_GROUP = 32
 PAGE_SLOTS = 64            # KVC_PAGE_SLOTS: slots per page of the paged layout
 KIVI_PAGE_GROUPS = 4       # KVC_KIVI_PAGE_GROUPS: 32-token groups per KIVI page
 H2O_ONCHIP_MAX_SLOTS = 1024   # KVC_H2O_ONCHIP_MAX_SLOTS: fused H2O with logits kept on chip
+PLAN_MAX_UNITS = 65536     # KVC_PLAN_MAX_UNITS: units of one kvc_append_plan
 KVC_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
 
@@ -71,6 +72,29 @@ class H2OArgs(C.Structure):
                 ("decay", C.c_float)]
 
 
+_I64x2, _I64x3 = C.c_int64 * 2, C.c_int64 * 3
+
+
+class PromptArgs(C.Structure):
+    _fields_ = [("B", C.c_int), ("Hq", C.c_int), ("Hkv", C.c_int), ("D", C.c_int),
+                ("L", C.c_int), ("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p),
+                ("o", C.c_void_p), ("lse", C.c_void_p), ("cu_seqlens", C.c_void_p),
+                ("lens", C.c_void_p), ("q_stride", _I64x3), ("k_stride", _I64x3),
+                ("v_stride", _I64x3), ("o_stride", _I64x3), ("softmax_scale", C.c_float)]
+
+
+class ChunkArgs(C.Structure):
+    _fields_ = [("Hq", C.c_int), ("T", C.c_int), ("cache", C.POINTER(SlotCacheDesc)),
+                ("q", C.c_void_p), ("o", C.c_void_p), ("cu_new", C.c_void_p),
+                ("lse", C.c_void_p), ("q_stride", _I64x2), ("o_stride", _I64x2),
+                ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t),
+                ("num_splits", C.c_int), ("softmax_scale", C.c_float)]
+
+
+class PagePoolDesc(C.Structure):
+    _fields_ = [("pages", C.c_void_p), ("free_list", C.c_void_p), ("count", C.c_void_p)]
+
+
 def lib():
     """Load libkvc.so (raises if it has not been built)."""
     global _lib
@@ -101,6 +125,14 @@ def lib():
                                                 P]),
                 "kvc_random_evict": (st, [C.POINTER(SlotCacheDesc), i, C.c_double, C.c_uint64,
                                           C.c_uint32, P]),
+                "kvc_prompt_attend": (st, [C.POINTER(PromptArgs), P]),
+                "kvc_chunk_workspace_size": (C.c_size_t, [C.POINTER(ChunkArgs)]),
+                "kvc_chunk_attend": (st, [C.POINTER(ChunkArgs), P]),
+                "kvc_append_plan": (st, [C.POINTER(SlotCacheDesc), C.POINTER(PagePoolDesc), P, i,
+                                         i, C.POINTER(SlotCacheDesc), C.POINTER(PagePoolDesc), P,
+                                         P]),
+                "kvc_append_packed": (st, [C.POINTER(SlotCacheDesc), P, _I64x2, P, _I64x2, i, P,
+                                           P]),
                 "kvc_status_string": (C.c_char_p, [i]),
                 "kvc_read_device_status": (st, [C.POINTER(C.c_int), P]),
             }
@@ -156,6 +188,37 @@ def _state_without_desc(obj):
         state.pop(k, None)
     return state
 
+
+
+def _rows(t, what, dims):
+    """Device address of binary16 rows: a tensor of `dims` dimensions whose last one is
+    contiguous; the others may have any strides, which the call passes on."""
+    if t.dtype is not torch.float16:
+        raise ValueError(f"kvc: {what} must be float16, got {t.dtype}")
+    if t.dim() != dims or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError(f"kvc: {what} must have {dims} dimensions, the last one contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"kvc: tensor on {t.device}; the library takes CUDA tensors")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"kvc: tensor on {t.device}, expected the current device "
+                         f"cuda:{torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
+def _typed(t, what, dtype, shape):
+    """Device address of a contiguous tensor of this type and shape (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or tuple(t.shape) != shape:
+        raise ValueError(f"kvc: {what} must be {dtype} of shape {shape}, got {t.dtype} of "
+                         f"{tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _stride(t, dim):
+    """Element stride of a dimension; one of size 1 is never stepped over, so any stride
+    stands for it."""
+    return t.stride(dim) if t.shape[dim] > 1 else 8
 
 
 def _stream(stream):
@@ -344,6 +407,113 @@ def kvc_random_evict(cache: "SlotCache", prompt_len: int, keep_ratio: float, see
            "kvc_random_evict")
 
 
+def kvc_prompt_attend(q, k, v, o, cu_seqlens=None, lens=None, lse=None,
+                      softmax_scale: float = 0.0, stream=None):
+    """Causal attention over whole prompts (see kvc.h).  Packed: q, o [T, Hq, D], k, v
+    [T, Hkv, D], cu_seqlens [B + 1] int32, lse [Hq, T].  Padded: q, o [B, Hq, L, D], k, v
+    [B, Hkv, >= L, D], optional lens [B] int32, lse [B, Hq, L].  Rows may be strided."""
+    a = PromptArgs()
+    if cu_seqlens is not None:
+        if lens is not None:
+            raise ValueError("kvc_prompt_attend takes cu_seqlens (packed) or lens (padded)")
+        T, Hq, D = q.shape
+        Hkv = k.shape[1]
+        a.B, a.L, seq, dims = cu_seqlens.numel() - 1, T, (), 3
+        kv, tok, head = (T, Hkv, D), 0, 1
+    else:
+        B, Hq, T, D = q.shape
+        Hkv = k.shape[1]
+        a.B, a.L, seq, dims = B, T, (B,), 4
+        kv, tok, head = (B, Hkv, T, D), 2, 1
+        if k.dim() == 4 and k.shape[2] > T:
+            k = k[:, :, :T]
+        if v.dim() == 4 and v.shape[2] > T:
+            v = v[:, :, :T]
+    if tuple(k.shape) != kv or tuple(v.shape) != kv or o.shape != q.shape:
+        raise ValueError(f"kvc_prompt_attend: q {tuple(q.shape)}, k {tuple(k.shape)}, v "
+                         f"{tuple(v.shape)}, o {tuple(o.shape)} do not belong together")
+    a.cu_seqlens = _typed(cu_seqlens, "cu_seqlens", torch.int32, (a.B + 1,))
+    a.lens = _typed(lens, "lens", torch.int32, (a.B,))
+    a.Hq, a.Hkv, a.D = Hq, Hkv, D
+    a.q, a.k, a.v, a.o = (_rows(q, "q", dims), _rows(k, "k", dims), _rows(v, "v", dims),
+                          _rows(o, "o", dims))
+    for t, s in ((q, a.q_stride), (k, a.k_stride), (v, a.v_stride), (o, a.o_stride)):
+        if seq:
+            s[0] = _stride(t, 0)
+        s[1], s[2] = _stride(t, head), _stride(t, tok)
+    a.lse = _typed(lse, "lse", torch.float32, (*seq, Hq, T))
+    a.softmax_scale = float(softmax_scale)
+    _check(lib().kvc_prompt_attend(C.byref(a), _stream(stream)), "kvc_prompt_attend")
+
+
+def _chunk_args(cache, q, num_splits, scale):
+    a = ChunkArgs()
+    if q.dim() != 3 or q.shape[2] != cache.D:
+        raise ValueError(f"kvc_chunk_attend: q must be [T, Hq, {cache.D}], got {tuple(q.shape)}")
+    d = cache.desc()
+    a.cache = cache.__dict__["_desc_p"]
+    a.T, a.Hq = int(q.shape[0]), int(q.shape[1])
+    a.num_splits = int(num_splits)
+    a.softmax_scale = float(scale)
+    return a, d
+
+
+def kvc_chunk_workspace_size(cache: "SlotCache", q, num_splits: int = 0) -> int:
+    a, _keep = _chunk_args(cache, q, num_splits, 0.0)
+    return int(lib().kvc_chunk_workspace_size(C.byref(a)))
+
+
+def kvc_chunk_attend(cache: "SlotCache", q, cu_new, o, lse=None, workspace=None,
+                     num_splits: int = 0, softmax_scale: float = 0.0, stream=None):
+    """Attention of each sequence's chunk of new tokens over the slot cache, which already
+    holds their rows in the last slots (see kvc.h): q, o [T, Hq, D] packed by cu_new [B + 1]
+    int32 (rows may be strided), lse [Hq, T]."""
+    a, _keep = _chunk_args(cache, q, num_splits, softmax_scale)
+    if o.shape != q.shape:
+        raise ValueError("kvc_chunk_attend: o must have q's shape")
+    a.q, a.o = _rows(q, "q", 3), _rows(o, "o", 3)
+    a.cu_new = _typed(cu_new, "cu_new", torch.int32, (cache.B + 1,))
+    for t, s in ((q, a.q_stride), (o, a.o_stride)):
+        s[0], s[1] = _stride(t, 1), _stride(t, 0)
+    a.lse = _typed(lse, "lse", torch.float32, (a.Hq, a.T))
+    a.workspace = _ptr(workspace)
+    a.workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().kvc_chunk_attend(C.byref(a), _stream(stream)), "kvc_chunk_attend")
+
+
+def kvc_append_plan(cache: "SlotCache", cu_new, slot_map, pool: "Optional[PagePool]" = None,
+                    out: "Optional[SlotCache]" = None, pool_out: "Optional[PagePool]" = None,
+                    release: bool = False, stream=None):
+    """Page tables, slot map [T, Hkv] int32, positions and lengths of a ragged batch of new
+    tokens (cu_new [B + 1] int32).  A paged cache takes its pages from `pool`.  `out` and
+    `pool_out` receive the new state (default: the cache and the pool, in place)."""
+    d = cache.desc()
+    n = out.desc() if out is not None else d
+    pi = pool.desc(cache) if pool is not None else None
+    po = pool_out.desc(out if out is not None else cache) if pool_out is not None else pi
+    T = int(slot_map.shape[0])
+    _check(lib().kvc_append_plan(C.byref(d), None if pi is None else C.byref(pi),
+                                 _typed(cu_new, "cu_new", torch.int32, (cache.B + 1,)), T,
+                                 int(release), C.byref(n), None if po is None else C.byref(po),
+                                 _typed(slot_map, "slot_map", torch.int32, (T, cache.Hkv)),
+                                 _stream(stream)), "kvc_append_plan")
+
+
+def kvc_append_packed(cache: "SlotCache", k_new, v_new, slot_map, stream=None):
+    """Packed rows k_new, v_new [T, Hkv, D] (rows may be strided) to the cache rows that
+    slot_map [T, Hkv] names (kvc_append_plan writes it); n and pos are not touched."""
+    d = cache.desc()
+    shape = (int(slot_map.shape[0]), cache.Hkv, cache.D)
+    if tuple(k_new.shape) != shape or tuple(v_new.shape) != shape:
+        raise ValueError(f"kvc_append_packed: k_new and v_new must be {shape}")
+    ks = _I64x2(_stride(k_new, 0), _stride(k_new, 1))
+    vs = _I64x2(_stride(v_new, 0), _stride(v_new, 1))
+    _check(lib().kvc_append_packed(C.byref(d), _rows(k_new, "k_new", 3), ks,
+                                   _rows(v_new, "v_new", 3), vs, shape[0],
+                                   _typed(slot_map, "slot_map", torch.int32, shape[:2]),
+                                   _stream(stream)), "kvc_append_packed")
+
+
 def kvc_read_device_status(stream=None) -> int:
     out = C.c_int(0)
     st = lib().kvc_read_device_status(C.byref(out), _stream(stream))
@@ -422,6 +592,29 @@ class SlotCache:
         self.__dict__["_desc"], self.__dict__["_desc_key"] = d, key
         self.__dict__["_desc_p"] = C.pointer(d)
         return d
+
+
+@dataclass
+class PagePool:
+    """Pages of a paged slot cache (see kvc_append_plan): pages [B, Hkv] int32 held by each
+    unit, free [num_pages] int32 a stack of the pages nobody holds, count [1] int32."""
+    pages: torch.Tensor
+    free: torch.Tensor
+    count: torch.Tensor
+
+    @classmethod
+    def empty(cls, cache: "SlotCache"):
+        """Every page free, none held; the cache's table becomes -1 throughout."""
+        dev = cache.n.device
+        cache.block_table.fill_(-1)
+        return cls(pages=torch.zeros_like(cache.n),
+                   free=torch.arange(cache.num_pages - 1, -1, -1, dtype=torch.int32, device=dev),
+                   count=torch.full((1,), cache.num_pages, dtype=torch.int32, device=dev))
+
+    def desc(self, cache: "SlotCache") -> PagePoolDesc:
+        return PagePoolDesc(_typed(self.pages, "pages", torch.int32, (cache.B, cache.Hkv)),
+                            _typed(self.free, "free", torch.int32, (cache.num_pages,)),
+                            _typed(self.count, "count", torch.int32, (1,)))
 
 
 @dataclass

@@ -17,6 +17,8 @@ __device__ int g_status;   // KVC_DEV_* bits, one word per device
 
 constexpr int MAX_DEVICES = 64;
 constexpr int EVICT_MAX_SLOTS = 65536;
+constexpr int MAX_GRID_Y = 65535;
+constexpr float LOG2E = 1.4426950408889634f;
 
 int *g_status_ptr[MAX_DEVICES];
 int g_sm_count[MAX_DEVICES];
@@ -653,6 +655,204 @@ kvc_status kvc_random_evict(const kvc_slot_cache *cache, int prompt_len, double 
     e.seed = seed;
     e.epoch = epoch;
     return from_cuda(launch_evict(e, stream));
+}
+
+// Strides of rows of D adjacent elements: positive multiples of 16 bytes.
+static bool strides_ok(const int64_t *st, int count)
+{
+    for (int i = 0; i < count; ++i)
+        if (st[i] <= 0 || st[i] % 8 != 0 || st[i] > (int64_t)1 << 38)
+            return false;
+    return true;
+}
+
+kvc_status kvc_prompt_attend(const kvc_prompt_args *a, cudaStream_t stream)
+{
+    if (!a || a->B <= 0 || a->Hkv <= 0 || a->Hq <= 0 || a->Hq % a->Hkv != 0 || a->L < 0)
+        return KVC_ERR_INVALID_ARG;
+    if (!head_dim_ok(a->D) || a->Hq / a->Hkv > 8 || a->Hkv > MAX_GRID_Y)
+        return KVC_ERR_UNSUPPORTED;
+    if (a->cu_seqlens && a->lens)
+        return KVC_ERR_INVALID_ARG;
+    if (a->L == 0)
+        return KVC_OK;
+    const int first = a->cu_seqlens || a->B == 1 ? 1 : 0;   // one sequence: its stride is not used
+    if (!a->q || !a->k || !a->v || !a->o || !aligned16(a->q) || !aligned16(a->k) ||
+        !aligned16(a->v) || !aligned16(a->o) || !strides_ok(a->q_stride + first, 3 - first) ||
+        !strides_ok(a->k_stride + first, 3 - first) ||
+        !strides_ok(a->v_stride + first, 3 - first) || !strides_ok(a->o_stride + first, 3 - first))
+        return KVC_ERR_INVALID_ARG;
+    if ((long long)(a->cu_seqlens ? 1 : a->B) * a->L * a->Hq > (long long)INT_MAX)
+        return KVC_ERR_UNSUPPORTED;
+    TokensLaunch p{};
+    p.B = a->B;
+    p.Hq = a->Hq;
+    p.Hkv = a->Hkv;
+    p.D = a->D;
+    p.L = a->L;
+    p.q = a->q;
+    p.k = a->k;
+    p.v = a->v;
+    p.o = a->o;
+    p.lse = a->lse;
+    for (int i = first; i < 3; ++i) {
+        p.qs[i] = a->q_stride[i];
+        p.ks[i] = a->k_stride[i];
+        p.vs[i] = a->v_stride[i];
+        p.os[i] = a->o_stride[i];
+    }
+    p.ls[0] = (long)a->Hq * a->L;
+    p.ls[1] = a->L;
+    p.cu = a->cu_seqlens;
+    p.lens = a->lens;
+    p.scale_log2 = (a->softmax_scale > 0.f ? a->softmax_scale : 1.0f / sqrtf((float)a->D)) *
+                   LOG2E;
+    p.status = dev_status_ptr();
+    return from_cuda(launch_attend_tokens(p, stream));
+}
+
+// The checks of a chunk's sizes; its pointers are checked by the call itself.
+static kvc_status check_chunk(const kvc_chunk_args *a)
+{
+    if (!a)
+        return KVC_ERR_INVALID_ARG;
+    const kvc_status st = check_slot_cache(a->cache);
+    if (st != KVC_OK)
+        return st;
+    const kvc_slot_cache &c = *a->cache;
+    if (a->Hq <= 0 || a->Hq % c.Hkv != 0 || a->T < 0 || a->num_splits < 0)
+        return KVC_ERR_INVALID_ARG;
+    if (a->Hq / c.Hkv > 8 || c.Hkv > MAX_GRID_Y || (long long)a->T * a->Hq > (long long)INT_MAX)
+        return KVC_ERR_UNSUPPORTED;
+    return KVC_OK;
+}
+
+size_t kvc_chunk_workspace_size(const kvc_chunk_args *a)
+{
+    (void)a;
+    return 0;
+}
+
+kvc_status kvc_chunk_attend(const kvc_chunk_args *a, cudaStream_t stream)
+{
+    const kvc_status st = check_chunk(a);
+    if (st != KVC_OK)
+        return st;
+    if (a->T == 0)
+        return KVC_OK;
+    if (!a->q || !a->o || !a->cu_new || !aligned16(a->q) || !aligned16(a->o) ||
+        !strides_ok(a->q_stride, 2) || !strides_ok(a->o_stride, 2))
+        return KVC_ERR_INVALID_ARG;
+    const kvc_slot_cache &c = *a->cache;
+    TokensLaunch p{};
+    p.B = c.B;
+    p.Hq = a->Hq;
+    p.Hkv = c.Hkv;
+    p.D = c.D;
+    p.L = a->T;
+    p.q = a->q;
+    p.k = c.K;
+    p.v = c.V;
+    p.o = a->o;
+    p.lse = a->lse;
+    for (int i = 0; i < 2; ++i) {
+        p.qs[i + 1] = a->q_stride[i];
+        p.os[i + 1] = a->o_stride[i];
+    }
+    p.ls[1] = a->T;
+    p.cu = a->cu_new;
+    p.n = c.n;
+    p.C = c.C;
+    p.block_table = c.block_table;
+    p.num_pages = c.num_pages;
+    p.scale_log2 = (a->softmax_scale > 0.f ? a->softmax_scale : 1.0f / sqrtf((float)c.D)) * LOG2E;
+    p.status = dev_status_ptr();
+    return from_cuda(launch_attend_tokens(p, stream));
+}
+
+kvc_status kvc_append_plan(const kvc_slot_cache *cache, const kvc_page_pool *pool,
+                           const int32_t *cu_new, int T, int release, const kvc_slot_cache *next,
+                           const kvc_page_pool *next_pool, int32_t *slot_map, cudaStream_t stream)
+{
+    kvc_status st = check_slot_cache(cache);
+    if (st == KVC_OK)
+        st = check_slot_cache(next);
+    if (st != KVC_OK)
+        return st;
+    if (!cu_new || T < 0 || (T > 0 && !slot_map))
+        return KVC_ERR_INVALID_ARG;
+    if (next->B != cache->B || next->Hkv != cache->Hkv || next->C != cache->C ||
+        !next->block_table != !cache->block_table || next->num_pages != cache->num_pages)
+        return KVC_ERR_INVALID_ARG;
+    if (cache->block_table &&
+        (!pool || !next_pool || !pool->pages || !pool->free_list || !pool->count ||
+         !next_pool->pages || !next_pool->free_list || !next_pool->count))
+        return KVC_ERR_INVALID_ARG;
+    if ((long long)cache->B * cache->Hkv > KVC_PLAN_MAX_UNITS ||
+        (long long)T * cache->Hkv > (long long)INT_MAX)
+        return KVC_ERR_UNSUPPORTED;
+    PlanLaunch p{};
+    p.B = cache->B;
+    p.Hkv = cache->Hkv;
+    p.C = cache->C;
+    p.T = T;
+    p.num_pages = cache->num_pages;
+    p.cu = cu_new;
+    p.n = cache->n;
+    p.seqlen = cache->seqlen;
+    p.n_out = next->n;
+    p.seqlen_out = next->seqlen;
+    p.pos = next->pos;
+    p.slot_map = slot_map;
+    if (cache->block_table) {
+        p.table = cache->block_table;
+        p.table_out = const_cast<int32_t *>(next->block_table);
+        p.pages = pool->pages;
+        p.free_list = pool->free_list;
+        p.count = pool->count;
+        p.pages_out = next_pool->pages;
+        p.free_out = next_pool->free_list;
+        p.count_out = next_pool->count;
+    }
+    p.release = release != 0;
+    p.status = dev_status_ptr();
+    return from_cuda(launch_append_plan(p, stream));
+}
+
+kvc_status kvc_append_packed(const kvc_slot_cache *cache, const uint16_t *k_new,
+                             const int64_t k_stride[2], const uint16_t *v_new,
+                             const int64_t v_stride[2], int T, const int32_t *slot_map,
+                             cudaStream_t stream)
+{
+    const kvc_status st = check_slot_cache(cache);
+    if (st != KVC_OK)
+        return st;
+    if (T < 0)
+        return KVC_ERR_INVALID_ARG;
+    if (T == 0)
+        return KVC_OK;
+    if (!k_new || !v_new || !slot_map || !k_stride || !v_stride || !aligned16(k_new) ||
+        !aligned16(v_new) || !strides_ok(k_stride, 2) || !strides_ok(v_stride, 2))
+        return KVC_ERR_INVALID_ARG;
+    if ((long long)T * cache->Hkv > (long long)INT_MAX)
+        return KVC_ERR_UNSUPPORTED;
+    PackedLaunch p{};
+    p.T = T;
+    p.Hkv = cache->Hkv;
+    p.D = cache->D;
+    p.rows = cache->block_table ? (long)cache->num_pages * KVC_PAGE_SLOTS
+                                : (long)cache->B * cache->Hkv * cache->C;
+    p.k_new = k_new;
+    p.v_new = v_new;
+    for (int i = 0; i < 2; ++i) {
+        p.ks[i] = k_stride[i];
+        p.vs[i] = v_stride[i];
+    }
+    p.K = cache->K;
+    p.V = cache->V;
+    p.slot_map = slot_map;
+    p.status = dev_status_ptr();
+    return from_cuda(launch_append_packed(p, stream));
 }
 
 const char *kvc_status_string(kvc_status s)

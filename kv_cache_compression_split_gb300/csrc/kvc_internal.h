@@ -104,6 +104,50 @@ cudaError_t launch_combine(int B, int Hq, int Hkv, int D, int splits, int unit0,
                            const float *part_o, const float *part_ml, uint16_t *o, float *lse,
                            cudaStream_t s);
 
+// Attention of many query tokens per sequence.  Keys are the sequence's own tokens
+// (n == nullptr: a causal prompt) or a unit's n slots, whose last ones hold the
+// sequence's query tokens (a chunk over the slot cache).
+struct TokensLaunch {
+    int B, Hq, Hkv, D;
+    int L;                     // packed: tokens of all sequences; padded: tokens per sequence
+    const uint16_t *q, *k, *v;
+    uint16_t *o;
+    float *lse;                // may be nullptr
+    long qs[3], ks[3], vs[3], os[3];   // element strides: sequence, head, token
+    long ls[2];                // lse: sequence, head (tokens adjacent)
+    const int32_t *cu;         // packed: first token of each sequence, [B + 1]
+    const int32_t *lens;       // padded: tokens of each sequence (nullptr: L)
+    const int32_t *n;          // chunk: slots of each unit
+    int C;                     // chunk: slots per unit
+    const int32_t *block_table; // chunk: paged layout (nullptr: dense)
+    int num_pages;
+    float scale_log2;
+    int *status;
+};
+cudaError_t launch_attend_tokens(const TokensLaunch &p, cudaStream_t s);
+
+// Page tables, slot map, positions and lengths of a ragged batch of new tokens.
+struct PlanLaunch {
+    int B, Hkv, C, T, num_pages;
+    const int32_t *cu, *n, *seqlen, *table, *pages, *free_list, *count;
+    int32_t *n_out, *seqlen_out, *table_out, *pages_out, *free_out, *count_out, *pos, *slot_map;
+    int release;
+    int *status;
+};
+cudaError_t launch_append_plan(const PlanLaunch &p, cudaStream_t s);
+
+// New rows to the slots of a slot map (rows of the cache's K / V arrays, -1: skipped).
+struct PackedLaunch {
+    int T, Hkv, D;
+    long rows;                 // rows of the K / V arrays
+    const uint16_t *k_new, *v_new;
+    long ks[2], vs[2];         // element strides: token, head
+    uint16_t *K, *V;
+    const int32_t *slot_map;
+    int *status;
+};
+cudaError_t launch_append_packed(const PackedLaunch &p, cudaStream_t s);
+
 cudaError_t launch_append_slots(const kvc_slot_cache &c, const uint16_t *k_new,
                                 const uint16_t *v_new, int n_new, cudaStream_t s);
 cudaError_t launch_append_quant(const kvc_quant_cache &c, const uint16_t *k_new,
