@@ -141,6 +141,25 @@ bool encode_tmap_2d_f16(CUtensorMap *map, const void *base, uint64_t inner, uint
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tmap_4d_f16(CUtensorMap *map, const void *base, const uint64_t dims[4],
+                        const uint64_t strides[3], const uint32_t box[4])
+{
+    auto fn = encode_fn();
+    if (!fn || !aligned16(base))
+        return false;
+    cuuint64_t d[4], st[3];
+    cuuint32_t bx[4], estr[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 4; ++i) {
+        d[i] = dims[i];
+        bx[i] = box[i];
+    }
+    for (int i = 0; i < 3; ++i)
+        st[i] = strides[i];
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(base), d, st, bx, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 SlotAttendPlan plan_attend(int units, int tiles_per_unit, int requested, int max_splits)
 {
     SlotAttendPlan pl{1, tiles_per_unit > 0 ? tiles_per_unit : 1};
@@ -703,6 +722,7 @@ kvc_status kvc_prompt_attend(const kvc_prompt_args *a, cudaStream_t stream)
     }
     p.ls[0] = (long)a->Hq * a->L;
     p.ls[1] = a->L;
+    p.splits = 1;
     p.cu = a->cu_seqlens;
     p.lens = a->lens;
     p.scale_log2 = (a->softmax_scale > 0.f ? a->softmax_scale : 1.0f / sqrtf((float)a->D)) *
@@ -727,10 +747,18 @@ static kvc_status check_chunk(const kvc_chunk_args *a)
     return KVC_OK;
 }
 
+static int chunk_splits(const kvc_chunk_args *a)
+{
+    const kvc_slot_cache &c = *a->cache;
+    return plan_tokens_splits(a->T, c.B, a->Hq, c.Hkv, c.C, a->num_splits);
+}
+
 size_t kvc_chunk_workspace_size(const kvc_chunk_args *a)
 {
-    (void)a;
-    return 0;
+    if (check_chunk(a) != KVC_OK)
+        return 0;
+    const int s = chunk_splits(a);
+    return s > 1 ? (size_t)a->T * a->Hq * s * (a->cache->D + 2) * sizeof(float) : 0;
 }
 
 kvc_status kvc_chunk_attend(const kvc_chunk_args *a, cudaStream_t stream)
@@ -745,6 +773,14 @@ kvc_status kvc_chunk_attend(const kvc_chunk_args *a, cudaStream_t stream)
         return KVC_ERR_INVALID_ARG;
     const kvc_slot_cache &c = *a->cache;
     TokensLaunch p{};
+    p.splits = chunk_splits(a);
+    if (p.splits > 1) {
+        if (!a->workspace || a->workspace_bytes < kvc_chunk_workspace_size(a) ||
+            !aligned16(a->workspace))
+            return KVC_ERR_WORKSPACE;
+        p.part_o = static_cast<float *>(a->workspace);
+        p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)a->T * a->Hq * p.splits * c.D);
+    }
     p.B = c.B;
     p.Hq = a->Hq;
     p.Hkv = c.Hkv;

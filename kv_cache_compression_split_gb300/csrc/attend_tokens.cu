@@ -1,6 +1,6 @@
 // attend_tokens.cu -- attention of many query tokens per sequence: whole prompts
 // (kvc_prompt_attend) and chunks of new tokens over the slot cache
-// (kvc_chunk_attend).
+// (kvc_chunk_attend), on the 5th-generation tensor cores.
 //
 // For query token i of a sequence and query head h of KV head hk
 //   s_j = scale q_i . k_j over the keys j < e_i,   m = max s, l = sum exp(s - m),
@@ -9,10 +9,29 @@
 // which the last m_b hold the chunk.  A row that sees nothing gives o = 0 and
 // lse = -inf.
 //
-// A tile's rows are (token, head of the group) pairs, token-major, so the query
-// heads of one KV head share every key they read.  One CTA of four warps takes
-// 64 rows; keys stream through shared memory 64 at a time, and each warp keeps
-// the running maximum, sum and weighted values of its 16 rows in registers.
+// Rows.  A tile is 128 rows of tcgen05.mma's M: (token, head of the group) pairs,
+// token-major, so the query heads of one KV head share every key they read.  A work
+// item is two tiles of one (sequence, KV head): two consecutive token ranges, or,
+// when its tokens fit one tile, the same rows twice with the 128-key blocks dealt out
+// alternately.  Either way two independent softmax chains run per SM, and the tensor
+// cores work on one while the other's scores become probabilities.
+//
+// Pipeline, one CTA per SM, persistent over the items: a producer warp (TMA: query
+// tiles, and K and V blocks through a ring), an MMA warp, and a warpgroup per tile in
+// which a thread owns a row.  S = Q K^T (128 x 128, fp32) lands in TMEM; the row's
+// thread reads it, keeps the running reference m and sum l in registers, and writes
+// the probabilities back over S as binary16, from where they are the A operand of
+// O += P V with O in TMEM.  The MMA warp issues O_t(j) and S_t(j + 1) of one tile
+// back to back, so when S_t(j + 1) is complete O_t is at rest and its rows may be
+// rescaled by their threads.  They rarely are: the reference follows the maximum only
+// when that has grown by 2^8 (probabilities then stay below 2^8, far inside binary16
+// and with the same relative rounding, 2^-11, as below 1).
+//
+// Non-finite values.  A masked score is replaced, not added to, so keys behind a
+// row's range never matter.  A masked value row would enter as 0 * v: rows behind the
+// sequence's last key are cleared in shared memory, and a row whose result is not
+// finite although its sum is computes its channels again from memory over the keys it
+// sees alone.
 #include "kvc_device.cuh"
 #include "kvc_internal.h"
 
@@ -22,9 +41,41 @@ namespace kvc {
 
 namespace {
 
-constexpr int ROWS = 64;
-constexpr int KEYS = 64;
+constexpr int TM = 128;                   // rows of a tile
+constexpr int TK = 128;                   // keys of a block
+constexpr int HALF = TK / 2;              // keys of one TMA box (a page of the cache)
+constexpr int NTHR = 320;                 // two warpgroups, producer warp, MMA warp
+constexpr int W_TMA = 8, W_MMA = 9;
+constexpr int NI = 2;                     // slots of the item feed
+constexpr int TMEM_COLS = 512;
 constexpr float LN2 = 0.6931471805599453f;
+constexpr float GROWTH = 8.f;             // log2 growth of the maximum that moves the reference
+
+template <int D> struct TokCfg {
+    static constexpr int NBOX = D / 64;
+    static constexpr int BOX_BYTES = TM * 128;
+    static constexpr int TILE_BYTES = NBOX * BOX_BYTES;
+    static constexpr int NS = D == 128 ? 5 : 10;           // ring stages (one K or V block each)
+    static constexpr int ML_BYTES = TM * 8;
+    static constexpr int SMEM = (2 + NS) * TILE_BYTES + ML_BYTES + 1024 + 1024;
+    static constexpr uint32_t IDESC_QK = idesc_f16_f32(TM, TK);
+    static constexpr uint32_t IDESC_PV = idesc_f16_f32_bmn(TM, D);
+    static constexpr uint32_t COL_O = 2 * TK;              // TMEM: S_0, S_1, O_0, O_1
+};
+
+struct TokItem {
+    int b, hk;
+    int tok0, ntok;      // tokens of the sequence
+    int start;           // the sequence's first token in the tensors
+    int shift;           // token i sees the keys j <= i + shift
+    int j0, j1;          // key blocks
+    int split;
+    int two;             // one tile of rows, its blocks dealt to both warpgroups
+};
+
+struct TokMaps {
+    CUtensorMap q, k, v;
+};
 
 // First token and length of sequence b; a range that leaves [0, L] counts as an
 // empty sequence and is reported.
@@ -38,220 +89,826 @@ __device__ __forceinline__ void seq_range(const TokensLaunch &p, int b, int &sta
     }
 }
 
-// Sequence and tile of tile number idx, counted over the sequences in order
-// (tiles of `tokens` tokens).  Every lane of the warp calls it; b = -1 when idx
-// lies behind the last tile.
-__device__ __forceinline__ void find_tile(const TokensLaunch &p, int tokens, int idx, int &b,
-                                          int &tile, int &start, int &len)
-{
-    const int lane = threadIdx.x & 31;
+// Walks the items in order: sequences, KV heads, token ranges from the last (longest)
+// to the first, splits.  Every lane of the warp calls it; idx only grows.
+struct ItemWalk {
+    int b0 = 0;
     long base = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        int s = 0, n = 0;
-        if (b0 + lane < p.B)
-            seq_range(p, b0 + lane, s, n);
-        const int t = (n + tokens - 1) / tokens;
-        int sum = t;
+    __device__ bool find(const TokensLaunch &p, int tpt, long idx, TokItem &it)
+    {
+        const int lane = threadIdx.x & 31;
+        for (; b0 < p.B; b0 += 32) {
+            int s = 0, n = 0;
+            if (b0 + lane < p.B)
+                seq_range(p, b0 + lane, s, n);
+            const int ranges = (n + 2 * tpt - 1) / (2 * tpt);
+            const long mine = (long)ranges * p.Hkv * p.splits;
+            long sum = mine;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, sum, off);
-            if (lane >= off)
-                sum += y;
-        }
-        const unsigned here = __ballot_sync(0xffffffffu, base + sum > idx);
-        if (here) {
+            for (int off = 1; off < 32; off <<= 1) {
+                const long y = __shfl_up_sync(0xffffffffu, sum, off);
+                if (lane >= off)
+                    sum += y;
+            }
+            const unsigned here = __ballot_sync(0xffffffffu, base + sum > idx);
+            if (!here) {
+                base += __shfl_sync(0xffffffffu, sum, 31);
+                continue;
+            }
             const int src = __ffs(here) - 1;
-            b = b0 + src;
-            tile = (int)(idx - base) - __shfl_sync(0xffffffffu, sum - t, src);
-            start = __shfl_sync(0xffffffffu, s, src);
-            len = __shfl_sync(0xffffffffu, n, src);
-            return;
+            const int r = (int)(idx - base - __shfl_sync(0xffffffffu, sum - mine, src));
+            const int per = __shfl_sync(0xffffffffu, ranges, src);
+            const int len = __shfl_sync(0xffffffffu, n, src);
+            it.start = __shfl_sync(0xffffffffu, s, src);
+            it.b = b0 + src;
+            it.hk = r / (per * p.splits);
+            const int rem = r - it.hk * per * p.splits;
+            it.split = rem % p.splits;
+            it.tok0 = (per - 1 - rem / p.splits) * 2 * tpt;
+            it.ntok = min(2 * tpt, len - it.tok0);
+            it.two = it.ntok <= tpt;
+            int n_keys = len;
+            if (p.n) {
+                n_keys = p.n[it.b * p.Hkv + it.hk];
+                if (n_keys < 0 || n_keys > p.C) {
+                    flag_error(p.status, DEV_CAPACITY);
+                    n_keys = 0;
+                }
+            }
+            it.shift = n_keys - len;
+            const int end = max(0, it.shift + it.tok0 + it.ntok);
+            const int blocks = (end + TK - 1) / TK;
+            const int chunk = (blocks + p.splits - 1) / p.splits;
+            it.j0 = min(blocks, it.split * chunk);
+            it.j1 = min(blocks, it.j0 + chunk);
+            return true;
         }
-        base += __shfl_sync(0xffffffffu, sum, 31);
+        return false;
     }
-    b = -1;
+};
+
+// Keys before `end` that tile t of the item sees, and its share of the blocks.
+struct TileRange {
+    int tok, ntok;       // tokens of the tile
+    int end;             // keys its last token sees
+    int j, step, count;  // blocks j, j + step, ...
+    __device__ TileRange(const TokItem &it, int t, int tpt)
+    {
+        tok = it.tok0 + (it.two ? 0 : t * tpt);
+        ntok = it.two ? it.ntok : t ? it.ntok - tpt : min(tpt, it.ntok);
+        end = max(0, it.shift + tok + ntok);
+        const int j1 = min(it.j1, (end + TK - 1) / TK);
+        step = it.two ? 2 : 1;
+        j = it.j0 + (it.two ? t : 0);
+        count = max(0, (j1 - j + step - 1) / step);
+    }
+};
+
+__device__ __forceinline__ const uint16_t *key_row(const TokensLaunch &p, const uint16_t *base,
+                                                   const long *st, const TokItem &it, int j)
+{
+    if (!p.n)
+        return base + (p.cu ? 0 : it.b) * st[0] + it.hk * st[1] + (long)(it.start + j) * st[2];
+    const long row = SlotRows{p.block_table, p.C, p.num_pages}.row(it.b * p.Hkv + it.hk, j);
+    return row < 0 ? nullptr : base + row * p.D;
+}
+
+// The 32 channels from c0 of one row, from memory, over the keys [first, last]: for a
+// row whose tensor-core result is not finite although its sum l is.
+__device__ __noinline__ void row_again(const TokensLaunch &p, const TokItem &it, const uint16_t *q,
+                                       int first, int last, float ref, int c0, float scale,
+                                       uint16_t *o, float *part)
+{
+    float acc[32];
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+        acc[c] = 0.f;
+    for (int j = first; j <= last; ++j) {
+        const uint16_t *k = key_row(p, p.k, p.ks, it, j), *v = key_row(p, p.v, p.vs, it, j);
+        if (!k)
+            continue;
+        float s = 0.f;
+        for (int d = 0; d < p.D; ++d)
+            s = fmaf(__half2float(__ushort_as_half(q[d])), __half2float(__ushort_as_half(k[d])), s);
+        const float w = ex2(s * p.scale_log2 - ref);
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            acc[c] = fmaf(w, __half2float(__ushort_as_half(v[c0 + c])), acc[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+        if (part)
+            part[c0 + c] = acc[c];
+        else
+            o[c0 + c] = __half_as_ushort(__float2half_rn(acc[c] * scale));
+    }
 }
 
 template <int D>
-__global__ void __launch_bounds__(128) k_attend_tokens(const TokensLaunch p)
+__global__ void __launch_bounds__(NTHR, 1)
+    k_attend_tokens(const __grid_constant__ TokMaps maps, const __grid_constant__ TokensLaunch p)
 {
-    constexpr int LD = D + 8;   // padded row of a key tile: conflict-free ldmatrix
-    constexpr int NK = D / 16;
-    __shared__ __align__(16) uint16_t sk[KEYS * LD];
-    __shared__ __align__(16) uint16_t sv[KEYS * LD];
+    using Cfg = TokCfg<D>;
+    constexpr int NS = Cfg::NS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_align1024(smem_raw);
+    uint8_t *sq = smem;                                      // two query tiles
+    uint8_t *ring = smem + 2 * Cfg::TILE_BYTES;              // NS blocks of K or V
+    float2 *s_ml = reinterpret_cast<float2 *>(ring + NS * Cfg::TILE_BYTES);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + NS * Cfg::TILE_BYTES + Cfg::ML_BYTES);
+    uint64_t *kv_full = bars, *kv_empty = kv_full + NS;
+    uint64_t *q_full = kv_empty + NS, *q_empty = q_full + 1;
+    uint64_t *s_full = q_empty + 1, *p_full = s_full + 2, *o_full = p_full + 2;
+    uint64_t *it_full = o_full + 2, *it_empty = it_full + NI;
+    uint64_t *mrg_full = it_empty + NI, *mrg_empty = mrg_full + 4;
+    uint64_t *mrg_done = mrg_empty + 4, *mma_done = mrg_done + 1;
+    TokItem *s_item = reinterpret_cast<TokItem *>(mma_done + 1);
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(s_item + NI);
+    volatile int *abort = reinterpret_cast<int *>(s_tmem + 1);
+
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = p.Hq / p.Hkv, tokens = ROWS / g;
-    const int hk = blockIdx.y;
-    const SlotRows rows{p.block_table, p.C, p.num_pages};
-    int b, tile, start, len;
-    find_tile(p, tokens, blockIdx.x, b, tile, start, len);
-    if (b < 0)
-        return;
-    const int tok0 = tile * tokens, n_tok = min(tokens, len - tok0);
-    const int unit = b * p.Hkv + hk;
-    int n_keys = len;   // keys the sequence's last token sees
-    if (p.n) {
-        n_keys = p.n[unit];
-        if (n_keys < 0 || n_keys > p.C) {
-            if (threadIdx.x == 0)
-                flag_error(p.status, DEV_CAPACITY);
-            n_keys = 0;
-        }
-    }
-    const int shift = n_keys - len;               // token i sees keys j <= i + shift
-    const int end = min(n_keys, shift + tok0 + n_tok);
+    const int g = p.Hq / p.Hkv, tpt = TM / g;
 
-    // this thread's two rows of the warp's 16
-    int tok[2], head[2], last[2];
-    bool real[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int r = 16 * warp + (lane >> 2) + 8 * u;
-        tok[u] = tok0 + r / g;
-        head[u] = hk * g + r % g;
-        real[u] = r < n_tok * g;
-        last[u] = real[u] ? tok[u] + shift : -1;
-    }
-    const long qb = p.cu ? 0 : b;
-    uint32_t qf[NK][4];
-#pragma unroll
-    for (int kk = 0; kk < NK; ++kk)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const uint16_t *row = p.q + qb * p.qs[0] + head[u] * p.qs[1] +
-                                  (long)(start + tok[u]) * p.qs[2] + 16 * kk + 2 * (lane & 3);
-            qf[kk][u] = real[u] ? *reinterpret_cast<const uint32_t *>(row) : 0u;
-            qf[kk][u + 2] = real[u] ? *reinterpret_cast<const uint32_t *>(row + 8) : 0u;
+    if (threadIdx.x == 0) {
+        *abort = 0;
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_empty[i], 1);
         }
-    float acc[D / 8][4];
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-        acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_full[t], 4);
+            mbar_init(&o_full[t], 1);
+        }
+        for (int i = 0; i < NI; ++i) {
+            mbar_init(&it_full[i], 1);
+            mbar_init(&it_empty[i], 9);   // the MMA warp and eight softmax warps
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&mrg_full[i], 1);
+            mbar_init(&mrg_empty[i], 1);
+        }
+        mbar_init(mrg_done, 4);
+        mbar_init(mma_done, 1);
+        fence_mbar_init();
+    }
+    if (warp == W_MMA) {
+        tmem_alloc(s_tmem, TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
 
-    for (int k0 = 0; k0 < end; k0 += KEYS) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < KEYS * (D / 8); i += blockDim.x) {
-            const int j = i / (D / 8), ch = i % (D / 8);
-            uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
-            if (k0 + j < end) {
-                const uint16_t *ks, *vs;
-                bool ok = true;
-                if (p.n) {
-                    const long row = rows.row(unit, k0 + j);
-                    ok = row >= 0;
-                    ks = p.k + row * D;
-                    vs = p.v + row * D;
-                } else {
-                    ks = p.k + qb * p.ks[0] + hk * p.ks[1] + (long)(start + k0 + j) * p.ks[2];
-                    vs = p.v + qb * p.vs[0] + hk * p.vs[1] + (long)(start + k0 + j) * p.vs[2];
-                }
+    // The k-th item of the feed; false at the end (or after a wait that ran out).
+    auto feed_get = [&](int k, TokItem &it) -> bool {
+        const int slot = k % NI;
+        const bool got = mbar_sleep_or_abort(&it_full[slot], (k / NI) & 1, abort);
+        if (!__all_sync(0xffffffffu, got))
+            return false;
+        it = s_item[slot];
+        __syncwarp();
+        mbar_arrive_warp(&it_empty[slot]);
+        return it.b >= 0;
+    };
+
+    if (warp == W_TMA) {
+        // ------------------------------------------------ producer
+        if (lane == 0) {
+            prefetch_tmap(&maps.q);
+            prefetch_tmap(&maps.k);
+            prefetch_tmap(&maps.v);
+        }
+        ItemWalk walk;
+        int n_it = 0, n_q = 0, n_two = 0, seen_two = 0;   // ring slots, query loads, merges
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            TokItem it;
+            const bool more = walk.find(p, tpt, blockIdx.x + (long)k * gridDim.x, it);
+            if (!more)
+                it.b = -1;
+            const int slot = k % NI;
+            if (lane == 0) {
+                if (k >= NI)
+                    ok = mbar_sleep_or_abort(&it_empty[slot], ((k / NI) & 1) ^ 1, abort);
                 if (ok) {
-                    kx = *reinterpret_cast<const uint4 *>(ks + 8 * ch);
-                    vx = *reinterpret_cast<const uint4 *>(vs + 8 * ch);
-                } else if (ch == 0) {
-                    flag_error(p.status, DEV_CAPACITY);
+                    s_item[slot] = it;
+                    mbar_arrive(&it_full[slot]);
                 }
             }
-            *reinterpret_cast<uint4 *>(&sk[j * LD + 8 * ch]) = kx;
-            *reinterpret_cast<uint4 *>(&sv[j * LD + 8 * ch]) = vx;
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok || !more)
+                break;
+            const int n = it.j1 - it.j0;
+            if (it.two)
+                ++n_two;
+            if (n <= 0)
+                continue;
+            const int unit = it.b * p.Hkv + it.hk;
+            const int per = p.C / PAGE_SLOTS;
+            if (p.block_table)   // the item's part of the page table into L1
+                for (int i = 2 * it.j0 + 32 * lane; i < min(per, 2 * it.j1); i += 1024)
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(p.block_table +
+                                                                  (size_t)unit * per + i));
+            if (lane == 0) {
+                if (n_q > 0)
+                    ok = mbar_sleep_or_abort(q_empty, (n_q - 1) & 1, abort);
+                // a merge of the item before used the second query tile
+                const int done = n_two - (it.two ? 1 : 0);
+                for (; ok && seen_two < done; ++seen_two)
+                    ok = mbar_sleep_or_abort(mrg_done, seen_two & 1, abort);
+                if (ok) {
+                    const int tiles = it.two ? 1 : 2;
+                    mbar_arrive_expect_tx(q_full, tiles * Cfg::NBOX * tpt * g * 128);
+                    for (int t = 0; t < tiles; ++t)
+                        for (int c = 0; c < Cfg::NBOX; ++c)
+                            tma_load_4d(sq + t * Cfg::TILE_BYTES + c * Cfg::BOX_BYTES, &maps.q,
+                                        q_full, 64 * c, it.hk * g, it.start + it.tok0 + t * tpt,
+                                        p.cu ? 0 : it.b);
+                    ++n_q;
+                }
+                const int n_keys = p.n ? it.shift + (p.cu ? p.cu[it.b + 1] - p.cu[it.b] : 0) : 0;
+                auto load = [&](const CUtensorMap *map, int j) {
+                    const int st = n_it % NS;
+                    if (n_it >= NS)
+                        ok = ok && mbar_sleep_or_abort(&kv_empty[st], ((n_it / NS) & 1) ^ 1, abort);
+                    if (!ok)
+                        return;
+                    mbar_arrive_expect_tx(&kv_full[st], Cfg::TILE_BYTES);
+                    uint8_t *dst = ring + st * Cfg::TILE_BYTES;
+                    for (int h = 0; h < 2; ++h) {
+                        const int j_key = j * TK + h * HALF;
+                        if (p.n) {
+                            // a half without a key, or without a page, reads as zeros: its
+                            // row lies behind the last one
+                            int row = p.kv_rows;
+                            if (j_key < n_keys) {
+                                if (!p.block_table) {
+                                    row = unit * p.C + j_key;
+                                } else {
+                                    const int pg =
+                                        __ldg(p.block_table + (size_t)unit * per + j_key / PAGE_SLOTS);
+                                    if (pg >= 0 && pg < p.num_pages)
+                                        row = pg * PAGE_SLOTS;
+                                    else
+                                        flag_error(p.status, DEV_CAPACITY);
+                                }
+                            }
+                            for (int c = 0; c < Cfg::NBOX; ++c)
+                                tma_load_2d(dst + c * Cfg::BOX_BYTES + h * (HALF * 128), map,
+                                            &kv_full[st], 64 * c, row);
+                        } else {
+                            for (int c = 0; c < Cfg::NBOX; ++c)
+                                tma_load_4d(dst + c * Cfg::BOX_BYTES + h * (HALF * 128), map,
+                                            &kv_full[st], 64 * c, it.hk, it.start + j_key,
+                                            p.cu ? 0 : it.b);
+                        }
+                    }
+                    ++n_it;
+                };
+                // the order in which the MMA warp takes them
+                const int ahead = it.two ? 2 : 1;
+                for (int i = 0; ok && i < ahead && i < n; ++i)
+                    load(&maps.k, it.j0 + i);
+                for (int i = 0; ok && i < n; ++i) {
+                    load(&maps.v, it.j0 + i);
+                    if (ok && i + ahead < n)
+                        load(&maps.k, it.j0 + i + ahead);
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
         }
-        __syncthreads();
-        float s[KEYS / 8][4];
+        // every copy has landed before the CTA leaves
+        if (lane == 0) {
+            for (int i = n_it > NS ? n_it - NS : 0; i < n_it; ++i)
+                mbar_wait(&kv_full[i % NS], (i / NS) & 1);
+            if (n_q > 0)
+                mbar_wait(q_full, (n_q - 1) & 1);
+        }
+    } else if (warp == W_MMA) {
+        // ------------------------------------------------ MMA issuer (lane 0 issues)
+        int n_it = 0, n_q = 0;
+        int n_p[2] = {0, 0};
+        bool ok = true;
+        TokItem it;
+        const uint32_t qb = smem_u32(sq);
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, abort));
+        };
+        auto stage = [&](int i) { return smem_u32(ring + (i % NS) * Cfg::TILE_BYTES); };
+        auto qk = [&](int t, int tile, uint32_t kb) {
+            if (lane == 0) {
 #pragma unroll
-        for (int nb = 0; nb < KEYS / 8; ++nb) {
-            s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < NK; kk += 2) {
-                uint32_t b0, b1, b2, b3;
-                ldsm_x4(smem_u32(&sk[(8 * nb + (lane & 7)) * LD + 16 * kk + 8 * (lane >> 3)]), b0,
-                        b1, b2, b3);
-                mma16816(s[nb], qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3], b0, b1);
-                mma16816(s[nb], qf[kk + 1][0], qf[kk + 1][1], qf[kk + 1][2], qf[kk + 1][3], b2, b3);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * Cfg::BOX_BYTES + (kk & 3) * 32;
+                    umma_f16(tmem + TK * t, sdesc_k_sw128(qb + tile * Cfg::TILE_BYTES + off),
+                             sdesc_k_sw128(kb + off), Cfg::IDESC_QK, kk > 0 ? 1u : 0u);
+                }
+                umma_commit(&s_full[t]);
+            }
+        };
+        auto pv = [&](int t, uint32_t vb, int keys, bool first) {
+            if (lane == 0) {
+                const int steps = min(TK, keys + 15) / 16;
+                for (int kk = 0; kk < steps; ++kk)
+                    umma_f16_ts(tmem + Cfg::COL_O + D * t, tmem + TK * t + 8 * kk,
+                                sdesc_mn_sw128(vb + 2048 * kk, Cfg::BOX_BYTES), Cfg::IDESC_PV,
+                                first && kk == 0 ? 0u : 1u);
+            }
+        };
+        auto commit = [&](uint64_t *bar) {
+            if (lane == 0)
+                umma_commit(bar);
+        };
+        for (int k = 0; ok && feed_get(k, it); ++k) {
+            const int n = it.j1 - it.j0;
+            if (n <= 0)
+                continue;
+            const TileRange r0(it, 0, tpt), r1(it, 1, tpt);
+            const int ahead = it.two ? 2 : 1;
+            wait(q_full, n_q & 1);
+            ++n_q;
+            // first scores of both tiles
+            for (int i = 0; ok && i < ahead && i < n; ++i, ++n_it) {
+                wait(&kv_full[n_it % NS], (n_it / NS) & 1);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint32_t kb = stage(n_it);
+                if (it.two) {
+                    qk(i, 0, kb);
+                } else {
+                    if (r0.count > 0)
+                        qk(0, 0, kb);
+                    qk(1, 1, kb);
+                }
+                commit(&kv_empty[n_it % NS]);
+            }
+            if (n <= ahead)
+                commit(q_empty);
+            for (int i = 0; ok && i < n; ++i) {
+                const int j = it.j0 + i;
+                const int vs = n_it++;
+                const int ks = i + ahead < n ? n_it++ : -1;
+                wait(&kv_full[vs % NS], (vs / NS) & 1);
+                if (!ok)
+                    break;
+                const uint32_t vb = stage(vs);
+                const int keys = min(TK, r1.end - j * TK);
+                if (keys & 15) {   // rows behind the last key of the item: cleared
+                    const int rows = 16 - (keys & 15);
+                    for (int x = lane; x < rows * Cfg::NBOX * 8; x += 32) {
+                        const int c = x / (rows * 8), y = x % (rows * 8);
+                        *reinterpret_cast<uint4 *>(ring + (vs % NS) * Cfg::TILE_BYTES +
+                                                   c * Cfg::BOX_BYTES + (keys + y / 8) * 128 +
+                                                   (y & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                if (it.two) {
+                    const int t = i & 1;
+                    wait(&p_full[t], n_p[t] & 1);
+                    if (!ok)
+                        break;
+                    ++n_p[t];
+                    tc_fence_after();
+                    pv(t, vb, keys, i < 2);
+                    commit(&kv_empty[vs % NS]);
+                    if (ks >= 0) {
+                        wait(&kv_full[ks % NS], (ks / NS) & 1);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        qk(t, 0, stage(ks));
+                        commit(&kv_empty[ks % NS]);
+                        if (i + ahead == n - 1)
+                            commit(q_empty);
+                    } else {
+                        commit(&o_full[t]);
+                    }
+                    continue;
+                }
+                if (i < r0.count) {
+                    wait(&p_full[0], n_p[0] & 1);
+                    if (!ok)
+                        break;
+                    ++n_p[0];
+                    tc_fence_after();
+                    pv(0, vb, min(TK, r0.end - j * TK), i == 0);
+                    if (i + 1 < r0.count) {
+                        wait(&kv_full[ks % NS], (ks / NS) & 1);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        qk(0, 0, stage(ks));
+                    } else {
+                        commit(&o_full[0]);
+                    }
+                }
+                wait(&p_full[1], n_p[1] & 1);
+                if (!ok)
+                    break;
+                ++n_p[1];
+                tc_fence_after();
+                pv(1, vb, keys, i == 0);
+                commit(&kv_empty[vs % NS]);
+                if (ks >= 0) {
+                    wait(&kv_full[ks % NS], (ks / NS) & 1);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    qk(1, 1, stage(ks));
+                    commit(&kv_empty[ks % NS]);
+                    if (i + 2 == n)
+                        commit(q_empty);
+                } else {
+                    commit(&o_full[1]);
+                }
             }
         }
-        float mx[2] = {m[0], m[1]};
-#pragma unroll
-        for (int nb = 0; nb < KEYS / 8; ++nb)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = k0 + 8 * nb + 2 * (lane & 3) + (e & 1), u = e >> 1;
-                s[nb][e] = j <= last[u] && j < end ? s[nb][e] * p.scale_log2 : -INFINITY;
-                mx[u] = fmaxf(mx[u], s[nb][e]);
-            }
-        float corr[2], ref[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
-            mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
-            ref[u] = mx[u] == -INFINITY ? 0.f : mx[u];
-            corr[u] = ex2(m[u] - ref[u]);
-            m[u] = mx[u];
-            l[u] *= corr[u];
+        // every product has finished before TMEM is released
+        if (lane == 0) {
+            umma_commit(mma_done);
+            mbar_wait(mma_done, 0);
         }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ softmax: a thread per row
+        const int t = warp >> 2, quarter = warp & 3;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+        const uint32_t s_col = lanes + TK * t, o_col = lanes + Cfg::COL_O + D * t;
+        const int r = 32 * quarter + lane;
+        const int r_tok = r / g, r_head = r - r_tok * g;
+        const float scale = p.scale_log2;
+        int n_s = 0, n_o = 0, n_m = 0;   // phases of s_full, o_full and the merge barriers
+        bool ok = true;
+        TokItem it;
+        for (int k = 0; ok && feed_get(k, it); ++k) {
+            const TileRange rg(it, t, tpt);
+            const bool real = r_tok < min(rg.ntok, tpt);
+            const int last = real ? it.shift + rg.tok + r_tok : -1;
+            const bool idle = (32 * quarter) / g >= rg.ntok;      // no row of the warp is real
+            const int first_last = it.shift + rg.tok + (32 * quarter) / g;
+            float m = -INFINITY, l = 0.f;
+            for (int i = 0; i < rg.count; ++i) {
+                const int k0 = (rg.j + i * rg.step) * TK;
+                const bool got = mbar_wait_or_abort(&s_full[t], n_s & 1, abort);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                ++n_s;
+                if (idle) {
+                    mbar_arrive_warp(&p_full[t]);
+                    continue;
+                }
+                tc_fence_after();
+                float x[TK];
+                tmem_ld64(s_col, reinterpret_cast<float(&)[64]>(x[0]));
+                tmem_ld64(s_col + 64, reinterpret_cast<float(&)[64]>(x[64]));
+                if (k0 + TK - 1 > first_last) {   // the block ends behind some row's range
+                    const int lim = last - k0;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
+                    for (int c = 0; c < TK; ++c)
+                        x[c] = c <= lim ? x[c] : -INFINITY;
+                }
+                float c0 = fmax3f(x[0], x[1], x[2]), c1 = fmax3f(x[32], x[33], x[34]);
+                float c2 = fmax3f(x[64], x[65], x[66]), c3 = fmax3f(x[96], x[97], x[98]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[i][e] *= corr[e >> 1];
-        uint32_t pf[KEYS / 8][2];
+                for (int c = 3; c < 31; c += 2) {
+                    c0 = fmax3f(c0, x[c], x[c + 1]);
+                    c1 = fmax3f(c1, x[32 + c], x[33 + c]);
+                    c2 = fmax3f(c2, x[64 + c], x[65 + c]);
+                    c3 = fmax3f(c3, x[96 + c], x[97 + c]);
+                }
+                const float mx = scale * fmaxf(fmax3f(c0, c1, x[31]),
+                                               fmax3f(c2, c3, fmax3f(x[63], x[95], x[127])));
+                const bool grow = mx > m + GROWTH;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float f = grow ? ex2(m - mx) : 1.f;   // 0 at the row's first key
+                    if (grow)
+                        m = mx;
+                    l *= f;
+                    if (i > 0) {
 #pragma unroll
-        for (int nb = 0; nb < KEYS / 8; ++nb) {
+                        for (int c = 0; c < D; c += 32) {
+                            float v[32];
+                            tmem_ld32(o_col + c, v);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[nb][e] = ex2(s[nb][e] - ref[e >> 1]);
-                l[e >> 1] += s[nb][e];
+                            for (int u = 0; u < 32; ++u)
+                                v[u] *= f;
+                            tmem_st32(o_col + c, v);
+                        }
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.f : m;
+                const float2 sc2 = make_float2(scale, scale), nr2 = make_float2(-ref, -ref);
+                float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+#pragma unroll
+                for (int c = 0; c < TK; c += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int u = 0; u < 16; u += 2) {
+                        const float2 y0 =
+                            ffma2(make_float2(x[c + 2 * u], x[c + 2 * u + 1]), sc2, nr2);
+                        const float2 y1 =
+                            ffma2(make_float2(x[c + 2 * u + 2], x[c + 2 * u + 3]), sc2, nr2);
+                        const float2 e0 = make_float2(ex2(y0.x), ex2(y0.y));
+                        const float2 e1 = make_float2(ex2(y1.x), ex2(y1.y));
+                        a0 = fadd2(a0, e0);
+                        a1 = fadd2(a1, e1);
+                        w[u] = pack_half2(e0.x, e0.y);
+                        w[u + 1] = pack_half2(e1.x, e1.y);
+                    }
+                    tmem_st16(s_col + c / 2, w);
+                }
+                const float2 a = fadd2(a0, a1);
+                l += a.x + a.y;
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                mbar_arrive_warp(&p_full[t]);
             }
-            pf[nb][0] = pack_half2(s[nb][0], s[nb][1]);
-            pf[nb][1] = pack_half2(s[nb][2], s[nb][3]);
+            if (!ok)
+                break;
+            if (rg.count > 0) {
+                const bool got = mbar_wait_or_abort(&o_full[t], n_o & 1, abort);
+                if (!__all_sync(0xffffffffu, got))
+                    break;
+                ++n_o;
+                tc_fence_after();
+            }
+            // ---- results
+            const int head = it.hk * g + r_head;
+            const long tok = it.start + rg.tok + r_tok;
+            const long qseq = p.cu ? 0 : it.b;
+            uint16_t *o_row = p.o + qseq * p.os[0] + head * p.os[1] + tok * p.os[2];
+            float *part = nullptr;
+            if (p.splits > 1)
+                part = p.part_o + ((tok * p.Hq + head) * p.splits + it.split) * D;
+            float fa = 1.f, fb = 0.f;        // weights of this tile's and the other's part
+            float *buf = reinterpret_cast<float *>(sq + Cfg::TILE_BYTES);
+            if (it.two) {
+                if (t == 1) {
+                    // second part: handed over D / 2 channels at a time, once the first
+                    // part's warp has read what was there
+#pragma unroll
+                    for (int h = 0; h < 2; ++h, ++n_m) {
+                        const bool got =
+                            n_m == 0 ||
+                            mbar_wait_or_abort(&mrg_empty[quarter], (n_m - 1) & 1, abort);
+                        if (!__all_sync(0xffffffffu, got)) {
+                            ok = false;
+                            break;
+                        }
+                        if (h == 0)
+                            s_ml[r] = make_float2(m, l);
+                        if (rg.count > 0 && !idle) {
+#pragma unroll
+                            for (int c = 0; c < D / 2; c += 32) {
+                                float v[32];
+                                tmem_ld32(o_col + h * (D / 2) + c, v);
+#pragma unroll
+                                for (int u = 0; u < 32; ++u)
+                                    buf[(c + u) * TM + r] = v[u];
+                            }
+                        }
+                        __syncwarp();
+                        mbar_arrive_warp(&mrg_full[quarter]);
+                    }
+                    if (!ok)
+                        break;
+                    tc_fence_before();
+                    continue;
+                }
+            }
+            unsigned bad = 0;
+            float inv = 1.f, lsum = l;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (it.two) {
+                    const bool got = mbar_wait_or_abort(&mrg_full[quarter], h, abort);
+                    if (!__all_sync(0xffffffffu, got)) {
+                        ok = false;
+                        break;
+                    }
+                    if (h == 0) {
+                        const float2 other = s_ml[r];
+                        const float mm = fmaxf(m, other.x);
+                        fa = m == -INFINITY ? 0.f : ex2(m - mm);
+                        fb = other.x == -INFINITY ? 0.f : ex2(other.x - mm);
+                        lsum = l * fa + other.y * fb;
+                        m = mm;
+                    }
+                }
+                if (h == 0)
+                    inv = part ? 1.f : lsum > 0.f ? 1.f / lsum : 0.f;
+                if (!idle) {
+#pragma unroll
+                    for (int c = 0; c < D / 2; c += 32) {
+                        float v[32];
+                        if (rg.count > 0) {
+                            tmem_ld32(o_col + h * (D / 2) + c, v);
+                        } else {
+#pragma unroll
+                            for (int u = 0; u < 32; ++u)
+                                v[u] = 0.f;
+                        }
+                        if (it.two) {
+#pragma unroll
+                            for (int u = 0; u < 32; ++u) {
+                                v[u] *= fa;
+                                if (fb > 0.f)
+                                    v[u] = fmaf(fb, buf[(c + u) * TM + r], v[u]);
+                            }
+                        }
+                        float probe = 0.f;
+#pragma unroll
+                        for (int u = 0; u < 32; ++u)
+                            probe = fmaf(v[u], 0.f, probe);
+                        const int c0 = h * (D / 2) + c;
+                        if (probe != 0.f)
+                            bad |= 1u << (c0 / 32);
+                        if (real) {
+                            if (lsum == 0.f) {
+#pragma unroll
+                                for (int u = 0; u < 32; ++u)
+                                    v[u] = 0.f;
+                            }
+                            if (part) {
+#pragma unroll
+                                for (int u = 0; u < 32; u += 4)
+                                    *reinterpret_cast<float4 *>(part + c0 + u) =
+                                        make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
+                            } else {
+#pragma unroll
+                                for (int u = 0; u < 32; u += 8)
+                                    *reinterpret_cast<uint4 *>(o_row + c0 + u) = make_uint4(
+                                        pack_half2(v[u] * inv, v[u + 1] * inv),
+                                        pack_half2(v[u + 2] * inv, v[u + 3] * inv),
+                                        pack_half2(v[u + 4] * inv, v[u + 5] * inv),
+                                        pack_half2(v[u + 6] * inv, v[u + 7] * inv));
+                            }
+                        }
+                    }
+                }
+                if (it.two) {
+                    fence_async_smem();   // the next query tile arrives by TMA
+                    __syncwarp();
+                    mbar_arrive_warp(&mrg_empty[quarter]);
+                    if (h == 1)
+                        mbar_arrive_warp(mrg_done);
+                }
+            }
+            if (!ok)
+                break;
+            if (real) {
+                if (bad && lsum > 0.f && lsum < INFINITY) {
+                    const uint16_t *q = p.q + qseq * p.qs[0] + head * p.qs[1] + tok * p.qs[2];
+                    for (int c0 = 0; c0 < D; c0 += 32)
+                        if (bad >> (c0 / 32) & 1)
+                            row_again(p, it, q, it.j0 * TK, min(last, it.j1 * TK - 1), m, c0, inv,
+                                      o_row, part);
+                }
+                if (part)
+                    p.part_ml[(tok * p.Hq + head) * p.splits + it.split] = make_float2(m, lsum);
+                else if (p.lse)
+                    p.lse[qseq * p.ls[0] + head * p.ls[1] + tok] =
+                        lsum > 0.f ? (m + log2f(lsum)) * LN2 : lsum == 0.f ? -INFINITY : lsum;
+            }
+            tc_fence_before();
         }
-#pragma unroll
-        for (int kb = 0; kb < KEYS / 16; ++kb)
-#pragma unroll
-            for (int nd = 0; nd < D / 16; ++nd) {
-                uint32_t b0, b1, b2, b3;
-                ldsm_x4_t(smem_u32(&sv[(16 * kb + (lane & 15)) * LD + 16 * nd + 8 * (lane >> 4)]),
-                          b0, b1, b2, b3);
-                mma16816(acc[2 * nd], pf[2 * kb][0], pf[2 * kb][1], pf[2 * kb + 1][0],
-                         pf[2 * kb + 1][1], b0, b1);
-                mma16816(acc[2 * nd + 1], pf[2 * kb][0], pf[2 * kb][1], pf[2 * kb + 1][0],
-                         pf[2 * kb + 1][1], b2, b3);
-            }
     }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
-        l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
-        if (!real[u])
-            continue;
-        const float inv = l[u] > 0.f ? 1.f / l[u] : 0.f;
-        uint16_t *row = p.o + qb * p.os[0] + head[u] * p.os[1] + (long)(start + tok[u]) * p.os[2];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<uint32_t *>(row + 8 * i + 2 * (lane & 3)) =
-                pack_half2(acc[i][2 * u] * inv, acc[i][2 * u + 1] * inv);
-        if (p.lse && (lane & 3) == 0)
-            p.lse[qb * p.ls[0] + head[u] * p.ls[1] + start + tok[u]] =
-                l[u] > 0.f ? (m[u] + log2f(l[u])) * LN2 : -INFINITY;
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == W_MMA) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
     }
+    if (threadIdx.x == 0 && *abort)
+        flag_error(p.status, DEV_TIMEOUT);
+}
+
+// Merges the splits of a row: a warp per row, D / 32 channels per lane.
+template <int D>
+__global__ void __launch_bounds__(256) k_combine_tokens(const TokensLaunch p)
+{
+    constexpr int V = D / 32;
+    const int lane = threadIdx.x & 31;
+    const long row = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= (long)p.L * p.Hq)
+        return;
+    const int tok = (int)(row / p.Hq), head = (int)(row % p.Hq);
+    int lo = 0, hi = p.B;   // the last sequence that starts at or before the token
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (p.cu[mid + 1] <= tok)
+            lo = mid + 1;
+        else
+            hi = mid;
+    }
+    if (lo >= p.B)
+        return;
+    int start, len;
+    seq_range(p, lo, start, len);
+    if (tok < start || tok >= start + len)
+        return;
+    const float2 *ml = p.part_ml + row * p.splits;
+    float ms = -INFINITY;
+    for (int s = 0; s < p.splits; ++s)
+        ms = fmaxf(ms, ml[s].x);
+    float l = 0.f, acc[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        acc[v] = 0.f;
+    for (int s = 0; s < p.splits; ++s) {
+        const float2 x = ml[s];
+        if (x.y == 0.f)
+            continue;   // the range held no key of the row
+        const float w = ex2(x.x - ms);
+        l = fmaf(w, x.y, l);
+        const float *src = p.part_o + (row * p.splits + s) * D + V * lane;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            acc[v] = fmaf(w, src[v], acc[v]);
+    }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    uint16_t *o = p.o + head * p.os[1] + (long)tok * p.os[2] + V * lane;
+#pragma unroll
+    for (int v = 0; v < V; v += 2)
+        *reinterpret_cast<uint32_t *>(o + v) = pack_half2(acc[v] * inv, acc[v + 1] * inv);
+    if (p.lse && lane == 0)
+        p.lse[head * p.ls[1] + tok] = l > 0.f ? (ms + log2f(l)) * LN2 : l == 0.f ? -INFINITY : l;
+}
+
+template <int D> cudaError_t attend_tokens_impl(TokensLaunch p, cudaStream_t s)
+{
+    using Cfg = TokCfg<D>;
+    const int g = p.Hq / p.Hkv, tpt = TM / g;
+    TokMaps maps;
+    const uint64_t seqs = p.cu ? 1 : p.B;
+    const uint64_t D_ = D, L_ = p.L;
+    auto map4 = [&](CUtensorMap *m, const uint16_t *base, const long *st, int heads, int box_heads,
+                    int box_tok) {
+        const uint64_t dims[4] = {D_, (uint64_t)heads, L_, seqs};
+        const uint64_t str[3] = {(uint64_t)st[1] * 2, (uint64_t)st[2] * 2,
+                                 (uint64_t)(seqs > 1 ? st[0] : st[2]) * 2};
+        const uint32_t box[4] = {64, (uint32_t)box_heads, (uint32_t)box_tok, 1};
+        return encode_tmap_4d_f16(m, base, dims, str, box);
+    };
+    bool ok = map4(&maps.q, p.q, p.qs, p.Hq, g, tpt);
+    if (p.n) {
+        p.kv_rows = p.block_table ? p.num_pages * PAGE_SLOTS : p.B * p.Hkv * p.C;
+        ok = ok && encode_tmap_2d_f16(&maps.k, p.k, D, p.kv_rows, 64, HALF) &&
+             encode_tmap_2d_f16(&maps.v, p.v, D, p.kv_rows, 64, HALF);
+    } else {
+        ok = ok && map4(&maps.k, p.k, p.ks, p.Hkv, 1, HALF) &&
+             map4(&maps.v, p.v, p.vs, p.Hkv, 1, HALF);
+    }
+    if (!ok)
+        return cudaErrorInvalidValue;
+    cudaError_t e =
+        set_smem_once(reinterpret_cast<const void *>(k_attend_tokens<D>), Cfg::SMEM);
+    if (e != cudaSuccess)
+        return e;
+    // packed: every sequence ends in at most one partial range
+    const long ranges = p.cu ? (long)p.L / (2 * tpt) + p.B
+                             : (long)((p.L + 2 * tpt - 1) / (2 * tpt)) * p.B;
+    const long items = ranges * p.Hkv * p.splits;
+    const int sms = sm_count();
+    k_attend_tokens<D><<<(unsigned)(items < sms ? items : sms), NTHR, Cfg::SMEM, s>>>(maps, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || p.splits == 1)
+        return e;
+    const long rows = (long)p.L * p.Hq;
+    k_combine_tokens<D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
+    return cudaGetLastError();
 }
 
 } // namespace
 
+int plan_tokens_splits(int T, int B, int Hq, int Hkv, int C, int requested)
+{
+    const int blocks = (C + TK - 1) / TK;
+    int s = requested;
+    if (s <= 0) {
+        // the items that certainly exist, against one CTA per SM
+        const int tpt = TM / (Hq / Hkv);
+        const long items = ((long)T / (2 * tpt) + B) * Hkv;
+        s = (int)(sm_count() / (items > 0 ? items : 1));
+    }
+    s = s < blocks ? s : blocks;
+    return s < 1 ? 1 : s > 64 ? 64 : s;
+}
+
 cudaError_t launch_attend_tokens(const TokensLaunch &p, cudaStream_t s)
 {
-    const int g = p.Hq / p.Hkv, tokens = ROWS / g;
-    const long per = (p.L + tokens - 1) / tokens;
-    // packed: every sequence ends in at most one partial tile
-    const long tiles = p.cu ? (long)p.L / tokens + p.B : per * p.B;
-    if (tiles > 0x7fffffffL)
-        return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)tiles, (unsigned)p.Hkv);
-    if (p.D == 128)
-        k_attend_tokens<128><<<grid, 128, 0, s>>>(p);
-    else
-        k_attend_tokens<64><<<grid, 128, 0, s>>>(p);
-    return cudaGetLastError();
+    return p.D == 128 ? attend_tokens_impl<128>(p, s) : attend_tokens_impl<64>(p, s);
 }
 
 } // namespace kvc

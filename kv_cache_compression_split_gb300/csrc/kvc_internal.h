@@ -32,6 +32,10 @@ int resident_ctas(const void *func, int threads, int smem);
 bool encode_tmap_2d_f16(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows,
                         uint32_t box_inner, uint32_t box_rows);
 
+// Rank-4 map of binary16 data (dims and box innermost first, byte strides of dims 1..3).
+bool encode_tmap_4d_f16(CUtensorMap *map, const void *base, const uint64_t dims[4],
+                        const uint64_t strides[3], const uint32_t box[4]);
+
 struct SlotAttendPlan {
     int splits;
     int tiles_per_split;
@@ -121,10 +125,17 @@ struct TokensLaunch {
     int C;                     // chunk: slots per unit
     const int32_t *block_table; // chunk: paged layout (nullptr: dense)
     int num_pages;
+    int kv_rows;               // chunk: rows of the K / V arrays (set by the launcher)
+    int splits;                // key ranges per item, merged by a second launch when above 1
+    float *part_o;             // [L * Hq, splits, D]
+    float2 *part_ml;           // [L * Hq, splits]: reference and sum
     float scale_log2;
     int *status;
 };
 cudaError_t launch_attend_tokens(const TokensLaunch &p, cudaStream_t s);
+
+// Key ranges per unit of a chunk of T tokens (requested > 0: that many, within the cache).
+int plan_tokens_splits(int T, int B, int Hq, int Hkv, int C, int requested);
 
 // Page tables, slot map, positions and lengths of a ragged batch of new tokens.
 struct PlanLaunch {
