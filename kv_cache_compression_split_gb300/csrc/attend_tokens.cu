@@ -16,7 +16,9 @@
 // alternately.  Either way two independent softmax chains run per SM, and the tensor
 // cores work on one while the other's scores become probabilities.
 //
-// Pipeline, one CTA per SM, persistent over the items: a producer warp (TMA: query
+// Pipeline, one CTA per SM.  The grid has a CTA per item; one that runs takes over the
+// items of CTAs that have not started (cluster launch control), so work is balanced
+// without a counter in memory and its pipeline never drains.  A producer warp (TMA: query
 // tiles, and K and V blocks through a ring), an MMA warp, and a warpgroup per tile in
 // which a thread owns a row.  S = Q K^T (128 x 128, fp32) lands in TMEM; the row's
 // thread reads it, keeps the running reference m and sum l in registers, and writes
@@ -44,8 +46,12 @@ namespace {
 constexpr int TM = 128;                   // rows of a tile
 constexpr int TK = 128;                   // keys of a block
 constexpr int HALF = TK / 2;              // keys of one TMA box (a page of the cache)
-constexpr int NTHR = 320;                 // two warpgroups, producer warp, MMA warp
-constexpr int W_TMA = 8, W_MMA = 9;
+constexpr int NTHR = 384;                 // two softmax warpgroups; producer and MMA warp
+constexpr int W_TMA = 8, W_MMA = 9;       // warps 10 and 11 only fill their warpgroup
+// Registers: 384 threads are launched with 168 each, 64,512 in all.  A row's thread holds
+// its 128 scores and needs more; the third warpgroup gives what it does not use.
+constexpr int REGS_ROW = 208, REGS_IO = 88;
+static_assert(2 * 128 * REGS_ROW + 128 * REGS_IO <= NTHR * 168, "register split");
 constexpr int NI = 2;                     // slots of the item feed
 constexpr int TMEM_COLS = 512;
 constexpr float LN2 = 0.6931471805599453f;
@@ -89,14 +95,19 @@ __device__ __forceinline__ void seq_range(const TokensLaunch &p, int b, int &sta
     }
 }
 
-// Walks the items in order: sequences, KV heads, token ranges from the last (longest)
-// to the first, splits.  Every lane of the warp calls it; idx only grows.
+// Walks the items in order: sequences, token ranges from the last (longest) to the
+// first, KV heads, splits.  Every lane of the warp calls it.  It goes on from the
+// sequences of the last call, since the work is handed out in order.
 struct ItemWalk {
     int b0 = 0;
     long base = 0;
     __device__ bool find(const TokensLaunch &p, int tpt, long idx, TokItem &it)
     {
         const int lane = threadIdx.x & 31;
+        if (idx < base) {
+            b0 = 0;
+            base = 0;
+        }
         for (; b0 < p.B; b0 += 32) {
             int s = 0, n = 0;
             if (b0 + lane < p.B)
@@ -121,10 +132,10 @@ struct ItemWalk {
             const int len = __shfl_sync(0xffffffffu, n, src);
             it.start = __shfl_sync(0xffffffffu, s, src);
             it.b = b0 + src;
-            it.hk = r / (per * p.splits);
-            const int rem = r - it.hk * per * p.splits;
-            it.split = rem % p.splits;
-            it.tok0 = (per - 1 - rem / p.splits) * 2 * tpt;
+            it.split = r % p.splits;
+            const int q = r / p.splits;
+            it.hk = q % p.Hkv;
+            it.tok0 = (per - 1 - q / p.Hkv) * 2 * tpt;
             it.ntok = min(2 * tpt, len - it.tok0);
             it.two = it.ntok <= tpt;
             int n_keys = len;
@@ -222,7 +233,9 @@ __global__ void __launch_bounds__(NTHR, 1)
     uint64_t *it_full = o_full + 2, *it_empty = it_full + NI;
     uint64_t *mrg_full = it_empty + NI, *mrg_empty = mrg_full + 4;
     uint64_t *mrg_done = mrg_empty + 4, *mma_done = mrg_done + 1;
-    TokItem *s_item = reinterpret_cast<TokItem *>(mma_done + 1);
+    uint64_t *clc_full = mma_done + 1;
+    uint4 *clc = reinterpret_cast<uint4 *>(bars + 64);       // a 16-byte answer
+    TokItem *s_item = reinterpret_cast<TokItem *>(clc + 1);
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(s_item + NI);
     volatile int *abort = reinterpret_cast<int *>(s_tmem + 1);
 
@@ -252,6 +265,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         }
         mbar_init(mrg_done, 4);
         mbar_init(mma_done, 1);
+        mbar_init(clc_full, 1);
         fence_mbar_init();
     }
     if (warp == W_MMA) {
@@ -275,6 +289,8 @@ __global__ void __launch_bounds__(NTHR, 1)
         return it.b >= 0;
     };
 
+    if (warp >= W_TMA) {
+    regs_dec<REGS_IO>();
     if (warp == W_TMA) {
         // ------------------------------------------------ producer
         if (lane == 0) {
@@ -283,37 +299,44 @@ __global__ void __launch_bounds__(NTHR, 1)
             prefetch_tmap(&maps.v);
         }
         ItemWalk walk;
+        long idx = blockIdx.x;
         int n_it = 0, n_q = 0, n_two = 0, seen_two = 0;   // ring slots, query loads, merges
         bool ok = true;
-        for (int k = 0; ok; ++k) {
+        int n_clc = 0;
+        for (int k = 0; ok; ++n_clc) {
             TokItem it;
-            const bool more = walk.find(p, tpt, blockIdx.x + (long)k * gridDim.x, it);
-            if (!more)
-                it.b = -1;
-            const int slot = k % NI;
-            if (lane == 0) {
-                if (k >= NI)
-                    ok = mbar_sleep_or_abort(&it_empty[slot], ((k / NI) & 1) ^ 1, abort);
-                if (ok) {
-                    s_item[slot] = it;
-                    mbar_arrive(&it_full[slot]);
-                }
+            it.b = -1;
+            if (idx >= 0) {
+                // the next item while this one runs: take over a CTA that has not started
+                if (lane == 0)
+                    clc_request(clc, clc_full);
+                if (!walk.find(p, tpt, idx, it))
+                    it.j0 = it.j1 = it.two = 0;   // the grid is an upper bound
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok || !more)
-                break;
+            if (idx < 0 || it.b >= 0) {
+                const int slot = k % NI;
+                if (lane == 0) {
+                    ok = k < NI || mbar_sleep_or_abort(&it_empty[slot], ((k / NI) & 1) ^ 1, abort);
+                    if (ok) {
+                        s_item[slot] = it;
+                        mbar_arrive(&it_full[slot]);
+                    }
+                }
+                ++k;
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok || idx < 0)
+                    break;
+            }
             const int n = it.j1 - it.j0;
             if (it.two)
                 ++n_two;
-            if (n <= 0)
-                continue;
             const int unit = it.b * p.Hkv + it.hk;
             const int per = p.C / PAGE_SLOTS;
             if (p.block_table)   // the item's part of the page table into L1
                 for (int i = 2 * it.j0 + 32 * lane; i < min(per, 2 * it.j1); i += 1024)
                     asm volatile("prefetch.global.L1 [%0];" ::"l"(p.block_table +
                                                                   (size_t)unit * per + i));
-            if (lane == 0) {
+            if (lane == 0 && n > 0) {
                 if (n_q > 0)
                     ok = mbar_sleep_or_abort(q_empty, (n_q - 1) & 1, abort);
                 // a merge of the item before used the second query tile
@@ -379,10 +402,19 @@ __global__ void __launch_bounds__(NTHR, 1)
                         load(&maps.k, it.j0 + i + ahead);
                 }
             }
+            int next = -1;
+            if (lane == 0 && ok) {
+                ok = mbar_sleep_or_abort(clc_full, n_clc & 1, abort);
+                if (ok)
+                    next = clc_answer(clc);
+            }
             ok = __shfl_sync(0xffffffffu, ok, 0);
+            idx = __shfl_sync(0xffffffffu, next, 0);
         }
         // every copy has landed before the CTA leaves
         if (lane == 0) {
+            if (!ok && idx >= 0)
+                mbar_wait(clc_full, n_clc & 1);
             for (int i = n_it > NS ? n_it - NS : 0; i < n_it; ++i)
                 mbar_wait(&kv_full[i % NS], (i / NS) & 1);
             if (n_q > 0)
@@ -536,8 +568,10 @@ __global__ void __launch_bounds__(NTHR, 1)
             mbar_wait(mma_done, 0);
         }
         __syncwarp();
+    }
     } else {
         // ------------------------------------------------ softmax: a thread per row
+        regs_inc<REGS_ROW>();
         const int t = warp >> 2, quarter = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t s_col = lanes + TK * t, o_col = lanes + Cfg::COL_O + D * t;
@@ -880,8 +914,9 @@ template <int D> cudaError_t attend_tokens_impl(TokensLaunch p, cudaStream_t s)
     const long ranges = p.cu ? (long)p.L / (2 * tpt) + p.B
                              : (long)((p.L + 2 * tpt - 1) / (2 * tpt)) * p.B;
     const long items = ranges * p.Hkv * p.splits;
-    const int sms = sm_count();
-    k_attend_tokens<D><<<(unsigned)(items < sms ? items : sms), NTHR, Cfg::SMEM, s>>>(maps, p);
+    if (items > 0x7fffffffL)
+        return cudaErrorInvalidValue;
+    k_attend_tokens<D><<<(unsigned)items, NTHR, Cfg::SMEM, s>>>(maps, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1)
         return e;

@@ -292,6 +292,48 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
         : "memory");
 }
 
+// ---------------------------------------------------------------- launch control, registers
+
+// Asks to take over a CTA of this grid that has not started; the 16-byte answer arrives at
+// `dst` and completes `bar`.  Not to be called again once an answer was negative.
+__device__ __forceinline__ void clc_request(uint4 *dst, uint64_t *bar)
+{
+    fence_async_smem();   // the last answer has been read
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+        " [%0], [%1];" ::"r"(smem_u32(dst)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+
+// blockIdx.x of the CTA that was taken over, -1 when there was none.
+__device__ __forceinline__ int clc_answer(const uint4 *src)
+{
+    int x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+        "ld.shared.b128 h, [%1];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "mov.s32 %0, -1;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
+        : "=r"(x)
+        : "r"(smem_u32(src))
+        : "memory");
+    return x;
+}
+
+// Registers per thread of the calling warpgroup (every warp of it calls the same).
+template <int N> __device__ __forceinline__ void regs_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int N> __device__ __forceinline__ void regs_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ---------------------------------------------------------------- fragments
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2,
