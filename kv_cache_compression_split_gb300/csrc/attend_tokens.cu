@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(s_item + NI);
     volatile int *abort = reinterpret_cast<int *>(s_tmem + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int g = p.Hq / p.Hkv, tpt = TM / g;
 
     if (threadIdx.x == 0) {
@@ -426,36 +426,59 @@ __global__ void __launch_bounds__(NTHR, 1)
         int n_p[2] = {0, 0};
         bool ok = true;
         TokItem it;
-        const uint32_t qb = smem_u32(sq);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        // descriptors differ in the start address alone (bits 0..13, in 16 bytes)
+        const uint64_t q_desc = sdesc_k_sw128(smem_u32(sq));
+        const uint64_t k_desc = sdesc_k_sw128(smem_u32(ring));
+        const uint64_t v_desc = sdesc_mn_sw128(smem_u32(ring), Cfg::BOX_BYTES);
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             ok = ok && __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, abort));
         };
-        auto stage = [&](int i) { return smem_u32(ring + (i % NS) * Cfg::TILE_BYTES); };
-        auto qk = [&](int t, int tile, uint32_t kb) {
-            if (lane == 0) {
+        auto qk = [&](int t, int tile, int st) {   // S_t = Q_tile K^T, K in ring stage st
+            const uint64_t qd = q_desc + tile * (Cfg::TILE_BYTES >> 4);
+            const uint64_t kd = k_desc + (uint32_t)st * (Cfg::TILE_BYTES >> 4);
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * Cfg::BOX_BYTES + (kk & 3) * 32;
-                    umma_f16(tmem + TK * t, sdesc_k_sw128(qb + tile * Cfg::TILE_BYTES + off),
-                             sdesc_k_sw128(kb + off), Cfg::IDESC_QK, kk > 0 ? 1u : 0u);
+                    const uint32_t off = ((kk >> 2) * Cfg::BOX_BYTES + (kk & 3) * 32) >> 4;
+                    umma_f16(tm + TK * t, qd + off, kd + off, Cfg::IDESC_QK, kk > 0 ? 1u : 0u);
                 }
                 umma_commit(&s_full[t]);
             }
+            __syncwarp();
         };
-        auto pv = [&](int t, uint32_t vb, int keys, bool first) {
-            if (lane == 0) {
-                const int steps = min(TK, keys + 15) / 16;
-                for (int kk = 0; kk < steps; ++kk)
-                    umma_f16_ts(tmem + Cfg::COL_O + D * t, tmem + TK * t + 8 * kk,
-                                sdesc_mn_sw128(vb + 2048 * kk, Cfg::BOX_BYTES), Cfg::IDESC_PV,
-                                first && kk == 0 ? 0u : 1u);
+        auto pv = [&](int t, int st, int keys, bool first) {   // O_t (+)= P_t V
+            const uint64_t vd = v_desc + (uint32_t)st * (Cfg::TILE_BYTES >> 4);
+            const uint32_t od = tm + Cfg::COL_O + D * t, pd = tm + TK * t;
+            const uint32_t acc = first ? 0u : 1u;
+            const int steps = (keys + 15) / 16;
+            if (elect_one()) {
+                if (steps >= TK / 16) {
+#pragma unroll
+                    for (int kk = 0; kk < TK / 16; ++kk)
+                        umma_f16_ts(od, pd + 8 * kk, vd + kk * (2048 >> 4), Cfg::IDESC_PV,
+                                    kk > 0 ? 1u : acc);
+                } else {
+                    for (int kk = 0; kk < steps; ++kk)
+                        umma_f16_ts(od, pd + 8 * kk, vd + kk * (2048 >> 4), Cfg::IDESC_PV,
+                                    kk > 0 ? 1u : acc);
+                }
             }
+            __syncwarp();
         };
         auto commit = [&](uint64_t *bar) {
-            if (lane == 0)
+            if (elect_one())
                 umma_commit(bar);
+            __syncwarp();
         };
         for (int k = 0; ok && feed_get(k, it); ++k) {
+            // the same in every lane, and known to be
+            it.tok0 = __shfl_sync(0xffffffffu, it.tok0, 0);
+            it.ntok = __shfl_sync(0xffffffffu, it.ntok, 0);
+            it.shift = __shfl_sync(0xffffffffu, it.shift, 0);
+            it.j0 = __shfl_sync(0xffffffffu, it.j0, 0);
+            it.j1 = __shfl_sync(0xffffffffu, it.j1, 0);
+            it.two = __shfl_sync(0xffffffffu, it.two, 0);
             const int n = it.j1 - it.j0;
             if (n <= 0)
                 continue;
@@ -469,7 +492,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                 if (!ok)
                     break;
                 tc_fence_after();
-                const uint32_t kb = stage(n_it);
+                const int kb = n_it % NS;
                 if (it.two) {
                     qk(i, 0, kb);
                 } else {
@@ -488,7 +511,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                 wait(&kv_full[vs % NS], (vs / NS) & 1);
                 if (!ok)
                     break;
-                const uint32_t vb = stage(vs);
+                const int vb = vs % NS;
                 const int keys = min(TK, r1.end - j * TK);
                 if (keys & 15) {   // rows behind the last key of the item: cleared
                     const int rows = 16 - (keys & 15);
@@ -515,7 +538,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                         if (!ok)
                             break;
                         tc_fence_after();
-                        qk(t, 0, stage(ks));
+                        qk(t, 0, ks % NS);
                         commit(&kv_empty[ks % NS]);
                         if (i + ahead == n - 1)
                             commit(q_empty);
@@ -536,7 +559,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                         if (!ok)
                             break;
                         tc_fence_after();
-                        qk(0, 0, stage(ks));
+                        qk(0, 0, ks % NS);
                     } else {
                         commit(&o_full[0]);
                     }
@@ -553,7 +576,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                     if (!ok)
                         break;
                     tc_fence_after();
-                    qk(1, 1, stage(ks));
+                    qk(1, 1, ks % NS);
                     commit(&kv_empty[ks % NS]);
                     if (i + 2 == n)
                         commit(q_empty);
@@ -563,10 +586,8 @@ __global__ void __launch_bounds__(NTHR, 1)
             }
         }
         // every product has finished before TMEM is released
-        if (lane == 0) {
-            umma_commit(mma_done);
-            mbar_wait(mma_done, 0);
-        }
+        commit(mma_done);
+        mbar_wait(mma_done, 0);
         __syncwarp();
     }
     } else {

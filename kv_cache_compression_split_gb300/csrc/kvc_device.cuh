@@ -480,6 +480,20 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
+// True in one lane of a converged warp, the same one each time.  A branch on it keeps
+// operands that are the same in every lane in uniform registers: two instructions per
+// tcgen05.mma, against ten behind a test of the lane number.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(x));
+    return x != 0;
+}
+
 // The mbarrier receives one arrival once every tcgen05 operation this thread
 // issued before has completed.
 __device__ __forceinline__ void umma_commit(uint64_t *bar)
