@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 import threading
 from dataclasses import dataclass
 from typing import Optional
@@ -125,14 +126,11 @@ def lib():
                                                 P]),
                 "kvc_random_evict": (st, [C.POINTER(SlotCacheDesc), i, C.c_double, C.c_uint64,
                                           C.c_uint32, P]),
-                "kvc_prompt_attend": (st, [C.POINTER(PromptArgs), P]),
-                "kvc_chunk_workspace_size": (C.c_size_t, [C.POINTER(ChunkArgs)]),
-                "kvc_chunk_attend": (st, [C.POINTER(ChunkArgs), P]),
-                "kvc_append_plan": (st, [C.POINTER(SlotCacheDesc), C.POINTER(PagePoolDesc), P, i,
-                                         i, C.POINTER(SlotCacheDesc), C.POINTER(PagePoolDesc), P,
-                                         P]),
-                "kvc_append_packed": (st, [C.POINTER(SlotCacheDesc), P, _I64x2, P, _I64x2, i, P,
-                                           P]),
+                "kvc_prompt_attend": (st, [P, P]),
+                "kvc_chunk_workspace_size": (C.c_size_t, [P]),
+                "kvc_chunk_attend": (st, [P, P]),
+                "kvc_append_plan": (st, [P, P, P, i, i, P, P, P, P]),
+                "kvc_append_packed": (st, [P, P, P, P, P, i, P, P]),
                 "kvc_status_string": (C.c_char_p, [i]),
                 "kvc_read_device_status": (st, [C.POINTER(C.c_int), P]),
             }
@@ -190,35 +188,59 @@ def _state_without_desc(obj):
 
 
 
-def _rows(t, what, dims):
-    """Device address of binary16 rows: a tensor of `dims` dimensions whose last one is
-    contiguous; the others may have any strides, which the call passes on."""
+def _rows(t, what, dims, dev):
+    """Device address and strides of binary16 rows: a tensor of `dims` dimensions whose last
+    one is contiguous; the others may have any strides, which the call passes on."""
     if t.dtype is not torch.float16:
         raise ValueError(f"kvc: {what} must be float16, got {t.dtype}")
-    if t.dim() != dims or (t.stride(-1) != 1 and t.shape[-1] > 1):
+    st = t.stride()
+    if len(st) != dims or (st[-1] != 1 and t.shape[-1] > 1):
         raise ValueError(f"kvc: {what} must have {dims} dimensions, the last one contiguous")
-    if not t.is_cuda:
-        raise ValueError(f"kvc: tensor on {t.device}; the library takes CUDA tensors")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"kvc: tensor on {t.device}, expected the current device "
-                         f"cuda:{torch.cuda.current_device()}")
+    if t.get_device() != dev:
+        _wrong_device(t, dev)
+    if 1 in t.shape:   # a dimension of size 1 is never stepped over: any stride stands for it
+        st = tuple(8 if n == 1 else x for n, x in zip(t.shape, st))
+    return t.data_ptr(), st
+
+
+def _typed(t, what, dtype, shape, dev):
+    """Device address of a contiguous tensor of this type and shape (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"kvc: {what} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of "
+                         f"{tuple(t.shape)}")
+    if t.get_device() != dev:
+        _wrong_device(t, dev)
+    if not t.is_contiguous():
+        raise ValueError("kvc: tensor arguments must be contiguous")
     return t.data_ptr()
 
 
-def _typed(t, what, dtype, shape):
-    """Device address of a contiguous tensor of this type and shape (None stays None)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or tuple(t.shape) != shape:
-        raise ValueError(f"kvc: {what} must be {dtype} of shape {shape}, got {t.dtype} of "
-                         f"{tuple(t.shape)}")
-    return _ptr(t)
+def _wrong_device(t, dev):
+    if not t.is_cuda:
+        raise ValueError(f"kvc: tensor on {t.device}; the library takes CUDA tensors")
+    raise ValueError(f"kvc: tensor on {t.device}, expected the current device cuda:{dev}")
 
 
-def _stride(t, dim):
-    """Element stride of a dimension; one of size 1 is never stepped over, so any stride
-    stands for it."""
-    return t.stride(dim) if t.shape[dim] > 1 else 8
+# The argument structs packed field by field in one call (a ctypes assignment per field took
+# longer than the launch); the field order is that of PromptArgs and ChunkArgs.
+_pack_prompt = struct.Struct("@5i4x7P12qf4x").pack
+_pack_chunk = struct.Struct("@2i5P4qPNif").pack
+_pack_2q = struct.Struct("@2q").pack
+_pack_3p = struct.Struct("@3P").pack
+
+
+def _device(stream):
+    """Index of the current device, and the stream's handle (-2, which no tensor's device
+    equals, on a machine without one: the checks of the arguments then say what is wrong)."""
+    try:
+        dev = torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2, 0
+    if stream is None:
+        return dev, _raw_stream(dev) if _raw_stream is not None else _stream(None)
+    return dev, _stream(stream)
 
 
 def _stream(stream):
@@ -412,55 +434,46 @@ def kvc_prompt_attend(q, k, v, o, cu_seqlens=None, lens=None, lse=None,
     """Causal attention over whole prompts (see kvc.h).  Packed: q, o [T, Hq, D], k, v
     [T, Hkv, D], cu_seqlens [B + 1] int32, lse [Hq, T].  Padded: q, o [B, Hq, L, D], k, v
     [B, Hkv, >= L, D], optional lens [B] int32, lse [B, Hq, L].  Rows may be strided."""
-    a = PromptArgs()
+    dev, stream = _device(stream)
     if cu_seqlens is not None:
         if lens is not None:
             raise ValueError("kvc_prompt_attend takes cu_seqlens (packed) or lens (padded)")
-        T, Hq, D = q.shape
+        L, Hq, D = q.shape
         Hkv = k.shape[1]
-        a.B, a.L, seq, dims = cu_seqlens.numel() - 1, T, (), 3
-        kv, tok, head = (T, Hkv, D), 0, 1
+        B, dims = cu_seqlens.numel() - 1, 3
+        kv, rows = (L, Hkv, D), (Hq, L)
     else:
-        B, Hq, T, D = q.shape
+        B, Hq, L, D = q.shape
         Hkv = k.shape[1]
-        a.B, a.L, seq, dims = B, T, (B,), 4
-        kv, tok, head = (B, Hkv, T, D), 2, 1
-        if k.dim() == 4 and k.shape[2] > T:
-            k = k[:, :, :T]
-        if v.dim() == 4 and v.shape[2] > T:
-            v = v[:, :, :T]
-    if tuple(k.shape) != kv or tuple(v.shape) != kv or o.shape != q.shape:
+        dims = 4
+        kv, rows = (B, Hkv, L, D), (B, Hq, L)
+        if k.dim() == 4 and k.shape[2] > L:
+            k = k[:, :, :L]
+        if v.dim() == 4 and v.shape[2] > L:
+            v = v[:, :, :L]
+    if k.shape != kv or v.shape != kv or o.shape != q.shape:
         raise ValueError(f"kvc_prompt_attend: q {tuple(q.shape)}, k {tuple(k.shape)}, v "
                          f"{tuple(v.shape)}, o {tuple(o.shape)} do not belong together")
-    a.cu_seqlens = _typed(cu_seqlens, "cu_seqlens", torch.int32, (a.B + 1,))
-    a.lens = _typed(lens, "lens", torch.int32, (a.B,))
-    a.Hq, a.Hkv, a.D = Hq, Hkv, D
-    a.q, a.k, a.v, a.o = (_rows(q, "q", dims), _rows(k, "k", dims), _rows(v, "v", dims),
-                          _rows(o, "o", dims))
-    for t, s in ((q, a.q_stride), (k, a.k_stride), (v, a.v_stride), (o, a.o_stride)):
-        if seq:
-            s[0] = _stride(t, 0)
-        s[1], s[2] = _stride(t, head), _stride(t, tok)
-    a.lse = _typed(lse, "lse", torch.float32, (*seq, Hq, T))
-    a.softmax_scale = float(softmax_scale)
-    _check(lib().kvc_prompt_attend(C.byref(a), _stream(stream)), "kvc_prompt_attend")
-
-
-def _chunk_args(cache, q, num_splits, scale):
-    a = ChunkArgs()
-    if q.dim() != 3 or q.shape[2] != cache.D:
-        raise ValueError(f"kvc_chunk_attend: q must be [T, Hq, {cache.D}], got {tuple(q.shape)}")
-    d = cache.desc()
-    a.cache = cache.__dict__["_desc_p"]
-    a.T, a.Hq = int(q.shape[0]), int(q.shape[1])
-    a.num_splits = int(num_splits)
-    a.softmax_scale = float(scale)
-    return a, d
+    cu = _typed(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
+    ln = _typed(lens, "lens", torch.int32, (B,), dev)
+    ls = _typed(lse, "lse", torch.float32, rows, dev)
+    (qp, qs), (kp, ks) = _rows(q, "q", dims, dev), _rows(k, "k", dims, dev)
+    (vp, vs), (op, os_) = _rows(v, "v", dims, dev), _rows(o, "o", dims, dev)
+    if dims == 3:
+        args = _pack_prompt(B, Hq, Hkv, D, L, qp, kp, vp, op, ls, cu, ln, 0, qs[1], qs[0], 0, ks[1],
+                            ks[0], 0, vs[1], vs[0], 0, os_[1], os_[0], softmax_scale)
+    else:
+        args = _pack_prompt(B, Hq, Hkv, D, L, qp, kp, vp, op, ls, cu, ln, *qs[:3], *ks[:3], *vs[:3],
+                            *os_[:3], softmax_scale)
+    _check((_lib or lib()).kvc_prompt_attend(args, stream), "kvc_prompt_attend")
 
 
 def kvc_chunk_workspace_size(cache: "SlotCache", q, num_splits: int = 0) -> int:
-    a, _keep = _chunk_args(cache, q, num_splits, 0.0)
-    return int(lib().kvc_chunk_workspace_size(C.byref(a)))
+    """Bytes of workspace for kvc_chunk_attend (only q's shape is read)."""
+    cache.desc()
+    args = _pack_chunk(q.shape[1], q.shape[0], C.addressof(cache.__dict__["_desc"]), 0, 0, 0, 0, 0, 0,
+                       0, 0, 0, 0, num_splits, 0.0)
+    return int((_lib or lib()).kvc_chunk_workspace_size(args))
 
 
 def kvc_chunk_attend(cache: "SlotCache", q, cu_new, o, lse=None, workspace=None,
@@ -468,17 +481,20 @@ def kvc_chunk_attend(cache: "SlotCache", q, cu_new, o, lse=None, workspace=None,
     """Attention of each sequence's chunk of new tokens over the slot cache, which already
     holds their rows in the last slots (see kvc.h): q, o [T, Hq, D] packed by cu_new [B + 1]
     int32 (rows may be strided), lse [Hq, T]."""
-    a, _keep = _chunk_args(cache, q, num_splits, softmax_scale)
-    if o.shape != q.shape:
-        raise ValueError("kvc_chunk_attend: o must have q's shape")
-    a.q, a.o = _rows(q, "q", 3), _rows(o, "o", 3)
-    a.cu_new = _typed(cu_new, "cu_new", torch.int32, (cache.B + 1,))
-    for t, s in ((q, a.q_stride), (o, a.o_stride)):
-        s[0], s[1] = _stride(t, 1), _stride(t, 0)
-    a.lse = _typed(lse, "lse", torch.float32, (a.Hq, a.T))
-    a.workspace = _ptr(workspace)
-    a.workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().kvc_chunk_attend(C.byref(a), _stream(stream)), "kvc_chunk_attend")
+    dev, stream = _device(stream)
+    d = cache.desc()
+    T, Hq, D = q.shape
+    if D != d.D or o.shape != q.shape:
+        raise ValueError(f"kvc_chunk_attend: q and o must be [T, Hq, {d.D}], got "
+                         f"{tuple(q.shape)} and {tuple(o.shape)}")
+    cu = _typed(cu_new, "cu_new", torch.int32, (d.B + 1,), dev)
+    ls = _typed(lse, "lse", torch.float32, (Hq, T), dev)
+    (qp, qs), (op, os_) = _rows(q, "q", 3, dev), _rows(o, "o", 3, dev)
+    ws = _ptr(workspace) or 0
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    args = _pack_chunk(Hq, T, C.addressof(d), qp, op, cu, ls, qs[1], qs[0], os_[1], os_[0], ws,
+                       size, num_splits, softmax_scale)
+    _check((_lib or lib()).kvc_chunk_attend(args, stream), "kvc_chunk_attend")
 
 
 def kvc_append_plan(cache: "SlotCache", cu_new, slot_map, pool: "Optional[PagePool]" = None,
@@ -487,31 +503,31 @@ def kvc_append_plan(cache: "SlotCache", cu_new, slot_map, pool: "Optional[PagePo
     """Page tables, slot map [T, Hkv] int32, positions and lengths of a ragged batch of new
     tokens (cu_new [B + 1] int32).  A paged cache takes its pages from `pool`.  `out` and
     `pool_out` receive the new state (default: the cache and the pool, in place)."""
+    dev, stream = _device(stream)
     d = cache.desc()
     n = out.desc() if out is not None else d
-    pi = pool.desc(cache) if pool is not None else None
-    po = pool_out.desc(out if out is not None else cache) if pool_out is not None else pi
-    T = int(slot_map.shape[0])
-    _check(lib().kvc_append_plan(C.byref(d), None if pi is None else C.byref(pi),
-                                 _typed(cu_new, "cu_new", torch.int32, (cache.B + 1,)), T,
-                                 int(release), C.byref(n), None if po is None else C.byref(po),
-                                 _typed(slot_map, "slot_map", torch.int32, (T, cache.Hkv)),
-                                 _stream(stream)), "kvc_append_plan")
+    pi = pool.desc(d, dev) if pool is not None else None
+    po = pool_out.desc(n, dev) if pool_out is not None else pi
+    T = slot_map.shape[0]
+    _check((_lib or lib()).kvc_append_plan(
+        C.addressof(d), pi, _typed(cu_new, "cu_new", torch.int32, (d.B + 1,), dev), T,
+        1 if release else 0, C.addressof(n), po,
+        _typed(slot_map, "slot_map", torch.int32, (T, d.Hkv), dev), stream), "kvc_append_plan")
 
 
 def kvc_append_packed(cache: "SlotCache", k_new, v_new, slot_map, stream=None):
     """Packed rows k_new, v_new [T, Hkv, D] (rows may be strided) to the cache rows that
     slot_map [T, Hkv] names (kvc_append_plan writes it); n and pos are not touched."""
+    dev, stream = _device(stream)
     d = cache.desc()
-    shape = (int(slot_map.shape[0]), cache.Hkv, cache.D)
-    if tuple(k_new.shape) != shape or tuple(v_new.shape) != shape:
+    T = slot_map.shape[0]
+    shape = (T, d.Hkv, d.D)
+    if k_new.shape != shape or v_new.shape != shape:
         raise ValueError(f"kvc_append_packed: k_new and v_new must be {shape}")
-    ks = _I64x2(_stride(k_new, 0), _stride(k_new, 1))
-    vs = _I64x2(_stride(v_new, 0), _stride(v_new, 1))
-    _check(lib().kvc_append_packed(C.byref(d), _rows(k_new, "k_new", 3), ks,
-                                   _rows(v_new, "v_new", 3), vs, shape[0],
-                                   _typed(slot_map, "slot_map", torch.int32, shape[:2]),
-                                   _stream(stream)), "kvc_append_packed")
+    (kp, ks), (vp, vs) = _rows(k_new, "k_new", 3, dev), _rows(v_new, "v_new", 3, dev)
+    _check((_lib or lib()).kvc_append_packed(
+        C.addressof(d), kp, _pack_2q(ks[0], ks[1]), vp, _pack_2q(vs[0], vs[1]), T,
+        _typed(slot_map, "slot_map", torch.int32, (T, d.Hkv), dev), stream), "kvc_append_packed")
 
 
 def kvc_read_device_status(stream=None) -> int:
@@ -581,8 +597,11 @@ class SlotCache:
     def desc(self) -> SlotCacheDesc:
         # built once and kept while the fields' storage, shapes and strides stay the same (a
         # field replaced or resized in place yields a new key, and the fields are checked again)
-        t = (self.K, self.V, self.pos, self.n, self.seqlen, self.block_table)
-        key = _desc_key(t)
+        K, V, pos, n, sl, bt = self.K, self.V, self.pos, self.n, self.seqlen, self.block_table
+        key = (K.data_ptr(), K.shape, K.stride(), V.data_ptr(), V.shape, V.stride(),
+               pos.data_ptr(), pos.shape, pos.stride(), n.data_ptr(), n.shape, n.stride(),
+               sl.data_ptr(), sl.shape, sl.stride(),
+               None if bt is None else (bt.data_ptr(), bt.shape, bt.stride()))
         d = self.__dict__.get("_desc")
         if d is not None and self.__dict__.get("_desc_key") == key:
             return d
@@ -611,10 +630,12 @@ class PagePool:
                    free=torch.arange(cache.num_pages - 1, -1, -1, dtype=torch.int32, device=dev),
                    count=torch.full((1,), cache.num_pages, dtype=torch.int32, device=dev))
 
-    def desc(self, cache: "SlotCache") -> PagePoolDesc:
-        return PagePoolDesc(_typed(self.pages, "pages", torch.int32, (cache.B, cache.Hkv)),
-                            _typed(self.free, "free", torch.int32, (cache.num_pages,)),
-                            _typed(self.count, "count", torch.int32, (1,)))
+    def desc(self, cache: SlotCacheDesc, dev: int) -> bytes:
+        """The kvc_page_pool struct (the fields of PagePoolDesc) for a cache's descriptor."""
+        i32 = torch.int32
+        return _pack_3p(_typed(self.pages, "pages", i32, (cache.B, cache.Hkv), dev),
+                        _typed(self.free, "free", i32, (cache.num_pages,), dev),
+                        _typed(self.count, "count", i32, (1,), dev))
 
 
 @dataclass

@@ -22,8 +22,10 @@ namespace kvc {
 
 namespace {
 
-constexpr int CTAS = 8;        // one portable cluster
+constexpr int CTAS = 16;       // one cluster
 constexpr int THREADS = 1024;
+constexpr int CU_CACHE = 2048; // sequence starts held in shared memory
+constexpr int HEADS = 8;       // heads of a token whose loads are in flight together
 constexpr int PLAN_MAX_SPAN = KVC_PLAN_MAX_UNITS / (CTAS * THREADS);
 
 __device__ __forceinline__ int ld_cluster_s32(const int *local, uint32_t rank)
@@ -86,23 +88,82 @@ __device__ __forceinline__ void scan2(int &x, int &y, int &tx, int &ty)
     ty = s_y[31];
 }
 
-// Units a thread owns: SPAN consecutive ones, so 8192 * SPAN units at most.
-template <int SPAN>
-__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(THREADS)
-    k_append_plan(const PlanLaunch p)
+// dst[i] = src[i] for i in [0, n), by the whole cluster, 16 bytes at a time where both are
+// aligned, four loads in flight per thread.
+__device__ __forceinline__ void copy_i32(int32_t *dst, const int32_t *src, long n, int gtid)
 {
+    constexpr int U = 4;
+    const long gsize = CTAS * THREADS;
+    long done = 0;
+    if (((reinterpret_cast<uintptr_t>(dst) | reinterpret_cast<uintptr_t>(src)) & 15) == 0) {
+        const long n4 = n / 4;
+        for (long i = gtid; i < n4; i += U * gsize) {
+            int4 x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i + u * gsize < n4)
+                    x[u] = reinterpret_cast<const int4 *>(src)[i + u * gsize];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i + u * gsize < n4)
+                    reinterpret_cast<int4 *>(dst)[i + u * gsize] = x[u];
+        }
+        done = 4 * n4;
+    }
+    for (long i = done + gtid; i < n; i += gsize)
+        dst[i] = src[i];
+}
+
+// The last index whose value is at most x, in v[0] = 0, v[1], ..., v[n], none smaller than
+// the one before it.
+__device__ __forceinline__ int last_at_most(const int *v, int n, int x)
+{
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (v[mid] <= x)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// A thread owns SPAN consecutive units, so CTAS * THREADS * SPAN units at most.
+template <int SPAN> struct PlanSmem {
+    int cu[CU_CACHE];
+    int grow[THREADS * SPAN + 1];   // pages taken by the CTA's units before each unit
+    int back[THREADS * SPAN + 1];   // pages given back
+    int held[THREADS * SPAN];
+};
+
+template <int SPAN>
+__global__ void __launch_bounds__(THREADS) k_append_plan(const PlanLaunch p)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    PlanSmem<SPAN> &sm = *reinterpret_cast<PlanSmem<SPAN> *>(smem);
     __shared__ int s_sum[3];   // this CTA's pages asked for, given back and granted
     const int rank = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
     const int gtid = rank * THREADS + tid, gsize = CTAS * THREADS;
     const int units = p.B * p.Hkv;
     const int per = p.C / PAGE_SLOTS;
-    const int u0 = gtid * SPAN;
+    const int u0 = gtid * SPAN, cta_u0 = rank * THREADS * SPAN;
     int left = 0, n_back = 0;      // pages left on the stack, pages given back
-    int held[SPAN], now[SPAN], at[SPAN];   // pages before and after; place in the stack
+
+    bool backwards = false;
+    for (int b = tid; b < p.B; b += THREADS) {
+        const int c0 = p.cu[b], c1 = p.cu[b + 1];
+        backwards |= c1 < c0;
+        if (b < CU_CACHE)
+            sm.cu[b] = c0;
+    }
 
     if (p.table) {
+        if (p.table_out != p.table)   // entries that change are written again below
+            copy_i32(p.table_out, p.table, (long)units * per, gtid);
         // ---- scan: pages asked for and given back by the units before each unit
         const int count = min(max(*p.count, 0), p.num_pages);
+        int held[SPAN], now[SPAN];     // pages before and after
         int ask = 0, back = 0;
 #pragma unroll
         for (int i = 0; i < SPAN; ++i) {
@@ -124,36 +185,47 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(THREADS)
         }
         int tx, ty;
         scan2(ask, back, tx, ty);
+#pragma unroll
+        for (int i = 0; i < SPAN; ++i) {
+            sm.held[tid * SPAN + i] = held[i];
+            sm.grow[tid * SPAN + i] = ask;
+            sm.back[tid * SPAN + i] = back;
+            ask += max(0, now[i] - held[i]);
+            back += max(0, held[i] - now[i]);
+        }
         if (tid == 0) {
             s_sum[0] = tx;
             s_sum[1] = ty;
             s_sum[2] = 0;
+            sm.grow[THREADS * SPAN] = tx;
+            sm.back[THREADS * SPAN] = ty;
         }
         cluster_sync_all();
-        int total = 0;
+        int total = 0, before = 0, back0 = 0;   // before this CTA's first unit
         for (int r = 0; r < CTAS; ++r) {
             const int a = ld_cluster_s32(&s_sum[0], r), k = ld_cluster_s32(&s_sum[1], r);
-            ask += r < rank ? a : 0;
-            back += r < rank ? k : 0;
+            before += r < rank ? a : 0;
+            back0 += r < rank ? k : 0;
             total += a;
             n_back += k;
         }
-        // ---- grants: a unit that the stack cannot serve in full keeps what it has
+        // ---- grants: a unit that the stack cannot serve in full keeps what it has.  Units
+        // are served in order, so those served are the ones up to some unit and those that
+        // ask for nothing.
         int granted = 0;
 #pragma unroll
         for (int i = 0; i < SPAN; ++i) {
-            const int g = max(0, now[i] - held[i]), k = max(0, held[i] - now[i]);
-            at[i] = g ? count - 1 - ask : back;
-            if (g && ask + g > count) {
+            const int g = max(0, now[i] - held[i]);
+            if (g && before + sm.grow[tid * SPAN + i] + g > count) {
                 now[i] = held[i];
                 flag_error(p.status, DEV_CAPACITY);
             } else {
                 granted += g;
             }
-            ask += g;
-            back += k;
+            if (u0 + i < units)
+                p.pages_out[u0 + i] = now[i];
         }
-        int taken = total;
+        int taken = total, mine = tx;   // pages taken in all, and by this CTA
         if (total > count) {   // the same on every CTA of the cluster
             granted = __reduce_add_sync(0xffffffffu, granted);
             if (lane == 0)
@@ -162,55 +234,29 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(THREADS)
             taken = 0;
             for (int r = 0; r < CTAS; ++r)
                 taken += ld_cluster_s32(&s_sum[2], r);
+            mine = s_sum[2];
         }
         left = count - taken;
-        // ---- table rows, a warp per row: kept entries, then the new pages
-        const bool copy = p.table_out != p.table;
-#pragma unroll
-        for (int i = 0; i < SPAN; ++i) {
-            for (int l = 0; l < 32; ++l) {
-                const int u = __shfl_sync(0xffffffffu, u0, l) + i;
-                if (u >= units)
-                    break;
-                const int h = __shfl_sync(0xffffffffu, held[i], l);
-                const int w = __shfl_sync(0xffffffffu, now[i], l);
-                const int top = __shfl_sync(0xffffffffu, at[i], l);
-                const int32_t *src = p.table + (size_t)u * per;
-                int32_t *dst = p.table_out + (size_t)u * per;
-                for (int j = (copy ? 0 : h) + lane; j < (copy ? per : w); j += 32) {
-                    if (j >= h && j < w)
-                        dst[j] = p.free_list[top - (j - h)];
-                    else if (j < w || j >= h)   // entries that go back are written below
-                        dst[j] = src[j];
-                }
-            }
-            if (u0 + i < units)
-                p.pages_out[u0 + i] = now[i];
+        // ---- new pages of the CTA's units, the next ones of the stack
+        for (int x = tid; x < mine; x += THREADS) {
+            const int i = last_at_most(sm.grow, THREADS * SPAN, x);
+            p.table_out[(size_t)(cta_u0 + i) * per + sm.held[i] + x - sm.grow[i]] =
+                p.free_list[count - 1 - before - x];
         }
         if (p.free_out != p.free_list)
-            for (int i = gtid; i < left; i += gsize)
-                p.free_out[i] = p.free_list[i];
-        cluster_sync_all();   // every new page is taken, every row and page count written
+            copy_i32(p.free_out, p.free_list, left, gtid);
+        cluster_sync_all();   // every new page is taken, every page count written
         // ---- returned pages go on the stack in unit order
-#pragma unroll
-        for (int i = 0; i < SPAN; ++i) {
-            unsigned any = __ballot_sync(0xffffffffu, now[i] < held[i]);
-            while (any) {
-                const int l = __ffs(any) - 1;
-                any &= any - 1;
-                const int u = __shfl_sync(0xffffffffu, u0, l) + i;
-                const int h = __shfl_sync(0xffffffffu, held[i], l);
-                const int w = __shfl_sync(0xffffffffu, now[i], l);
-                const int to = left + __shfl_sync(0xffffffffu, at[i], l);
-                for (int j = w + lane; j < h; j += 32) {
-                    const int pg = p.table[(size_t)u * per + j];
-                    p.table_out[(size_t)u * per + j] = -1;
-                    if (to + j - w < p.num_pages)
-                        p.free_out[to + j - w] = pg;
-                    else
-                        flag_error(p.status, DEV_CAPACITY);
-                }
-            }
+        for (int x = tid; x < ty; x += THREADS) {
+            const int i = last_at_most(sm.back, THREADS * SPAN, x);
+            const int gave = sm.back[i + 1] - sm.back[i];
+            const size_t e = (size_t)(cta_u0 + i) * per + sm.held[i] - gave + x - sm.back[i];
+            const int pg = p.table[e], to = left + back0 + x;
+            p.table_out[e] = -1;
+            if (to < p.num_pages)
+                p.free_out[to] = pg;
+            else
+                flag_error(p.status, DEV_CAPACITY);
         }
     } else {
         for (int u = gtid; u < units; u += gsize) {
@@ -222,48 +268,61 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(THREADS)
 
     // ---- slot map and positions: a thread per token.  Ranges that run backwards cannot be
     // bisected: then the first sequence that holds the token is looked for one by one.
-    bool backwards = false;
-    for (int b = tid; b < p.B; b += THREADS)
-        backwards |= p.cu[b + 1] < p.cu[b];
     backwards = __syncthreads_or(backwards);
+    const int *starts = p.B <= CU_CACHE ? sm.cu : p.cu;
     for (int t = gtid; t < p.T; t += gsize) {
-        int lo = 0, hi = p.B;   // the first sequence that starts behind t, less one
-        while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (p.cu[mid + 1] <= t)
-                lo = mid + 1;
-            else
-                hi = mid;
-        }
-        int start = 0;
-        int m = lo < p.B && !backwards ? new_tokens(p, lo, start) : 0;
-        for (int b = 0; backwards && b < p.B; ++b) {
+        int b = 0, start = 0, m = 0;
+        if (!backwards) {
+            b = last_at_most(starts, p.B - 1, t);   // of sequences without tokens, the last
             m = new_tokens(p, b, start);
-            lo = b;
-            if (t >= start && t < start + m)
-                break;
+        } else {
+            for (; b < p.B; ++b) {
+                m = new_tokens(p, b, start);
+                if (t >= start && t < start + m)
+                    break;
+            }
         }
-        const bool inside = t >= start && t < start + m;
+        const bool inside = b < p.B && t >= start && t < start + m;
         const int step = t - start;
-        const int P = inside ? p.seqlen[lo] + step : 0;
-        for (int h = 0; h < p.Hkv; ++h) {
-            int row = -1;
-            if (inside) {
-                const int u = lo * p.Hkv + h, n = p.n[u], slot = n + step;
-                if (fits(p, n, m) && (!p.table || p.pages_out[u] * (long)PAGE_SLOTS >= n + m)) {
-                    if (!p.table) {
-                        row = u * p.C + slot;
-                    } else {
-                        const int pg = p.table_out[(size_t)u * per + slot / PAGE_SLOTS];
-                        if (pg >= 0 && pg < p.num_pages)
-                            row = pg * PAGE_SLOTS + slot % PAGE_SLOTS;
-                        else
-                            flag_error(p.status, DEV_CAPACITY);
-                    }
-                    p.pos[(size_t)u * p.C + slot] = P;
+        const int P = inside ? p.seqlen[b] + step : 0;
+        for (int h0 = 0; h0 < p.Hkv; h0 += HEADS) {
+            const int nh = min(HEADS, p.Hkv - h0), u = b * p.Hkv + h0;
+            int n[HEADS], row[HEADS];
+            unsigned ok = 0;   // heads that take the token
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h) {
+                n[h] = 0;
+                if (inside && h < nh) {
+                    n[h] = p.n[u + h];
+                    const int pages = p.table ? p.pages_out[u + h] : per;
+                    if (fits(p, n[h], m) && (!p.table || pages * (long)PAGE_SLOTS >= n[h] + m))
+                        ok |= 1u << h;
                 }
             }
-            p.slot_map[(size_t)t * p.Hkv + h] = row;
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h) {
+                row[h] = -1;
+                if (ok >> h & 1)
+                    row[h] = p.table ? p.table_out[(size_t)(u + h) * per + (n[h] + step) / PAGE_SLOTS]
+                                     : (u + h) * p.C + n[h] + step;
+            }
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h) {
+                const int slot = n[h] + step;
+                if (ok >> h & 1) {
+                    p.pos[(size_t)(u + h) * p.C + slot] = P;
+                    if (p.table) {
+                        if (row[h] >= 0 && row[h] < p.num_pages) {
+                            row[h] = row[h] * PAGE_SLOTS + slot % PAGE_SLOTS;
+                        } else {
+                            row[h] = -1;
+                            flag_error(p.status, DEV_CAPACITY);
+                        }
+                    }
+                }
+                if (h < nh)
+                    p.slot_map[(size_t)t * p.Hkv + h0 + h] = row[h];
+            }
         }
     }
     cluster_sync_all();   // the old counts have been read everywhere
@@ -315,13 +374,30 @@ __global__ void __launch_bounds__(256) k_append_packed(const PackedLaunch p)
 
 } // namespace
 
+template <int SPAN> static cudaError_t plan_impl(const PlanLaunch &p, cudaStream_t s)
+{
+    const void *f = reinterpret_cast<const void *>(k_append_plan<SPAN>);
+    cudaError_t e = set_smem_once(f, sizeof(PlanSmem<SPAN>), true);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(CTAS);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = sizeof(PlanSmem<SPAN>);
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = CTAS;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_append_plan<SPAN>, p);
+}
+
 cudaError_t launch_append_plan(const PlanLaunch &p, cudaStream_t s)
 {
-    if ((long)p.B * p.Hkv <= (long)CTAS * THREADS)
-        k_append_plan<1><<<CTAS, THREADS, 0, s>>>(p);
-    else
-        k_append_plan<PLAN_MAX_SPAN><<<CTAS, THREADS, 0, s>>>(p);
-    return cudaGetLastError();
+    return (long)p.B * p.Hkv <= (long)CTAS * THREADS ? plan_impl<1>(p, s)
+                                                     : plan_impl<PLAN_MAX_SPAN>(p, s);
 }
 
 cudaError_t launch_append_packed(const PackedLaunch &p, cudaStream_t s)
