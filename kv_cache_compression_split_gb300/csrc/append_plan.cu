@@ -26,6 +26,9 @@ constexpr int CTAS = 16;       // one cluster
 constexpr int THREADS = 1024;
 constexpr int CU_CACHE = 2048; // sequence starts held in shared memory
 constexpr int HEADS = 8;       // heads of a token whose loads are in flight together
+// Tokens whose slot map the cluster writes itself; more go to a second kernel on all SMs
+// (scattered words: TODO).
+constexpr int CLUSTER_TOKENS = 2048;
 constexpr int PLAN_MAX_SPAN = KVC_PLAN_MAX_UNITS / (CTAS * THREADS);
 
 __device__ __forceinline__ int ld_cluster_s32(const int *local, uint32_t rank)
@@ -129,6 +132,104 @@ __device__ __forceinline__ int last_at_most(const int *v, int n, int x)
     return lo;
 }
 
+// Whether unit u takes its m new tokens, once its pages are granted.
+__device__ __forceinline__ bool takes(const PlanLaunch &p, int u, int n, int m)
+{
+    return fits(p, n, m) && (!p.table || p.pages_out[u] * (long)PAGE_SLOTS >= n + m);
+}
+
+// Row of unit u's slot, once its pages are granted; -1 when its table entry is not a page.
+__device__ __forceinline__ int slot_row(const PlanLaunch &p, int u, int slot)
+{
+    if (!p.table)
+        return u * p.C + slot;
+    const int pg = p.table_out[(size_t)u * (p.C / PAGE_SLOTS) + slot / PAGE_SLOTS];
+    if (pg >= 0 && pg < p.num_pages)
+        return pg * PAGE_SLOTS + slot % PAGE_SLOTS;
+    flag_error(p.status, DEV_CAPACITY);
+    return -1;
+}
+
+// Slot map and positions of token t for every head.  `starts` are the sequences' first
+// tokens (cu, or a copy).  Ranges that run backwards cannot be bisected: then the first
+// sequence that holds the token is looked for one by one.
+// AFTER: the counts are already the new ones, and the first token of each unit is done: its
+// entry says whether the unit takes its tokens.
+template <bool AFTER>
+__device__ __forceinline__ void plan_token(const PlanLaunch &p, int t, const int *starts,
+                                           bool backwards)
+{
+    int b = 0, start = 0, m = 0;
+    if (!backwards) {
+        b = last_at_most(starts, p.B - 1, t);   // of sequences without tokens, the last
+        m = new_tokens(p, b, start);
+    } else {
+        for (; b < p.B; ++b) {
+            m = new_tokens(p, b, start);
+            if (t >= start && t < start + m)
+                break;
+        }
+    }
+    const bool inside = b < p.B && t >= start && t < start + m;
+    const int step = t - start;
+    if (AFTER && inside && step == 0)
+        return;
+    const int P = inside ? (AFTER ? p.seqlen_out[b] - m : p.seqlen[b]) + step : 0;
+    int *map = p.slot_map + (size_t)t * p.Hkv;
+    const int per = p.C / PAGE_SLOTS;
+    for (int h0 = 0; h0 < p.Hkv; h0 += HEADS) {
+        const int nh = min(HEADS, p.Hkv - h0), u = b * p.Hkv + h0;
+        // each step loads for all heads before any value is used
+        int n[HEADS], x[HEADS], row[HEADS];
+#pragma unroll
+        for (int h = 0; h < HEADS; ++h) {
+            const bool here = inside && h < nh;
+            n[h] = here ? (AFTER ? p.n_out : p.n)[u + h] : -1;
+            // what tells whether the unit takes its tokens: its pages, or its first entry
+            x[h] = !here ? -1
+                   : AFTER ? p.slot_map[(size_t)start * p.Hkv + h0 + h]
+                           : p.table ? p.pages_out[u + h] : per;
+        }
+        unsigned ok = 0;   // heads that take the token
+#pragma unroll
+        for (int h = 0; h < HEADS; ++h) {
+            n[h] -= AFTER ? m : 0;
+            const bool room = !p.table || x[h] * (long)PAGE_SLOTS >= n[h] + m;
+            ok |= (unsigned)(fits(p, n[h], m) && (AFTER ? x[h] >= 0 : room)) << h;
+            n[h] += step;   // the token's slot
+        }
+#pragma unroll
+        for (int h = 0; h < HEADS; ++h) {
+            row[h] = -1;
+            if (ok >> h & 1)
+                row[h] = p.table ? p.table_out[(size_t)(u + h) * per + n[h] / PAGE_SLOTS]
+                                 : (u + h) * p.C + n[h];
+        }
+        bool bad = false;
+#pragma unroll
+        for (int h = 0; h < HEADS; ++h) {
+            if (ok >> h & 1)
+                p.pos[(size_t)(u + h) * p.C + n[h]] = P;
+            if (p.table) {
+                const bool page = row[h] >= 0 && row[h] < p.num_pages;
+                bad |= (ok >> h & 1) && !page;
+                row[h] = page ? row[h] * PAGE_SLOTS + n[h] % PAGE_SLOTS : -1;
+            }
+        }
+        if (bad)
+            flag_error(p.status, DEV_CAPACITY);
+        if (nh == HEADS && p.Hkv % 4 == 0 && (reinterpret_cast<uintptr_t>(p.slot_map) & 15) == 0) {
+            *reinterpret_cast<int4 *>(map + h0) = make_int4(row[0], row[1], row[2], row[3]);
+            *reinterpret_cast<int4 *>(map + h0 + 4) = make_int4(row[4], row[5], row[6], row[7]);
+        } else {
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h)
+                if (h < nh)
+                    map[h0 + h] = row[h];
+        }
+    }
+}
+
 // A thread owns SPAN consecutive units, so CTAS * THREADS * SPAN units at most.
 template <int SPAN> struct PlanSmem {
     int cu[CU_CACHE];
@@ -149,6 +250,8 @@ __global__ void __launch_bounds__(THREADS) k_append_plan(const PlanLaunch p)
     const int per = p.C / PAGE_SLOTS;
     const int u0 = gtid * SPAN, cta_u0 = rank * THREADS * SPAN;
     int left = 0, n_back = 0;      // pages left on the stack, pages given back
+
+    asm volatile("griddepcontrol.launch_dependents;");
 
     bool backwards = false;
     for (int b = tid; b < p.B; b += THREADS) {
@@ -201,14 +304,13 @@ __global__ void __launch_bounds__(THREADS) k_append_plan(const PlanLaunch p)
             sm.back[THREADS * SPAN] = ty;
         }
         cluster_sync_all();
-        int total = 0, before = 0, back0 = 0;   // before this CTA's first unit
-        for (int r = 0; r < CTAS; ++r) {
-            const int a = ld_cluster_s32(&s_sum[0], r), k = ld_cluster_s32(&s_sum[1], r);
-            before += r < rank ? a : 0;
-            back0 += r < rank ? k : 0;
-            total += a;
-            n_back += k;
-        }
+        // pages asked for and given back in all, and before this CTA's first unit
+        const int r_ask = lane < CTAS ? ld_cluster_s32(&s_sum[0], lane) : 0;
+        const int r_back = lane < CTAS ? ld_cluster_s32(&s_sum[1], lane) : 0;
+        const int total = __reduce_add_sync(0xffffffffu, r_ask);
+        const int before = __reduce_add_sync(0xffffffffu, lane < rank ? r_ask : 0);
+        const int back0 = __reduce_add_sync(0xffffffffu, lane < rank ? r_back : 0);
+        n_back = __reduce_add_sync(0xffffffffu, r_back);
         // ---- grants: a unit that the stack cannot serve in full keeps what it has.  Units
         // are served in order, so those served are the ones up to some unit and those that
         // ask for nothing.
@@ -231,9 +333,8 @@ __global__ void __launch_bounds__(THREADS) k_append_plan(const PlanLaunch p)
             if (lane == 0)
                 atomicAdd(&s_sum[2], granted);
             cluster_sync_all();
-            taken = 0;
-            for (int r = 0; r < CTAS; ++r)
-                taken += ld_cluster_s32(&s_sum[2], r);
+            taken = __reduce_add_sync(0xffffffffu,
+                                      lane < CTAS ? ld_cluster_s32(&s_sum[2], lane) : 0);
             mine = s_sum[2];
         }
         left = count - taken;
@@ -266,63 +367,25 @@ __global__ void __launch_bounds__(THREADS) k_append_plan(const PlanLaunch p)
         }
     }
 
-    // ---- slot map and positions: a thread per token.  Ranges that run backwards cannot be
-    // bisected: then the first sequence that holds the token is looked for one by one.
+    // ---- slot map and positions
     backwards = __syncthreads_or(backwards);
-    const int *starts = p.B <= CU_CACHE ? sm.cu : p.cu;
-    for (int t = gtid; t < p.T; t += gsize) {
-        int b = 0, start = 0, m = 0;
-        if (!backwards) {
-            b = last_at_most(starts, p.B - 1, t);   // of sequences without tokens, the last
-            m = new_tokens(p, b, start);
-        } else {
-            for (; b < p.B; ++b) {
-                m = new_tokens(p, b, start);
-                if (t >= start && t < start + m)
-                    break;
+    if (p.T <= CLUSTER_TOKENS) {
+        // a thread per token, warps dealt to the CTAs in turn
+        for (int t = ((tid >> 5) * CTAS + rank) * 32 + lane; t < p.T; t += gsize)
+            plan_token<false>(p, t, p.B <= CU_CACHE ? sm.cu : p.cu, backwards);
+    } else {
+        // the first token of each unit; k_plan_tokens follows with the others
+        for (int u = gtid; u < units; u += gsize) {
+            int start;
+            const int b = u / p.Hkv, m = new_tokens(p, b, start), n = p.n[u];
+            if (m == 0)
+                continue;
+            int row = -1;
+            if (takes(p, u, n, m)) {
+                row = slot_row(p, u, n);
+                p.pos[(size_t)u * p.C + n] = p.seqlen[b];
             }
-        }
-        const bool inside = b < p.B && t >= start && t < start + m;
-        const int step = t - start;
-        const int P = inside ? p.seqlen[b] + step : 0;
-        for (int h0 = 0; h0 < p.Hkv; h0 += HEADS) {
-            const int nh = min(HEADS, p.Hkv - h0), u = b * p.Hkv + h0;
-            int n[HEADS], row[HEADS];
-            unsigned ok = 0;   // heads that take the token
-#pragma unroll
-            for (int h = 0; h < HEADS; ++h) {
-                n[h] = 0;
-                if (inside && h < nh) {
-                    n[h] = p.n[u + h];
-                    const int pages = p.table ? p.pages_out[u + h] : per;
-                    if (fits(p, n[h], m) && (!p.table || pages * (long)PAGE_SLOTS >= n[h] + m))
-                        ok |= 1u << h;
-                }
-            }
-#pragma unroll
-            for (int h = 0; h < HEADS; ++h) {
-                row[h] = -1;
-                if (ok >> h & 1)
-                    row[h] = p.table ? p.table_out[(size_t)(u + h) * per + (n[h] + step) / PAGE_SLOTS]
-                                     : (u + h) * p.C + n[h] + step;
-            }
-#pragma unroll
-            for (int h = 0; h < HEADS; ++h) {
-                const int slot = n[h] + step;
-                if (ok >> h & 1) {
-                    p.pos[(size_t)(u + h) * p.C + slot] = P;
-                    if (p.table) {
-                        if (row[h] >= 0 && row[h] < p.num_pages) {
-                            row[h] = row[h] * PAGE_SLOTS + slot % PAGE_SLOTS;
-                        } else {
-                            row[h] = -1;
-                            flag_error(p.status, DEV_CAPACITY);
-                        }
-                    }
-                }
-                if (h < nh)
-                    p.slot_map[(size_t)t * p.Hkv + h0 + h] = row[h];
-            }
+            p.slot_map[(size_t)start * p.Hkv + u - b * p.Hkv] = row;
         }
     }
     cluster_sync_all();   // the old counts have been read everywhere
@@ -331,9 +394,7 @@ __global__ void __launch_bounds__(THREADS) k_append_plan(const PlanLaunch p)
     for (int u = gtid; u < units; u += gsize) {
         int st;
         const int m = new_tokens(p, u / p.Hkv, st), n = p.n[u];
-        const bool ok =
-            fits(p, n, m) && (!p.table || p.pages_out[u] * (long)PAGE_SLOTS >= n + m);
-        p.n_out[u] = ok ? n + m : n;
+        p.n_out[u] = takes(p, u, n, m) ? n + m : n;
     }
     for (int b = gtid; b < p.B; b += gsize) {
         int st;
@@ -345,6 +406,25 @@ __global__ void __launch_bounds__(THREADS) k_append_plan(const PlanLaunch p)
     }
     if (p.table && gtid == 0)
         *p.count_out = min(left + n_back, p.num_pages);
+}
+
+// The other tokens of a large batch, a thread per token.  Launched so that its CTAs may
+// start while the plan still runs: they wait for it before they read what it wrote.
+__global__ void __launch_bounds__(256) k_plan_tokens(const PlanLaunch p)
+{
+    __shared__ int s_cu[CU_CACHE];
+    bool backwards = false;
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+        const int c0 = p.cu[b], c1 = p.cu[b + 1];
+        backwards |= c1 < c0;
+        if (b < CU_CACHE)
+            s_cu[b] = c0;
+    }
+    backwards = __syncthreads_or(backwards);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int t = blockIdx.x * blockDim.x + threadIdx.x;
+    if (t < p.T)
+        plan_token<true>(p, t, p.B <= CU_CACHE ? s_cu : p.cu, backwards);
 }
 
 // Rows of the packed new tokens to the cache.  Each thread copies 16 bytes of K and
@@ -391,7 +471,15 @@ template <int SPAN> static cudaError_t plan_impl(const PlanLaunch &p, cudaStream
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_append_plan<SPAN>, p);
+    e = cudaLaunchKernelEx(&cfg, k_append_plan<SPAN>, p);
+    if (e != cudaSuccess || p.T <= CLUSTER_TOKENS)
+        return e;
+    cfg.gridDim = dim3((p.T + 255) / 256);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    return cudaLaunchKernelEx(&cfg, k_plan_tokens, p);
 }
 
 cudaError_t launch_append_plan(const PlanLaunch &p, cudaStream_t s)

@@ -76,7 +76,10 @@ CASES = [
     (5, 8, 2048, 700, 0, 600, False),
     (16, 4, 256, 256, 1, 20, True),       # the stack runs out: later growing units are refused
     (4, 2, 256, 200, 0, 0, False),        # nothing to give
-    (300, 32, 192, 2, 1, 5000, True),     # 9600 units: more than one per thread
+    (300, 32, 192, 2, 1, 5000, True),     # thousands of units
+    (700, 30, 128, 4, 1, 9000, True),     # 21000 units: more than one per thread
+    (40, 9, 640, 500, 1, 900, True),      # thousands of tokens, nine heads, the stack runs out
+    (3, 2, 8192, 4000, 2, 400, False),    # a few long prompts
 ]
 
 
