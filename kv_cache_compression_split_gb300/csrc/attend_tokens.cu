@@ -10,15 +10,18 @@
 // lse = -inf.
 //
 // Rows.  A tile is 128 rows of tcgen05.mma's M: (token, head of the group) pairs,
-// token-major, so the query heads of one KV head share every key they read.  A work
-// item is two tiles of one (sequence, KV head): two consecutive token ranges, or,
-// when its tokens fit one tile, the same rows twice with the 128-key blocks dealt out
-// alternately.  Either way two independent softmax chains run per SM, and the tensor
-// cores work on one while the other's scores become probabilities.
+// token-major, so the query heads of one KV head share every key they read.  Two forms:
+//   TILES = 2  one CTA per SM, a work item is two tiles of one (sequence, KV head): two
+//              consecutive token ranges that share the K and V blocks, or, when its
+//              tokens fit one tile, the same rows twice with the 128-key blocks dealt
+//              out alternately.  Two independent softmax chains run per SM, and the
+//              tensor cores work on one while the other's scores become probabilities.
+//   TILES = 1  two CTAs per SM, one tile each: batches whose sequences bring few tokens,
+//              where an item is a few key blocks and most of its time is latency.
 //
-// Pipeline, one CTA per SM.  The grid has a CTA per item; one that runs takes over the
-// items of CTAs that have not started (cluster launch control), so work is balanced
-// without a counter in memory and its pipeline never drains.  A producer warp (TMA: query
+// Pipeline.  The grid has a CTA per item; one that runs takes over the items of CTAs that
+// have not started (cluster launch control), so work is balanced without a counter in
+// memory and the pipeline does not drain between items.  A producer warp (TMA: query
 // tiles, and K and V blocks through a ring), an MMA warp, and a warpgroup per tile in
 // which a thread owns a row.  S = Q K^T (128 x 128, fp32) lands in TMEM; the row's
 // thread reads it, keeps the running reference m and sum l in registers, and writes
@@ -27,7 +30,9 @@
 // back to back, so when S_t(j + 1) is complete O_t is at rest and its rows may be
 // rescaled by their threads.  They rarely are: the reference follows the maximum only
 // when that has grown by 2^8 (probabilities then stay below 2^8, far inside binary16
-// and with the same relative rounding, 2^-11, as below 1).
+// and with the same relative rounding, 2^-11, as below 1).  Results leave through a
+// small area of shared memory per warp, so that a warp stores whole rows: a thread that
+// stores its own row touches 32 lines per instruction, which took 7000 clocks a tile.
 //
 // Non-finite values.  A masked score is replaced, not added to, so keys behind a
 // row's range never matter.  A masked value row would enter as 0 * v: rows behind the
@@ -46,27 +51,39 @@ namespace {
 constexpr int TM = 128;                   // rows of a tile
 constexpr int TK = 128;                   // keys of a block
 constexpr int HALF = TK / 2;              // keys of one TMA box (a page of the cache)
-constexpr int NTHR = 384;                 // two softmax warpgroups; producer and MMA warp
-constexpr int W_TMA = 8, W_MMA = 9;       // warps 10 and 11 only fill their warpgroup
-// Registers: 384 threads are launched with 168 each, 64,512 in all.  A row's thread holds
-// its 128 scores and needs more; the third warpgroup gives what it does not use.
-constexpr int REGS_ROW = 208, REGS_IO = 88;
-static_assert(2 * 128 * REGS_ROW + 128 * REGS_IO <= NTHR * 168, "register split");
 constexpr int NI = 2;                     // slots of the item feed
-constexpr int TMEM_COLS = 512;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float GROWTH = 8.f;             // log2 growth of the maximum that moves the reference
 
-template <int D> struct TokCfg {
+template <int D, int TILES> struct TokCfg {
+    static constexpr int W_TMA = 4 * TILES, W_MMA = W_TMA + 1;   // two more warps are idle
+    static constexpr int NTHR = 128 * (TILES + 1);
+    static constexpr int CTAS = 3 - TILES;                 // per SM
     static constexpr int NBOX = D / 64;
     static constexpr int BOX_BYTES = TM * 128;
     static constexpr int TILE_BYTES = NBOX * BOX_BYTES;
-    static constexpr int NS = D == 128 ? 5 : 10;           // ring stages (one K or V block each)
+    // ring stages (one K or V block each)
+    static constexpr int NS = (D == 128 ? 4 : 8) / (3 - TILES);
+    // output area of a row warp: buffers of 32 rows of 64 bytes
+    static constexpr int OUT_BUF = 32 * 64, OUT_BUFS = TILES;
+    static constexpr int OUT_BYTES = OUT_BUFS * OUT_BUF;
     static constexpr int ML_BYTES = TM * 8;
-    static constexpr int SMEM = (2 + NS) * TILE_BYTES + ML_BYTES + 1024 + 1024;
+    static constexpr int SMEM = (TILES + NS) * TILE_BYTES + 4 * TILES * OUT_BYTES + ML_BYTES + 1024 + 1024;
     static constexpr uint32_t IDESC_QK = idesc_f16_f32(TM, TK);
     static constexpr uint32_t IDESC_PV = idesc_f16_f32_bmn(TM, D);
-    static constexpr uint32_t COL_O = 2 * TK;              // TMEM: S_0, S_1, O_0, O_1
+    static constexpr uint32_t COL_O = TILES * TK;          // TMEM: S_t, then O_t
+    static constexpr uint32_t TMEM_COLS = 256 * TILES;
+    // Registers.  384 threads are launched with 168 each, 256 (two CTAs per SM) with 128.
+    // A row's thread holds its 128 scores and needs more; the last warpgroup gives what it
+    // does not use.
+    static constexpr int REGS = TILES == 2 ? 168 : 128;
+    static constexpr int REGS_ROW = TILES == 2 ? 208 : 168, REGS_IO = 88;
+    static_assert(128 * (TILES * REGS_ROW + REGS_IO) <= NTHR * REGS, "register split");
+    static_assert(CTAS * SMEM <= 227 * 1024 + (CTAS - 1) * 1024, "shared memory");
+};
+
+template <int N> struct Int {
+    static constexpr int value = N;
 };
 
 struct TokItem {
@@ -80,7 +97,7 @@ struct TokItem {
 };
 
 struct TokMaps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, o;
 };
 
 // First token and length of sequence b; a range that leaves [0, L] counts as an
@@ -101,7 +118,8 @@ __device__ __forceinline__ void seq_range(const TokensLaunch &p, int b, int &sta
 struct ItemWalk {
     int b0 = 0;
     long base = 0;
-    __device__ bool find(const TokensLaunch &p, int tpt, long idx, TokItem &it)
+    // tiles: per item
+    __device__ bool find(const TokensLaunch &p, int tpt, int tiles, long idx, TokItem &it)
     {
         const int lane = threadIdx.x & 31;
         if (idx < base) {
@@ -112,7 +130,7 @@ struct ItemWalk {
             int s = 0, n = 0;
             if (b0 + lane < p.B)
                 seq_range(p, b0 + lane, s, n);
-            const int ranges = (n + 2 * tpt - 1) / (2 * tpt);
+            const int ranges = (n + tiles * tpt - 1) / (tiles * tpt);
             const long mine = (long)ranges * p.Hkv * p.splits;
             long sum = mine;
 #pragma unroll
@@ -135,9 +153,9 @@ struct ItemWalk {
             it.split = r % p.splits;
             const int q = r / p.splits;
             it.hk = q % p.Hkv;
-            it.tok0 = (per - 1 - q / p.Hkv) * 2 * tpt;
-            it.ntok = min(2 * tpt, len - it.tok0);
-            it.two = it.ntok <= tpt;
+            it.tok0 = (per - 1 - q / p.Hkv) * tiles * tpt;
+            it.ntok = min(tiles * tpt, len - it.tok0);
+            it.two = tiles == 2 && it.ntok <= tpt;
             int n_keys = len;
             if (p.n) {
                 n_keys = p.n[it.b * p.Hkv + it.hk];
@@ -184,6 +202,54 @@ __device__ __forceinline__ const uint16_t *key_row(const TokensLaunch &p, const 
     return row < 0 ? nullptr : base + row * p.D;
 }
 
+// Scores behind the row's range (column > lim) become -inf.
+__device__ __forceinline__ void mask64(float (&x)[64], int lim)
+{
+#pragma unroll
+    for (int c = 0; c < 64; ++c)
+        x[c] = c <= lim ? x[c] : -INFINITY;
+}
+
+__device__ __forceinline__ float max64(const float (&x)[64])
+{
+    float c0 = fmax3f(x[0], x[1], x[2]), c1 = fmax3f(x[16], x[17], x[18]);
+    float c2 = fmax3f(x[32], x[33], x[34]), c3 = fmax3f(x[48], x[49], x[50]);
+#pragma unroll
+    for (int c = 3; c < 15; c += 2) {
+        c0 = fmax3f(c0, x[c], x[c + 1]);
+        c1 = fmax3f(c1, x[16 + c], x[17 + c]);
+        c2 = fmax3f(c2, x[32 + c], x[33 + c]);
+        c3 = fmax3f(c3, x[48 + c], x[49 + c]);
+    }
+    return fmaxf(fmax3f(c0, c1, x[15]), fmax3f(c2, c3, fmax3f(x[31], x[47], x[63])));
+}
+
+// Probabilities 2^(x scale - ref) of 64 scores into TMEM (two per column, binary16: they
+// are an operand of the second product), and their sum before that rounding.
+__device__ __forceinline__ float prob64(uint32_t taddr, const float (&x)[64], float2 scale,
+                                        float2 nref)
+{
+    float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+#pragma unroll
+    for (int c = 0; c < 64; c += 32) {
+        uint32_t w[16];
+#pragma unroll
+        for (int u = 0; u < 16; u += 2) {
+            const float2 y0 = ffma2(make_float2(x[c + 2 * u], x[c + 2 * u + 1]), scale, nref);
+            const float2 y1 = ffma2(make_float2(x[c + 2 * u + 2], x[c + 2 * u + 3]), scale, nref);
+            const float2 e0 = make_float2(ex2(y0.x), ex2(y0.y));
+            const float2 e1 = make_float2(ex2(y1.x), ex2(y1.y));
+            a0 = fadd2(a0, e0);
+            a1 = fadd2(a1, e1);
+            w[u] = pack_half2(e0.x, e0.y);
+            w[u + 1] = pack_half2(e1.x, e1.y);
+        }
+        tmem_st16(taddr + c / 2, w);
+    }
+    const float2 a = fadd2(a0, a1);
+    return a.x + a.y;
+}
+
 // The 32 channels from c0 of one row, from memory, over the keys [first, last]: for a
 // row whose tensor-core result is not finite although its sum l is.
 __device__ __noinline__ void row_again(const TokensLaunch &p, const TokItem &it, const uint16_t *q,
@@ -215,24 +281,25 @@ __device__ __noinline__ void row_again(const TokensLaunch &p, const TokItem &it,
     }
 }
 
-template <int D>
-__global__ void __launch_bounds__(NTHR, 1)
+template <int D, int TILES>
+__global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS)
     k_attend_tokens(const __grid_constant__ TokMaps maps, const __grid_constant__ TokensLaunch p)
 {
-    using Cfg = TokCfg<D>;
-    constexpr int NS = Cfg::NS;
+    using Cfg = TokCfg<D, TILES>;
+    constexpr int NS = Cfg::NS, W_TMA = Cfg::W_TMA, W_MMA = Cfg::W_MMA;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_align1024(smem_raw);
-    uint8_t *sq = smem;                                      // two query tiles
-    uint8_t *ring = smem + 2 * Cfg::TILE_BYTES;              // NS blocks of K or V
-    float2 *s_ml = reinterpret_cast<float2 *>(ring + NS * Cfg::TILE_BYTES);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + NS * Cfg::TILE_BYTES + Cfg::ML_BYTES);
+    uint8_t *sq = smem;                                      // query tiles
+    uint8_t *ring = sq + TILES * Cfg::TILE_BYTES;            // NS blocks of K or V
+    uint8_t *s_out = ring + NS * Cfg::TILE_BYTES;            // an output area per row warp
+    float2 *s_ml = reinterpret_cast<float2 *>(s_out + 4 * TILES * Cfg::OUT_BYTES);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(s_ml) + TM;
     uint64_t *kv_full = bars, *kv_empty = kv_full + NS;
     uint64_t *q_full = kv_empty + NS, *q_empty = q_full + 1;
     uint64_t *s_full = q_empty + 1, *p_full = s_full + 2, *o_full = p_full + 2;
     uint64_t *it_full = o_full + 2, *it_empty = it_full + NI;
     uint64_t *mrg_full = it_empty + NI, *mrg_empty = mrg_full + 4;
-    uint64_t *mrg_done = mrg_empty + 4, *mma_done = mrg_done + 1;
+    uint64_t *mma_done = mrg_empty + 4;
     uint64_t *clc_full = mma_done + 1;
     uint4 *clc = reinterpret_cast<uint4 *>(bars + 64);       // a 16-byte answer
     TokItem *s_item = reinterpret_cast<TokItem *>(clc + 1);
@@ -250,26 +317,25 @@ __global__ void __launch_bounds__(NTHR, 1)
         }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < TILES; ++t) {
             mbar_init(&s_full[t], 1);
             mbar_init(&p_full[t], 4);
             mbar_init(&o_full[t], 1);
         }
         for (int i = 0; i < NI; ++i) {
             mbar_init(&it_full[i], 1);
-            mbar_init(&it_empty[i], 9);   // the MMA warp and eight softmax warps
+            mbar_init(&it_empty[i], 1 + 4 * TILES);   // the MMA warp and the row warps
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&mrg_full[i], 1);
             mbar_init(&mrg_empty[i], 1);
         }
-        mbar_init(mrg_done, 4);
         mbar_init(mma_done, 1);
         mbar_init(clc_full, 1);
         fence_mbar_init();
     }
     if (warp == W_MMA) {
-        tmem_alloc(s_tmem, TMEM_COLS);
+        tmem_alloc(s_tmem, Cfg::TMEM_COLS);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -290,17 +356,18 @@ __global__ void __launch_bounds__(NTHR, 1)
     };
 
     if (warp >= W_TMA) {
-    regs_dec<REGS_IO>();
+    regs_dec<Cfg::REGS_IO>();
     if (warp == W_TMA) {
         // ------------------------------------------------ producer
         if (lane == 0) {
             prefetch_tmap(&maps.q);
             prefetch_tmap(&maps.k);
             prefetch_tmap(&maps.v);
+            prefetch_tmap(&maps.o);
         }
         ItemWalk walk;
         long idx = blockIdx.x;
-        int n_it = 0, n_q = 0, n_two = 0, seen_two = 0;   // ring slots, query loads, merges
+        int n_it = 0, n_q = 0;   // ring slots and query loads
         bool ok = true;
         int n_clc = 0;
         for (int k = 0; ok; ++n_clc) {
@@ -310,7 +377,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                 // the next item while this one runs: take over a CTA that has not started
                 if (lane == 0)
                     clc_request(clc, clc_full);
-                if (!walk.find(p, tpt, idx, it))
+                if (!walk.find(p, tpt, TILES, idx, it))
                     it.j0 = it.j1 = it.two = 0;   // the grid is an upper bound
             }
             if (idx < 0 || it.b >= 0) {
@@ -328,8 +395,6 @@ __global__ void __launch_bounds__(NTHR, 1)
                     break;
             }
             const int n = it.j1 - it.j0;
-            if (it.two)
-                ++n_two;
             const int unit = it.b * p.Hkv + it.hk;
             const int per = p.C / PAGE_SLOTS;
             if (p.block_table)   // the item's part of the page table into L1
@@ -337,22 +402,6 @@ __global__ void __launch_bounds__(NTHR, 1)
                     asm volatile("prefetch.global.L1 [%0];" ::"l"(p.block_table +
                                                                   (size_t)unit * per + i));
             if (lane == 0 && n > 0) {
-                if (n_q > 0)
-                    ok = mbar_sleep_or_abort(q_empty, (n_q - 1) & 1, abort);
-                // a merge of the item before used the second query tile
-                const int done = n_two - (it.two ? 1 : 0);
-                for (; ok && seen_two < done; ++seen_two)
-                    ok = mbar_sleep_or_abort(mrg_done, seen_two & 1, abort);
-                if (ok) {
-                    const int tiles = it.two ? 1 : 2;
-                    mbar_arrive_expect_tx(q_full, tiles * Cfg::NBOX * tpt * g * 128);
-                    for (int t = 0; t < tiles; ++t)
-                        for (int c = 0; c < Cfg::NBOX; ++c)
-                            tma_load_4d(sq + t * Cfg::TILE_BYTES + c * Cfg::BOX_BYTES, &maps.q,
-                                        q_full, 64 * c, it.hk * g, it.start + it.tok0 + t * tpt,
-                                        p.cu ? 0 : it.b);
-                    ++n_q;
-                }
                 const int n_keys = p.n ? it.shift + (p.cu ? p.cu[it.b + 1] - p.cu[it.b] : 0) : 0;
                 auto load = [&](const CUtensorMap *map, int j) {
                     const int st = n_it % NS;
@@ -392,12 +441,29 @@ __global__ void __launch_bounds__(NTHR, 1)
                     }
                     ++n_it;
                 };
-                // the order in which the MMA warp takes them
+                // The order in which the MMA warp takes them.  The first blocks go ahead of
+                // the query tile, whose place is free only when the last item's scores are
+                // done.
                 const int ahead = it.two ? 2 : 1;
                 for (int i = 0; ok && i < ahead && i < n; ++i)
                     load(&maps.k, it.j0 + i);
+                if (ok)
+                    load(&maps.v, it.j0);
+                if (ok && n_q > 0)
+                    ok = mbar_sleep_or_abort(q_empty, (n_q - 1) & 1, abort);
+                if (ok) {
+                    const int tiles = it.ntok > tpt ? 2 : 1;
+                    mbar_arrive_expect_tx(q_full, tiles * Cfg::NBOX * tpt * g * 128);
+                    for (int t = 0; t < tiles; ++t)
+                        for (int c = 0; c < Cfg::NBOX; ++c)
+                            tma_load_4d(sq + t * Cfg::TILE_BYTES + c * Cfg::BOX_BYTES, &maps.q,
+                                        q_full, 64 * c, it.hk * g, it.start + it.tok0 + t * tpt,
+                                        p.cu ? 0 : it.b);
+                    ++n_q;
+                }
                 for (int i = 0; ok && i < n; ++i) {
-                    load(&maps.v, it.j0 + i);
+                    if (i > 0)
+                        load(&maps.v, it.j0 + i);
                     if (ok && i + ahead < n)
                         load(&maps.k, it.j0 + i + ahead);
                 }
@@ -424,6 +490,8 @@ __global__ void __launch_bounds__(NTHR, 1)
         // ------------------------------------------------ MMA issuer (lane 0 issues)
         int n_it = 0, n_q = 0;
         int n_p[2] = {0, 0};
+        const Int<0> T0;
+        const Int<TILES - 1> T1;
         bool ok = true;
         TokItem it;
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -434,7 +502,9 @@ __global__ void __launch_bounds__(NTHR, 1)
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             ok = ok && __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, abort));
         };
-        auto qk = [&](int t, int tile, int st) {   // S_t = Q_tile K^T, K in ring stage st
+        // t as a type: its TMEM columns and barrier are constants then
+        auto qk = [&](auto t_, int tile, int st) {   // S_t = Q_tile K^T, K in ring stage st
+            constexpr int t = decltype(t_)::value;
             const uint64_t qd = q_desc + tile * (Cfg::TILE_BYTES >> 4);
             const uint64_t kd = k_desc + (uint32_t)st * (Cfg::TILE_BYTES >> 4);
             if (elect_one()) {
@@ -447,7 +517,8 @@ __global__ void __launch_bounds__(NTHR, 1)
             }
             __syncwarp();
         };
-        auto pv = [&](int t, int st, int keys, bool first) {   // O_t (+)= P_t V
+        auto pv = [&](auto t_, int st, int keys, bool first) {   // O_t (+)= P_t V
+            constexpr int t = decltype(t_)::value;
             const uint64_t vd = v_desc + (uint32_t)st * (Cfg::TILE_BYTES >> 4);
             const uint32_t od = tm + Cfg::COL_O + D * t, pd = tm + TK * t;
             const uint32_t acc = first ? 0u : 1u;
@@ -482,7 +553,7 @@ __global__ void __launch_bounds__(NTHR, 1)
             const int n = it.j1 - it.j0;
             if (n <= 0)
                 continue;
-            const TileRange r0(it, 0, tpt), r1(it, 1, tpt);
+            const TileRange r0(it, 0, tpt), r1(it, TILES - 1, tpt);
             const int ahead = it.two ? 2 : 1;
             wait(q_full, n_q & 1);
             ++n_q;
@@ -493,12 +564,15 @@ __global__ void __launch_bounds__(NTHR, 1)
                     break;
                 tc_fence_after();
                 const int kb = n_it % NS;
-                if (it.two) {
-                    qk(i, 0, kb);
+                if (TILES == 1 || it.two) {
+                    if (i == 0)
+                        qk(T0, 0, kb);
+                    else
+                        qk(T1, 0, kb);
                 } else {
                     if (r0.count > 0)
-                        qk(0, 0, kb);
-                    qk(1, 1, kb);
+                        qk(T0, 0, kb);
+                    qk(T1, 1, kb);
                 }
                 commit(&kv_empty[n_it % NS]);
             }
@@ -524,27 +598,33 @@ __global__ void __launch_bounds__(NTHR, 1)
                     fence_async_smem();
                     __syncwarp();
                 }
-                if (it.two) {
-                    const int t = i & 1;
-                    wait(&p_full[t], n_p[t] & 1);
-                    if (!ok)
-                        break;
-                    ++n_p[t];
-                    tc_fence_after();
-                    pv(t, vb, keys, i < 2);
-                    commit(&kv_empty[vs % NS]);
-                    if (ks >= 0) {
-                        wait(&kv_full[ks % NS], (ks / NS) & 1);
+                if (TILES == 1 || it.two) {
+                    auto one = [&](auto t) {
+                        constexpr int T = decltype(t)::value;
+                        wait(&p_full[T], n_p[T] & 1);
                         if (!ok)
-                            break;
+                            return;
+                        ++n_p[T];
                         tc_fence_after();
-                        qk(t, 0, ks % NS);
-                        commit(&kv_empty[ks % NS]);
-                        if (i + ahead == n - 1)
-                            commit(q_empty);
-                    } else {
-                        commit(&o_full[t]);
-                    }
+                        pv(t, vb, keys, i < ahead);
+                        commit(&kv_empty[vs % NS]);
+                        if (ks >= 0) {
+                            wait(&kv_full[ks % NS], (ks / NS) & 1);
+                            if (!ok)
+                                return;
+                            tc_fence_after();
+                            qk(t, 0, ks % NS);
+                            commit(&kv_empty[ks % NS]);
+                            if (i + ahead == n - 1)
+                                commit(q_empty);
+                        } else {
+                            commit(&o_full[T]);
+                        }
+                    };
+                    if (TILES == 1 || !(i & 1))
+                        one(T0);
+                    else
+                        one(T1);
                     continue;
                 }
                 if (i < r0.count) {
@@ -553,13 +633,13 @@ __global__ void __launch_bounds__(NTHR, 1)
                         break;
                     ++n_p[0];
                     tc_fence_after();
-                    pv(0, vb, min(TK, r0.end - j * TK), i == 0);
+                    pv(T0, vb, min(TK, r0.end - j * TK), i == 0);
                     if (i + 1 < r0.count) {
                         wait(&kv_full[ks % NS], (ks / NS) & 1);
                         if (!ok)
                             break;
                         tc_fence_after();
-                        qk(0, 0, ks % NS);
+                        qk(T0, 0, ks % NS);
                     } else {
                         commit(&o_full[0]);
                     }
@@ -569,14 +649,14 @@ __global__ void __launch_bounds__(NTHR, 1)
                     break;
                 ++n_p[1];
                 tc_fence_after();
-                pv(1, vb, keys, i == 0);
+                pv(T1, vb, keys, i == 0);
                 commit(&kv_empty[vs % NS]);
                 if (ks >= 0) {
                     wait(&kv_full[ks % NS], (ks / NS) & 1);
                     if (!ok)
                         break;
                     tc_fence_after();
-                    qk(1, 1, ks % NS);
+                    qk(T1, 1, ks % NS);
                     commit(&kv_empty[ks % NS]);
                     if (i + 2 == n)
                         commit(q_empty);
@@ -592,22 +672,24 @@ __global__ void __launch_bounds__(NTHR, 1)
     }
     } else {
         // ------------------------------------------------ softmax: a thread per row
-        regs_inc<REGS_ROW>();
+        regs_inc<Cfg::REGS_ROW>();
         const int t = warp >> 2, quarter = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t s_col = lanes + TK * t, o_col = lanes + Cfg::COL_O + D * t;
         const int r = 32 * quarter + lane;
         const int r_tok = r / g, r_head = r - r_tok * g;
+        const int w_tok = 32 * quarter / g;   // token of the warp's first row
         const float scale = p.scale_log2;
-        int n_s = 0, n_o = 0, n_m = 0;   // phases of s_full, o_full and the merge barriers
+        int n_s = 0, n_o = 0, n_m = 0;   // phases of s_full, o_full and the hand-over
         bool ok = true;
         TokItem it;
         for (int k = 0; ok && feed_get(k, it); ++k) {
             const TileRange rg(it, t, tpt);
             const bool real = r_tok < min(rg.ntok, tpt);
             const int last = real ? it.shift + rg.tok + r_tok : -1;
-            const bool idle = (32 * quarter) / g >= rg.ntok;      // no row of the warp is real
-            const int first_last = it.shift + rg.tok + (32 * quarter) / g;
+            const bool idle = w_tok >= rg.ntok;                   // no row of the warp is real
+            const bool full = 32 % g == 0 && w_tok + 32 / g <= rg.ntok;
+            const int first_last = it.shift + rg.tok + w_tok;
             float m = -INFINITY, l = 0.f;
             for (int i = 0; i < rg.count; ++i) {
                 const int k0 = (rg.j + i * rg.step) * TK;
@@ -622,26 +704,20 @@ __global__ void __launch_bounds__(NTHR, 1)
                     continue;
                 }
                 tc_fence_after();
-                float x[TK];
-                tmem_ld64(s_col, reinterpret_cast<float(&)[64]>(x[0]));
-                tmem_ld64(s_col + 64, reinterpret_cast<float(&)[64]>(x[64]));
-                if (k0 + TK - 1 > first_last) {   // the block ends behind some row's range
-                    const int lim = last - k0;
-#pragma unroll
-                    for (int c = 0; c < TK; ++c)
-                        x[c] = c <= lim ? x[c] : -INFINITY;
-                }
-                float c0 = fmax3f(x[0], x[1], x[2]), c1 = fmax3f(x[32], x[33], x[34]);
-                float c2 = fmax3f(x[64], x[65], x[66]), c3 = fmax3f(x[96], x[97], x[98]);
-#pragma unroll
-                for (int c = 3; c < 31; c += 2) {
-                    c0 = fmax3f(c0, x[c], x[c + 1]);
-                    c1 = fmax3f(c1, x[32 + c], x[33 + c]);
-                    c2 = fmax3f(c2, x[64 + c], x[65 + c]);
-                    c3 = fmax3f(c3, x[96 + c], x[97 + c]);
-                }
-                const float mx = scale * fmaxf(fmax3f(c0, c1, x[31]),
-                                               fmax3f(c2, c3, fmax3f(x[63], x[95], x[127])));
+                // The upper half of the scores first: with one tile per CTA (fewer registers)
+                // it is read for the maximum and again for the probabilities, whose lower
+                // half lands on columns that are done with by then.
+                float hi[HALF], lo[HALF];
+                const int lim = last - k0;
+                const bool cut = k0 + TK - 1 > first_last;   // ends behind some row's range
+                tmem_ld64(s_col + HALF, hi);
+                if (cut)
+                    mask64(hi, lim - HALF);
+                const float top = max64(hi);
+                tmem_ld64(s_col, lo);
+                if (cut)
+                    mask64(lo, lim);
+                const float mx = scale * fmaxf(top, max64(lo));
                 const bool grow = mx > m + GROWTH;
                 if (__any_sync(0xffffffffu, grow)) {
                     const float f = grow ? ex2(m - mx) : 1.f;   // 0 at the row's first key
@@ -662,27 +738,14 @@ __global__ void __launch_bounds__(NTHR, 1)
                 }
                 const float ref = m == -INFINITY ? 0.f : m;
                 const float2 sc2 = make_float2(scale, scale), nr2 = make_float2(-ref, -ref);
-                float2 a0 = make_float2(0.f, 0.f), a1 = a0;
-#pragma unroll
-                for (int c = 0; c < TK; c += 32) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int u = 0; u < 16; u += 2) {
-                        const float2 y0 =
-                            ffma2(make_float2(x[c + 2 * u], x[c + 2 * u + 1]), sc2, nr2);
-                        const float2 y1 =
-                            ffma2(make_float2(x[c + 2 * u + 2], x[c + 2 * u + 3]), sc2, nr2);
-                        const float2 e0 = make_float2(ex2(y0.x), ex2(y0.y));
-                        const float2 e1 = make_float2(ex2(y1.x), ex2(y1.y));
-                        a0 = fadd2(a0, e0);
-                        a1 = fadd2(a1, e1);
-                        w[u] = pack_half2(e0.x, e0.y);
-                        w[u + 1] = pack_half2(e1.x, e1.y);
-                    }
-                    tmem_st16(s_col + c / 2, w);
+                float sum = prob64(s_col, lo, sc2, nr2);
+                if (TILES == 1) {
+                    tmem_ld64(s_col + HALF, hi);
+                    if (cut)
+                        mask64(hi, lim - HALF);
                 }
-                const float2 a = fadd2(a0, a1);
-                l += a.x + a.y;
+                sum += prob64(s_col + HALF / 2, hi, sc2, nr2);
+                l += sum;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -705,53 +768,102 @@ __global__ void __launch_bounds__(NTHR, 1)
             float *part = nullptr;
             if (p.splits > 1)
                 part = p.part_o + ((tok * p.Hq + head) * p.splits + it.split) * D;
-            float fa = 1.f, fb = 0.f;        // weights of this tile's and the other's part
-            float *buf = reinterpret_cast<float *>(sq + Cfg::TILE_BYTES);
-            if (it.two) {
-                if (t == 1) {
-                    // second part: handed over D / 2 channels at a time, once the first
-                    // part's warp has read what was there
-#pragma unroll
-                    for (int h = 0; h < 2; ++h, ++n_m) {
-                        const bool got =
-                            n_m == 0 ||
-                            mbar_wait_or_abort(&mrg_empty[quarter], (n_m - 1) & 1, abort);
-                        if (!__all_sync(0xffffffffu, got)) {
-                            ok = false;
-                            break;
-                        }
-                        if (h == 0)
-                            s_ml[r] = make_float2(m, l);
-                        if (rg.count > 0 && !idle) {
-#pragma unroll
-                            for (int c = 0; c < D / 2; c += 32) {
-                                float v[32];
-                                tmem_ld32(o_col + h * (D / 2) + c, v);
-#pragma unroll
-                                for (int u = 0; u < 32; ++u)
-                                    buf[(c + u) * TM + r] = v[u];
-                            }
-                        }
-                        __syncwarp();
-                        mbar_arrive_warp(&mrg_full[quarter]);
-                    }
-                    if (!ok)
-                        break;
-                    tc_fence_before();
-                    continue;
-                }
-            }
-            unsigned bad = 0;
-            float inv = 1.f, lsum = l;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (it.two) {
-                    const bool got = mbar_wait_or_abort(&mrg_full[quarter], h, abort);
+            if (lane == 0)
+                bulk_wait_read<0>();   // the last item's stores have read the area
+            __syncwarp();
+            float *hand = reinterpret_cast<float *>(s_out + (4 + quarter) * Cfg::OUT_BYTES) + lane;
+            if (TILES == 2 && it.two && t == 1) {
+                // second part of the blocks: handed over 32 channels at a time, once the
+                // first part's warp has read what was there
+                for (int c = 0; c < D; c += 32, ++n_m) {
+                    const bool got =
+                        n_m == 0 || mbar_wait_or_abort(&mrg_empty[quarter], (n_m - 1) & 1, abort);
                     if (!__all_sync(0xffffffffu, got)) {
                         ok = false;
                         break;
                     }
-                    if (h == 0) {
+                    if (c == 0)
+                        s_ml[r] = make_float2(m, l);
+                    if (rg.count > 0 && !idle) {
+                        float v[32];
+                        tmem_ld32(o_col + c, v);
+#pragma unroll
+                        for (int u = 0; u < 32; ++u)
+                            hand[32 * u] = v[u];
+                    }
+                    __syncwarp();
+                    mbar_arrive_warp(&mrg_full[quarter]);
+                }
+                tc_fence_before();
+                continue;
+            }
+            unsigned bad = 0;
+            float fa = 1.f, fb = 0.f;        // weights of the two parts of the blocks
+            float inv = 1.f, lsum = l;
+            char *const row_to = real ? part ? reinterpret_cast<char *>(part)
+                                             : reinterpret_cast<char *>(o_row)
+                                      : nullptr;
+            // The area's rows are swizzled as TMA does it: 16-byte chunk ch of row r lies at
+            // chunk ch ^ (r / 2 % 4).
+            uint8_t *const area = s_out + warp * Cfg::OUT_BYTES;
+            auto chunk = [&](uint8_t *buf, int row, int ch) {
+                return reinterpret_cast<uint4 *>(buf + row * 64 + ((ch ^ (row >> 1 & 3)) << 4));
+            };
+            if (!it.two && !part && rg.count > 0 && full) {
+                // The common case: all 32 rows are real and whole tokens, so one TMA store
+                // takes 32 channels of them.  A short loop: this code runs once per item and
+                // comes from the instruction cache's far levels.
+                inv = l > 0.f ? rcp(l) : 0.f;
+                const float2 inv2 = make_float2(inv, inv), zero2 = make_float2(0.f, 0.f);
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint8_t *buf = area + c / 32 % Cfg::OUT_BUFS * Cfg::OUT_BUF;
+                    float v[32];
+                    tmem_ld32(o_col + c, v);
+                    if (c >= 32 * Cfg::OUT_BUFS) {
+                        if (lane == 0)
+                            bulk_wait_read<Cfg::OUT_BUFS - 1>();
+                        __syncwarp();
+                    }
+                    float2 z0 = zero2, z1 = zero2;   // not 0 when a value is not finite
+#pragma unroll
+                    for (int u = 0; u < 32; u += 8) {
+                        const float2 v0 = make_float2(v[u], v[u + 1]);
+                        const float2 v1 = make_float2(v[u + 2], v[u + 3]);
+                        const float2 v2 = make_float2(v[u + 4], v[u + 5]);
+                        const float2 v3 = make_float2(v[u + 6], v[u + 7]);
+                        z0 = ffma2(v0, zero2, z0);
+                        z1 = ffma2(v1, zero2, z1);
+                        z0 = ffma2(v2, zero2, z0);
+                        z1 = ffma2(v3, zero2, z1);
+                        const float2 w0 = fmul2(v0, inv2), w1 = fmul2(v1, inv2);
+                        const float2 w2 = fmul2(v2, inv2), w3 = fmul2(v3, inv2);
+                        *chunk(buf, lane, u / 8) =
+                            make_uint4(pack_half2(w0.x, w0.y), pack_half2(w1.x, w1.y),
+                                       pack_half2(w2.x, w2.y), pack_half2(w3.x, w3.y));
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_4d(&maps.o, buf, c, it.hk * g, it.start + rg.tok + w_tok,
+                                     (int)qseq);
+                        bulk_commit();
+                    }
+                    const float2 z = fadd2(z0, z1);
+                    if (z.x + z.y != 0.f)
+                        bad |= 1u << (c / 32);
+                }
+            } else {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                if (TILES == 2 && it.two) {
+                    const bool got = mbar_wait_or_abort(&mrg_full[quarter], n_m & 1, abort);
+                    if (!__all_sync(0xffffffffu, got)) {
+                        ok = false;
+                        break;
+                    }
+                    ++n_m;
+                    if (c == 0) {
                         const float2 other = s_ml[r];
                         const float mm = fmaxf(m, other.x);
                         fa = m == -INFINITY ? 0.f : ex2(m - mm);
@@ -760,90 +872,100 @@ __global__ void __launch_bounds__(NTHR, 1)
                         m = mm;
                     }
                 }
-                if (h == 0)
-                    inv = part ? 1.f : lsum > 0.f ? 1.f / lsum : 0.f;
-                if (!idle) {
+                if (c == 0)
+                    inv = part ? 1.f : lsum > 0.f ? rcp(lsum) : 0.f;
+                float v[32];
+                if (rg.count > 0 && !idle)
+                    tmem_ld32(o_col + c, v);
+                if (rg.count == 0 || idle || lsum == 0.f) {
 #pragma unroll
-                    for (int c = 0; c < D / 2; c += 32) {
-                        float v[32];
-                        if (rg.count > 0) {
-                            tmem_ld32(o_col + h * (D / 2) + c, v);
-                        } else {
+                    for (int u = 0; u < 32; ++u)
+                        v[u] = 0.f;
+                }
+                if (TILES == 2 && it.two) {
+                    if (lsum != 0.f) {
 #pragma unroll
-                            for (int u = 0; u < 32; ++u)
-                                v[u] = 0.f;
-                        }
-                        if (it.two) {
-#pragma unroll
-                            for (int u = 0; u < 32; ++u) {
-                                v[u] *= fa;
-                                if (fb > 0.f)
-                                    v[u] = fmaf(fb, buf[(c + u) * TM + r], v[u]);
-                            }
-                        }
-                        float probe = 0.f;
-#pragma unroll
-                        for (int u = 0; u < 32; ++u)
-                            probe = fmaf(v[u], 0.f, probe);
-                        const int c0 = h * (D / 2) + c;
-                        if (probe != 0.f)
-                            bad |= 1u << (c0 / 32);
-                        if (real) {
-                            if (lsum == 0.f) {
-#pragma unroll
-                                for (int u = 0; u < 32; ++u)
-                                    v[u] = 0.f;
-                            }
-                            if (part) {
-#pragma unroll
-                                for (int u = 0; u < 32; u += 4)
-                                    *reinterpret_cast<float4 *>(part + c0 + u) =
-                                        make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
-                            } else {
-#pragma unroll
-                                for (int u = 0; u < 32; u += 8)
-                                    *reinterpret_cast<uint4 *>(o_row + c0 + u) = make_uint4(
-                                        pack_half2(v[u] * inv, v[u + 1] * inv),
-                                        pack_half2(v[u + 2] * inv, v[u + 3] * inv),
-                                        pack_half2(v[u + 4] * inv, v[u + 5] * inv),
-                                        pack_half2(v[u + 6] * inv, v[u + 7] * inv));
-                            }
+                        for (int u = 0; u < 32; ++u) {
+                            const float y = hand[32 * u];
+                            v[u] = fmaf(fb, fb > 0.f ? y : 0.f, v[u] * fa);
                         }
                     }
-                }
-                if (it.two) {
-                    fence_async_smem();   // the next query tile arrives by TMA
                     __syncwarp();
                     mbar_arrive_warp(&mrg_empty[quarter]);
-                    if (h == 1)
-                        mbar_arrive_warp(mrg_done);
                 }
+                if (idle)
+                    continue;
+                float2 probe = make_float2(0.f, 0.f);   // not 0 when a value is not finite
+#pragma unroll
+                for (int u = 0; u < 32; u += 2)
+                    probe = ffma2(make_float2(v[u], v[u + 1]), make_float2(0.f, 0.f), probe);
+                if (probe.x + probe.y != 0.f)
+                    bad |= 1u << (c / 32);
+                // 16 fp32 or 32 binary16 channels of every row into the area, then whole rows
+                // to memory
+                const int halves = part ? 2 : 1;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (h >= halves)
+                        break;
+                    __syncwarp();
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const float *x = v + 16 * h + 4 * u, *y = v + 8 * u;
+                        *chunk(area, lane, u) =
+                            part ? make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]),
+                                              __float_as_uint(x[2]), __float_as_uint(x[3]))
+                                 : make_uint4(pack_half2(y[0] * inv, y[1] * inv),
+                                              pack_half2(y[2] * inv, y[3] * inv),
+                                              pack_half2(y[4] * inv, y[5] * inv),
+                                              pack_half2(y[6] * inv, y[7] * inv));
+                    }
+                    __syncwarp();
+                    const int at = part ? 4 * (c + 16 * h) : 2 * c;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = 8 * i + lane / 4;
+                        char *to = reinterpret_cast<char *>(__shfl_sync(
+                            0xffffffffu, reinterpret_cast<unsigned long long>(row_to), row));
+                        const uint4 x = *chunk(area, row, lane % 4);
+                        if (to)
+                            *reinterpret_cast<uint4 *>(to + at + 16 * (lane % 4)) = x;
+                    }
+                }
+            }
+            fence_async_smem();   // the area's next use may be a TMA store
             }
             if (!ok)
                 break;
+            const bool again = real && bad && lsum < INFINITY;   // false for a sum that is NaN
+            if (__any_sync(0xffffffffu, again)) {
+                if (lane == 0)
+                    bulk_wait_all();   // what is stored again comes after what was stored
+                __syncwarp();
+                const uint16_t *q = p.q + qseq * p.qs[0] + head * p.qs[1] + tok * p.qs[2];
+                for (int c0 = 0; c0 < D; c0 += 32)
+                    if (again && bad >> (c0 / 32) & 1)
+                        row_again(p, it, q, it.j0 * TK, min(last, it.j1 * TK - 1),
+                                  m == -INFINITY ? 0.f : m, c0, inv, o_row, part);
+            }
             if (real) {
-                if (bad && lsum > 0.f && lsum < INFINITY) {
-                    const uint16_t *q = p.q + qseq * p.qs[0] + head * p.qs[1] + tok * p.qs[2];
-                    for (int c0 = 0; c0 < D; c0 += 32)
-                        if (bad >> (c0 / 32) & 1)
-                            row_again(p, it, q, it.j0 * TK, min(last, it.j1 * TK - 1), m, c0, inv,
-                                      o_row, part);
-                }
                 if (part)
                     p.part_ml[(tok * p.Hq + head) * p.splits + it.split] = make_float2(m, lsum);
                 else if (p.lse)
                     p.lse[qseq * p.ls[0] + head * p.ls[1] + tok] =
-                        lsum > 0.f ? (m + log2f(lsum)) * LN2 : lsum == 0.f ? -INFINITY : lsum;
+                        lsum > 0.f ? (m + __log2f(lsum)) * LN2 : lsum == 0.f ? -INFINITY : lsum;
             }
             tc_fence_before();
         }
+        if (lane == 0)
+            bulk_wait_read<0>();   // no store reads shared memory after the CTA has left
     }
 
     tc_fence_before();
     __syncthreads();
     if (warp == W_MMA) {
         tc_fence_after();
-        tmem_dealloc(tmem, TMEM_COLS);
+        tmem_dealloc(tmem, Cfg::TMEM_COLS);
     }
     if (threadIdx.x == 0 && *abort)
         flag_error(p.status, DEV_TIMEOUT);
@@ -901,22 +1023,23 @@ __global__ void __launch_bounds__(256) k_combine_tokens(const TokensLaunch p)
         p.lse[head * p.ls[1] + tok] = l > 0.f ? (ms + log2f(l)) * LN2 : l == 0.f ? -INFINITY : l;
 }
 
-template <int D> cudaError_t attend_tokens_impl(TokensLaunch p, cudaStream_t s)
+template <int D, int TILES> cudaError_t attend_tokens_impl(TokensLaunch p, cudaStream_t s)
 {
-    using Cfg = TokCfg<D>;
+    using Cfg = TokCfg<D, TILES>;
     const int g = p.Hq / p.Hkv, tpt = TM / g;
     TokMaps maps;
     const uint64_t seqs = p.cu ? 1 : p.B;
     const uint64_t D_ = D, L_ = p.L;
     auto map4 = [&](CUtensorMap *m, const uint16_t *base, const long *st, int heads, int box_heads,
-                    int box_tok) {
+                    int box_tok, uint32_t box_d = 64) {
         const uint64_t dims[4] = {D_, (uint64_t)heads, L_, seqs};
         const uint64_t str[3] = {(uint64_t)st[1] * 2, (uint64_t)st[2] * 2,
                                  (uint64_t)(seqs > 1 ? st[0] : st[2]) * 2};
-        const uint32_t box[4] = {64, (uint32_t)box_heads, (uint32_t)box_tok, 1};
+        const uint32_t box[4] = {box_d, (uint32_t)box_heads, (uint32_t)box_tok, 1};
         return encode_tmap_4d_f16(m, base, dims, str, box);
     };
-    bool ok = map4(&maps.q, p.q, p.qs, p.Hq, g, tpt);
+    bool ok = map4(&maps.q, p.q, p.qs, p.Hq, g, tpt) &&
+              map4(&maps.o, p.o, p.os, p.Hq, g, 32 / g, 32);
     if (p.n) {
         p.kv_rows = p.block_table ? p.num_pages * PAGE_SLOTS : p.B * p.Hkv * p.C;
         ok = ok && encode_tmap_2d_f16(&maps.k, p.k, D, p.kv_rows, 64, HALF) &&
@@ -928,16 +1051,17 @@ template <int D> cudaError_t attend_tokens_impl(TokensLaunch p, cudaStream_t s)
     if (!ok)
         return cudaErrorInvalidValue;
     cudaError_t e =
-        set_smem_once(reinterpret_cast<const void *>(k_attend_tokens<D>), Cfg::SMEM);
+        set_smem_once(reinterpret_cast<const void *>(k_attend_tokens<D, TILES>), Cfg::SMEM);
     if (e != cudaSuccess)
         return e;
     // packed: every sequence ends in at most one partial range
-    const long ranges = p.cu ? (long)p.L / (2 * tpt) + p.B
-                             : (long)((p.L + 2 * tpt - 1) / (2 * tpt)) * p.B;
+    const int range = TILES * tpt;
+    const long ranges =
+        p.cu ? (long)p.L / range + p.B : (long)((p.L + range - 1) / range) * p.B;
     const long items = ranges * p.Hkv * p.splits;
     if (items > 0x7fffffffL)
         return cudaErrorInvalidValue;
-    k_attend_tokens<D><<<(unsigned)items, NTHR, Cfg::SMEM, s>>>(maps, p);
+    k_attend_tokens<D, TILES><<<(unsigned)items, Cfg::NTHR, Cfg::SMEM, s>>>(maps, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1)
         return e;
@@ -948,15 +1072,19 @@ template <int D> cudaError_t attend_tokens_impl(TokensLaunch p, cudaStream_t s)
 
 } // namespace
 
+// Whether the batch's sequences bring few tokens: at most one tile of rows each on average.
+static bool few_tokens(int T, int B, int g) { return T <= (long)B * (TM / g); }
+
 int plan_tokens_splits(int T, int B, int Hq, int Hkv, int C, int requested)
 {
     const int blocks = (C + TK - 1) / TK;
     int s = requested;
     if (s <= 0) {
-        // the items that certainly exist, against one CTA per SM
-        const int tpt = TM / (Hq / Hkv);
-        const long items = ((long)T / (2 * tpt) + B) * Hkv;
-        s = (int)(sm_count() / (items > 0 ? items : 1));
+        // the items that certainly exist, against the CTAs that run at once
+        const int g = Hq / Hkv;
+        const bool few = few_tokens(T, B, g);
+        const long items = ((long)T / ((few ? 1 : 2) * (TM / g)) + B) * Hkv;
+        s = (int)((few ? 2 : 1) * sm_count() / (items > 0 ? items : 1));
     }
     s = s < blocks ? s : blocks;
     return s < 1 ? 1 : s > 64 ? 64 : s;
@@ -964,7 +1092,10 @@ int plan_tokens_splits(int T, int B, int Hq, int Hkv, int C, int requested)
 
 cudaError_t launch_attend_tokens(const TokensLaunch &p, cudaStream_t s)
 {
-    return p.D == 128 ? attend_tokens_impl<128>(p, s) : attend_tokens_impl<64>(p, s);
+    const bool few = p.cu ? few_tokens(p.L, p.B, p.Hq / p.Hkv) : p.L <= TM / (p.Hq / p.Hkv);
+    if (few)
+        return p.D == 128 ? attend_tokens_impl<128, 1>(p, s) : attend_tokens_impl<64, 1>(p, s);
+    return p.D == 128 ? attend_tokens_impl<128, 2>(p, s) : attend_tokens_impl<64, 2>(p, s);
 }
 
 } // namespace kvc

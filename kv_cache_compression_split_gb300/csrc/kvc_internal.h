@@ -33,7 +33,8 @@ int resident_ctas(const void *func, int threads, int smem);
 bool encode_tmap_2d_f16(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows,
                         uint32_t box_inner, uint32_t box_rows);
 
-// Rank-4 map of binary16 data (dims and box innermost first, byte strides of dims 1..3).
+// Rank-4 map of binary16 data (dims and box innermost first, byte strides of dims 1..3);
+// swizzled over the bytes of the box's rows, 64 or 128.
 bool encode_tmap_4d_f16(CUtensorMap *map, const void *base, const uint64_t dims[4],
                         const uint64_t strides[3], const uint32_t box[4]);
 

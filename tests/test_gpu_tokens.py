@@ -300,3 +300,66 @@ def test_graph_replay_follows_device_lengths(kvc):
         check_prompt(q, k, v, o, lse, cu, lens, Hq, Hkv, what=str(lens))
         check_chunk(q, K, V, n, m, o2, None, Hq, what=str(m))
     assert device_status_clean(kvc)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,L", [(8, 1, 128, 300), (4, 4, 64, 200), (6, 2, 128, 90)])
+def test_prompt_non_finite_rows_stay_with_the_rows_that_attend_them(kvc, Hq, Hkv, D, L):
+    """Infinities and NaN in single key and value rows: rows before them, which do not attend
+    them, are what they are without them; rows from them on are what the formula gives: NaN
+    where a key is NaN, and in a channel whose attended values hold an infinity or NaN, that."""
+    gen = _gen(D + L)
+    q, k, v = _randn(gen, L, Hq, D), _randn(gen, L, Hkv, D), _randn(gen, L, Hkv, D)
+    clean_k, clean_v = k.clone(), v.clone()
+    inf_at, nan_at, key_at = L // 3, L // 2, 3 * L // 4
+    v[inf_at, 0, 5] = float("inf")
+    v[nan_at, 0, 9] = float("nan")
+    k[key_at, 0] = float("nan")
+    o, lse = torch.empty_like(q), torch.empty(Hq, L, device="cuda")
+    kvc.kvc_prompt_attend(q, k, v, o, cu_seqlens=_cu([L]), lse=lse)
+    g = Hq // Hkv
+    for h in range(Hq):
+        ref = attend_rows(q[:, h], clean_k[:, h // g], clean_v[:, h // g], torch.arange(L))
+        if h // g > 0:
+            check_rows(o[:, h], lse[h], ref, f"h={h}")
+            continue
+        assert torch.isnan(o[key_at:, h]).all() and torch.isnan(lse[h, key_at:]).all()
+        keep = torch.ones(D, dtype=torch.bool, device="cuda")
+        keep[5] = keep[9] = False
+        part = [x[:key_at] for x in ref]
+        check_rows(o[:key_at, h][:, keep], lse[h, :key_at],
+                   (part[0][:, keep], part[1], part[2][:, keep], part[3]), f"h={h}")
+        assert torch.isposinf(o[inf_at:key_at, h, 5]).all()
+        assert torch.isnan(o[nan_at:key_at, h, 9]).all()
+        for c, first in ((5, inf_at), (9, nan_at)):
+            err = (o[:first, h, c].double() - ref[0][:first, c]).abs()
+            assert (err <= ref[2][:first, c]).all()
+    assert device_status_clean(kvc)
+
+
+@pytest.mark.parametrize("splits", [1, 4])
+@pytest.mark.parametrize("m", [[3, 1], [60, 1], [150, 2]])
+def test_chunk_non_finite_values_behind_a_row(kvc, m, splits):
+    """The chunk's later value rows are infinite or NaN: the earlier rows do not attend them."""
+    gen = _gen(sum(m))
+    n = [[500, 700], [650, 513]]
+    cache, K, V = _cache(kvc, gen, n, 704, 128, False)
+    clean = V.clone()
+    for h in range(2):
+        last = n[0][h] - 1
+        V[0, h, last, 3] = cache.V[0, h, last, 3] = float("inf")
+        V[0, h, last, 77] = cache.V[0, h, last, 77] = float("nan")
+    q = _randn(gen, sum(m), 8, 128)
+    o, lse = torch.empty_like(q), torch.empty(8, sum(m), device="cuda")
+    ws = torch.empty(max(kvc.kvc_chunk_workspace_size(cache, q, splits) // 4, 4), device="cuda")
+    kvc.kvc_chunk_attend(cache, q, _cu(m), o, lse=lse, workspace=ws, num_splits=splits)
+    assert torch.isposinf(o[m[0] - 1, :, 3]).all() and torch.isnan(o[m[0] - 1, :, 77]).all()
+    o[m[0] - 1, :, 3] = o[m[0] - 1, :, 77] = 0
+    for b, w in ((0, slice(0, m[0])), (1, slice(m[0], sum(m)))):
+        for h in range(8):
+            nn = n[b][h // 4]
+            ref = attend_rows(q[w, h], K[b, h // 4, :nn], clean[b, h // 4, :nn],
+                              nn - m[b] + torch.arange(m[b]))
+            if b == 0:
+                ref[0][-1, 3] = ref[0][-1, 77] = 0
+            check_rows(o[w, h], lse[h, w], ref, f"b={b} h={h}")
+    assert device_status_clean(kvc)
