@@ -309,6 +309,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int g = p.Hq / p.Hkv, tpt = TM / g;
 
+    asm volatile("griddepcontrol.launch_dependents;");
     if (threadIdx.x == 0) {
         *abort = 0;
         for (int i = 0; i < NS; ++i) {
@@ -971,15 +972,19 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
         flag_error(p.status, DEV_TIMEOUT);
 }
 
-// Merges the splits of a row: a warp per row, D / 32 channels per lane.
+// Merges the splits of a row, a CTA per row: each warp takes every fourth split, all its
+// loads in flight together, and the warps' sums meet in shared memory.  Launched so that it
+// may start while the attention still runs; it waits before it reads the parts.
+constexpr int MERGE_WARPS = 4;
+constexpr int MAX_SPLITS = 64;
 template <int D>
-__global__ void __launch_bounds__(256) k_combine_tokens(const TokensLaunch p)
+__global__ void __launch_bounds__(32 * MERGE_WARPS) k_combine_tokens(const TokensLaunch p)
 {
-    constexpr int V = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long row = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= (long)p.L * p.Hq)
-        return;
+    constexpr int V = D / 32;             // channels per lane
+    constexpr int U = MAX_SPLITS / MERGE_WARPS / 4;
+    __shared__ float s_acc[MERGE_WARPS][D];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long row = blockIdx.x;
     const int tok = (int)(row / p.Hq), head = (int)(row % p.Hq);
     int lo = 0, hi = p.B;   // the last sequence that starts at or before the token
     while (lo < hi) {
@@ -995,32 +1000,65 @@ __global__ void __launch_bounds__(256) k_combine_tokens(const TokensLaunch p)
     seq_range(p, lo, start, len);
     if (tok < start || tok >= start + len)
         return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // every warp reads all references and sums (two per lane)
     const float2 *ml = p.part_ml + row * p.splits;
-    float ms = -INFINITY;
-    for (int s = 0; s < p.splits; ++s)
-        ms = fmaxf(ms, ml[s].x);
-    float l = 0.f, acc[V];
+    const float2 none = make_float2(-INFINITY, 0.f);
+    const float2 x0 = lane < p.splits ? ml[lane] : none;
+    const float2 x1 = lane + 32 < p.splits ? ml[lane + 32] : none;
+    float ms = fmaxf(x0.x, x1.x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, off));
+    // weight of each split; 0 where a range held no key of the row (its part is not read)
+    const float w0 = x0.y == 0.f ? 0.f : ex2(x0.x - ms);
+    const float w1 = x1.y == 0.f ? 0.f : ex2(x1.x - ms);
+    float l = w0 * x0.y + w1 * x1.y;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        l += __shfl_xor_sync(0xffffffffu, l, off);
+    float acc[V];
 #pragma unroll
     for (int v = 0; v < V; ++v)
         acc[v] = 0.f;
-    for (int s = 0; s < p.splits; ++s) {
-        const float2 x = ml[s];
-        if (x.y == 0.f)
-            continue;   // the range held no key of the row
-        const float w = ex2(x.x - ms);
-        l = fmaf(w, x.y, l);
-        const float *src = p.part_o + (row * p.splits + s) * D + V * lane;
+    for (int s0 = warp; s0 < p.splits; s0 += U * MERGE_WARPS) {
+        float x[U][V];
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            acc[v] = fmaf(w, src[v], acc[v]);
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u * MERGE_WARPS;
+            const float w = __shfl_sync(0xffffffffu, s & 32 ? w1 : w0, s & 31);
+            const bool read = s < p.splits && w != 0.f;
+            const float *src = p.part_o + (row * p.splits + s) * D + V * lane;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                x[u][v] = read ? src[v] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u * MERGE_WARPS;
+            const float w = __shfl_sync(0xffffffffu, s & 32 ? w1 : w0, s & 31);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                acc[v] = s < p.splits ? fmaf(w, x[u][v], acc[v]) : acc[v];
+        }
     }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    uint16_t *o = p.o + head * p.os[1] + (long)tok * p.os[2] + V * lane;
 #pragma unroll
-    for (int v = 0; v < V; v += 2)
-        *reinterpret_cast<uint32_t *>(o + v) = pack_half2(acc[v] * inv, acc[v + 1] * inv);
-    if (p.lse && lane == 0)
-        p.lse[head * p.ls[1] + tok] = l > 0.f ? (ms + log2f(l)) * LN2 : l == 0.f ? -INFINITY : l;
+    for (int v = 0; v < V; ++v)
+        s_acc[warp][V * lane + v] = acc[v];
+    __syncthreads();
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    uint16_t *o = p.o + head * p.os[1] + (long)tok * p.os[2];
+    for (int d = 2 * threadIdx.x; d < D; d += 64 * MERGE_WARPS) {
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int w = 0; w < MERGE_WARPS; ++w) {
+            a += s_acc[w][d];
+            b += s_acc[w][d + 1];
+        }
+        *reinterpret_cast<uint32_t *>(o + d) = pack_half2(a * inv, b * inv);
+    }
+    if (p.lse && threadIdx.x == 0)
+        p.lse[head * p.ls[1] + tok] = l > 0.f ? (ms + __log2f(l)) * LN2 : l == 0.f ? -INFINITY : l;
 }
 
 template <int D, int TILES> cudaError_t attend_tokens_impl(TokensLaunch p, cudaStream_t s)
@@ -1065,9 +1103,16 @@ template <int D, int TILES> cudaError_t attend_tokens_impl(TokensLaunch p, cudaS
     e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1)
         return e;
-    const long rows = (long)p.L * p.Hq;
-    k_combine_tokens<D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((long)p.L * p.Hq));
+    cfg.blockDim = dim3(32 * MERGE_WARPS);
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_combine_tokens<D>, p);
 }
 
 } // namespace
@@ -1087,7 +1132,7 @@ int plan_tokens_splits(int T, int B, int Hq, int Hkv, int C, int requested)
         s = (int)((few ? 2 : 1) * sm_count() / (items > 0 ? items : 1));
     }
     s = s < blocks ? s : blocks;
-    return s < 1 ? 1 : s > 64 ? 64 : s;
+    return s < 1 ? 1 : s > MAX_SPLITS ? MAX_SPLITS : s;
 }
 
 cudaError_t launch_attend_tokens(const TokensLaunch &p, cudaStream_t s)
