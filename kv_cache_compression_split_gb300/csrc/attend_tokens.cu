@@ -49,8 +49,7 @@ namespace kvc {
 namespace {
 
 constexpr int TM = 128;                   // rows of a tile
-constexpr int TK = 128;                   // keys of a block
-constexpr int HALF = TK / 2;              // keys of one TMA box (a page of the cache)
+constexpr int BOX = 64;                   // keys of one TMA box (a page of the cache)
 constexpr int NI = 2;                     // slots of the item feed
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float GROWTH = 8.f;             // log2 growth of the maximum that moves the reference
@@ -59,19 +58,21 @@ template <int D, int TILES> struct TokCfg {
     static constexpr int W_TMA = 4 * TILES, W_MMA = W_TMA + 1;   // two more warps are idle
     static constexpr int NTHR = 128 * (TILES + 1);
     static constexpr int CTAS = 3 - TILES;                 // per SM
+    // keys of a block, and score buffers in TMEM: one per tile, or two for the only tile, so
+    // that a block's scores are there when the row's threads have done the one before
+    static constexpr int TK = 64 * TILES;
     static constexpr int NBOX = D / 64;
-    static constexpr int BOX_BYTES = TM * 128;
-    static constexpr int TILE_BYTES = NBOX * BOX_BYTES;
-    // ring stages (one K or V block each)
-    static constexpr int NS = (D == 128 ? 4 : 8) / (3 - TILES);
+    static constexpr int QBOX_BYTES = TM * 128, QTILE_BYTES = NBOX * QBOX_BYTES;
+    static constexpr int BOX_BYTES = TK * 128, TILE_BYTES = NBOX * BOX_BYTES;
+    static constexpr int NS = D == 128 ? 4 : 8;   // ring stages (one K or V block each)
     // output area of a row warp: buffers of 32 rows of 64 bytes
     static constexpr int OUT_BUF = 32 * 64, OUT_BUFS = TILES;
     static constexpr int OUT_BYTES = OUT_BUFS * OUT_BUF;
     static constexpr int ML_BYTES = TM * 8;
-    static constexpr int SMEM = (TILES + NS) * TILE_BYTES + 4 * TILES * OUT_BYTES + ML_BYTES + 1024 + 1024;
+    static constexpr int SMEM = TILES * QTILE_BYTES + NS * TILE_BYTES + 4 * TILES * OUT_BYTES + ML_BYTES + 1024 + 1024;
     static constexpr uint32_t IDESC_QK = idesc_f16_f32(TM, TK);
     static constexpr uint32_t IDESC_PV = idesc_f16_f32_bmn(TM, D);
-    static constexpr uint32_t COL_O = TILES * TK;          // TMEM: S_t, then O_t
+    static constexpr uint32_t COL_O = 2 * TK;              // TMEM: two score buffers, then O_t
     static constexpr uint32_t TMEM_COLS = 256 * TILES;
     // Registers.  384 threads are launched with 168 each, 256 (two CTAs per SM) with 128.
     // A row's thread holds its 128 scores and needs more; the last warpgroup gives what it
@@ -118,8 +119,8 @@ __device__ __forceinline__ void seq_range(const TokensLaunch &p, int b, int &sta
 struct ItemWalk {
     int b0 = 0;
     long base = 0;
-    // tiles: per item
-    __device__ bool find(const TokensLaunch &p, int tpt, int tiles, long idx, TokItem &it)
+    // tiles: per item; keys: per block
+    __device__ bool find(const TokensLaunch &p, int tpt, int tiles, int keys, long idx, TokItem &it)
     {
         const int lane = threadIdx.x & 31;
         if (idx < base) {
@@ -166,7 +167,7 @@ struct ItemWalk {
             }
             it.shift = n_keys - len;
             const int end = max(0, it.shift + it.tok0 + it.ntok);
-            const int blocks = (end + TK - 1) / TK;
+            const int blocks = (end + keys - 1) / keys;
             const int chunk = (blocks + p.splits - 1) / p.splits;
             it.j0 = min(blocks, it.split * chunk);
             it.j1 = min(blocks, it.j0 + chunk);
@@ -177,7 +178,7 @@ struct ItemWalk {
 };
 
 // Keys before `end` that tile t of the item sees, and its share of the blocks.
-struct TileRange {
+template <int TK> struct TileRange {
     int tok, ntok;       // tokens of the tile
     int end;             // keys its last token sees
     int j, step, count;  // blocks j, j + step, ...
@@ -286,11 +287,11 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
     k_attend_tokens(const __grid_constant__ TokMaps maps, const __grid_constant__ TokensLaunch p)
 {
     using Cfg = TokCfg<D, TILES>;
-    constexpr int NS = Cfg::NS, W_TMA = Cfg::W_TMA, W_MMA = Cfg::W_MMA;
+    constexpr int NS = Cfg::NS, TK = Cfg::TK, W_TMA = Cfg::W_TMA, W_MMA = Cfg::W_MMA;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_align1024(smem_raw);
     uint8_t *sq = smem;                                      // query tiles
-    uint8_t *ring = sq + TILES * Cfg::TILE_BYTES;            // NS blocks of K or V
+    uint8_t *ring = sq + TILES * Cfg::QTILE_BYTES;            // NS blocks of K or V
     uint8_t *s_out = ring + NS * Cfg::TILE_BYTES;            // an output area per row warp
     float2 *s_ml = reinterpret_cast<float2 *>(s_out + 4 * TILES * Cfg::OUT_BYTES);
     uint64_t *bars = reinterpret_cast<uint64_t *>(s_ml) + TM;
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
         }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
-        for (int t = 0; t < TILES; ++t) {
+        for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
             mbar_init(&p_full[t], 4);
             mbar_init(&o_full[t], 1);
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 // the next item while this one runs: take over a CTA that has not started
                 if (lane == 0)
                     clc_request(clc, clc_full);
-                if (!walk.find(p, tpt, TILES, idx, it))
+                if (!walk.find(p, tpt, TILES, TK, idx, it))
                     it.j0 = it.j1 = it.two = 0;   // the grid is an upper bound
             }
             if (idx < 0 || it.b >= 0) {
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
             const int unit = it.b * p.Hkv + it.hk;
             const int per = p.C / PAGE_SLOTS;
             if (p.block_table)   // the item's part of the page table into L1
-                for (int i = 2 * it.j0 + 32 * lane; i < min(per, 2 * it.j1); i += 1024)
+                for (int i = TK / BOX * it.j0 + 32 * lane; i < min(per, TK / BOX * it.j1); i += 1024)
                     asm volatile("prefetch.global.L1 [%0];" ::"l"(p.block_table +
                                                                   (size_t)unit * per + i));
             if (lane == 0 && n > 0) {
@@ -412,10 +413,10 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                         return;
                     mbar_arrive_expect_tx(&kv_full[st], Cfg::TILE_BYTES);
                     uint8_t *dst = ring + st * Cfg::TILE_BYTES;
-                    for (int h = 0; h < 2; ++h) {
-                        const int j_key = j * TK + h * HALF;
+                    for (int h = 0; h < TK / BOX; ++h) {
+                        const int j_key = j * TK + h * BOX;
                         if (p.n) {
-                            // a half without a key, or without a page, reads as zeros: its
+                            // a box without a key, or without a page, reads as zeros: its
                             // row lies behind the last one
                             int row = p.kv_rows;
                             if (j_key < n_keys) {
@@ -431,11 +432,11 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                                 }
                             }
                             for (int c = 0; c < Cfg::NBOX; ++c)
-                                tma_load_2d(dst + c * Cfg::BOX_BYTES + h * (HALF * 128), map,
+                                tma_load_2d(dst + c * Cfg::BOX_BYTES + h * (BOX * 128), map,
                                             &kv_full[st], 64 * c, row);
                         } else {
                             for (int c = 0; c < Cfg::NBOX; ++c)
-                                tma_load_4d(dst + c * Cfg::BOX_BYTES + h * (HALF * 128), map,
+                                tma_load_4d(dst + c * Cfg::BOX_BYTES + h * (BOX * 128), map,
                                             &kv_full[st], 64 * c, it.hk, it.start + j_key,
                                             p.cu ? 0 : it.b);
                         }
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 // The order in which the MMA warp takes them.  The first blocks go ahead of
                 // the query tile, whose place is free only when the last item's scores are
                 // done.
-                const int ahead = it.two ? 2 : 1;
+                const int ahead = TILES == 1 || it.two ? 2 : 1;
                 for (int i = 0; ok && i < ahead && i < n; ++i)
                     load(&maps.k, it.j0 + i);
                 if (ok)
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                     mbar_arrive_expect_tx(q_full, tiles * Cfg::NBOX * tpt * g * 128);
                     for (int t = 0; t < tiles; ++t)
                         for (int c = 0; c < Cfg::NBOX; ++c)
-                            tma_load_4d(sq + t * Cfg::TILE_BYTES + c * Cfg::BOX_BYTES, &maps.q,
+                            tma_load_4d(sq + t * Cfg::QTILE_BYTES + c * Cfg::QBOX_BYTES, &maps.q,
                                         q_full, 64 * c, it.hk * g, it.start + it.tok0 + t * tpt,
                                         p.cu ? 0 : it.b);
                     ++n_q;
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
         int n_it = 0, n_q = 0;
         int n_p[2] = {0, 0};
         const Int<0> T0;
-        const Int<TILES - 1> T1;
+        const Int<1> T1;
         bool ok = true;
         TokItem it;
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -506,22 +507,23 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
         // t as a type: its TMEM columns and barrier are constants then
         auto qk = [&](auto t_, int tile, int st) {   // S_t = Q_tile K^T, K in ring stage st
             constexpr int t = decltype(t_)::value;
-            const uint64_t qd = q_desc + tile * (Cfg::TILE_BYTES >> 4);
+            const uint64_t qd = q_desc + tile * (Cfg::QTILE_BYTES >> 4);
             const uint64_t kd = k_desc + (uint32_t)st * (Cfg::TILE_BYTES >> 4);
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = ((kk >> 2) * Cfg::BOX_BYTES + (kk & 3) * 32) >> 4;
-                    umma_f16(tm + TK * t, qd + off, kd + off, Cfg::IDESC_QK, kk > 0 ? 1u : 0u);
+                    const uint32_t qo = ((kk >> 2) * Cfg::QBOX_BYTES + (kk & 3) * 32) >> 4;
+                    const uint32_t ko = ((kk >> 2) * Cfg::BOX_BYTES + (kk & 3) * 32) >> 4;
+                    umma_f16(tm + TK * t, qd + qo, kd + ko, Cfg::IDESC_QK, kk > 0 ? 1u : 0u);
                 }
                 umma_commit(&s_full[t]);
             }
             __syncwarp();
         };
-        auto pv = [&](auto t_, int st, int keys, bool first) {   // O_t (+)= P_t V
+        auto pv = [&](auto t_, int st, int keys, bool first) {   // O (+)= P_t V
             constexpr int t = decltype(t_)::value;
             const uint64_t vd = v_desc + (uint32_t)st * (Cfg::TILE_BYTES >> 4);
-            const uint32_t od = tm + Cfg::COL_O + D * t, pd = tm + TK * t;
+            const uint32_t od = tm + Cfg::COL_O + (TILES == 2 ? D * t : 0), pd = tm + TK * t;
             const uint32_t acc = first ? 0u : 1u;
             const int steps = (keys + 15) / 16;
             if (elect_one()) {
@@ -554,8 +556,8 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
             const int n = it.j1 - it.j0;
             if (n <= 0)
                 continue;
-            const TileRange r0(it, 0, tpt), r1(it, TILES - 1, tpt);
-            const int ahead = it.two ? 2 : 1;
+            const TileRange<TK> r0(it, 0, tpt), r1(it, TILES - 1, tpt);
+            const int ahead = TILES == 1 || it.two ? 2 : 1;
             wait(q_full, n_q & 1);
             ++n_q;
             // first scores of both tiles
@@ -607,8 +609,10 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                             return;
                         ++n_p[T];
                         tc_fence_after();
-                        pv(t, vb, keys, i < ahead);
+                        pv(t, vb, keys, i < TILES);
                         commit(&kv_empty[vs % NS]);
+                        if (TILES == 1)   // each step of the only accumulator
+                            commit(&o_full[T]);
                         if (ks >= 0) {
                             wait(&kv_full[ks % NS], (ks / NS) & 1);
                             if (!ok)
@@ -618,11 +622,11 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                             commit(&kv_empty[ks % NS]);
                             if (i + ahead == n - 1)
                                 commit(q_empty);
-                        } else {
+                        } else if (TILES == 2) {
                             commit(&o_full[T]);
                         }
                     };
-                    if (TILES == 1 || !(i & 1))
+                    if (!(i & 1))
                         one(T0);
                     else
                         one(T1);
@@ -676,16 +680,16 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
         regs_inc<Cfg::REGS_ROW>();
         const int t = warp >> 2, quarter = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
-        const uint32_t s_col = lanes + TK * t, o_col = lanes + Cfg::COL_O + D * t;
+        const uint32_t o_col = lanes + Cfg::COL_O + D * t;
         const int r = 32 * quarter + lane;
         const int r_tok = r / g, r_head = r - r_tok * g;
         const int w_tok = 32 * quarter / g;   // token of the warp's first row
         const float scale = p.scale_log2;
-        int n_s = 0, n_o = 0, n_m = 0;   // phases of s_full, o_full and the hand-over
+        int n_s[2] = {0, 0}, n_o[2] = {0, 0}, n_m = 0;   // phases: s_full, o_full, hand-over
         bool ok = true;
         TokItem it;
         for (int k = 0; ok && feed_get(k, it); ++k) {
-            const TileRange rg(it, t, tpt);
+            const TileRange<TK> rg(it, t, tpt);
             const bool real = r_tok < min(rg.ntok, tpt);
             const int last = real ? it.shift + rg.tok + r_tok : -1;
             const bool idle = w_tok >= rg.ntok;                   // no row of the warp is real
@@ -694,37 +698,52 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
             float m = -INFINITY, l = 0.f;
             for (int i = 0; i < rg.count; ++i) {
                 const int k0 = (rg.j + i * rg.step) * TK;
-                const bool got = mbar_wait_or_abort(&s_full[t], n_s & 1, abort);
+                // score buffer and its phase
+                const int sb = TILES == 2 ? t : i & 1;
+                const uint32_t s_col = lanes + TK * sb;
+                const int ph = TILES == 2 || !sb ? n_s[0]++ : n_s[1]++;
+                const bool got = mbar_wait_or_abort(&s_full[sb], ph & 1, abort);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
-                ++n_s;
                 if (idle) {
-                    mbar_arrive_warp(&p_full[t]);
+                    mbar_arrive_warp(&p_full[sb]);
                     continue;
                 }
                 tc_fence_after();
-                // The upper half of the scores first: with one tile per CTA (fewer registers)
-                // it is read for the maximum and again for the probabilities, whose lower
-                // half lands on columns that are done with by then.
-                float hi[HALF], lo[HALF];
+                float lo[64], hi[TILES == 2 ? 64 : 1];
                 const int lim = last - k0;
                 const bool cut = k0 + TK - 1 > first_last;   // ends behind some row's range
-                tmem_ld64(s_col + HALF, hi);
-                if (cut)
-                    mask64(hi, lim - HALF);
-                const float top = max64(hi);
                 tmem_ld64(s_col, lo);
                 if (cut)
                     mask64(lo, lim);
-                const float mx = scale * fmaxf(top, max64(lo));
+                float top = max64(lo);
+                if constexpr (TILES == 2) {
+                    tmem_ld64(s_col + 64, hi);
+                    if (cut)
+                        mask64(hi, lim - 64);
+                    top = fmaxf(top, max64(hi));
+                }
+                const float mx = scale * top;
                 const bool grow = mx > m + GROWTH;
                 if (__any_sync(0xffffffffu, grow)) {
                     const float f = grow ? ex2(m - mx) : 1.f;   // 0 at the row's first key
                     if (grow)
                         m = mx;
                     l *= f;
+                    // two tiles: the scores were computed after the last product into O; one
+                    // tile: they may be ahead of it
+                    if (TILES == 1 && i > 0) {
+                        const int e = (i - 1) & 1;   // the product before: its barrier and phase
+                        const bool rest = mbar_wait_or_abort(
+                            &o_full[e], ((e ? n_o[1] : n_o[0]) + ((i - 1) >> 1)) & 1, abort);
+                        if (!__all_sync(0xffffffffu, rest)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
                     if (i > 0) {
 #pragma unroll
                         for (int c = 0; c < D; c += 32) {
@@ -739,26 +758,31 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 }
                 const float ref = m == -INFINITY ? 0.f : m;
                 const float2 sc2 = make_float2(scale, scale), nr2 = make_float2(-ref, -ref);
-                float sum = prob64(s_col, lo, sc2, nr2);
-                if (TILES == 1) {
-                    tmem_ld64(s_col + HALF, hi);
-                    if (cut)
-                        mask64(hi, lim - HALF);
-                }
-                sum += prob64(s_col + HALF / 2, hi, sc2, nr2);
-                l += sum;
+                l += prob64(s_col, lo, sc2, nr2);
+                if constexpr (TILES == 2)
+                    l += prob64(s_col + 32, hi, sc2, nr2);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                mbar_arrive_warp(&p_full[t]);
+                mbar_arrive_warp(&p_full[sb]);
             }
             if (!ok)
                 break;
             if (rg.count > 0) {
-                const bool got = mbar_wait_or_abort(&o_full[t], n_o & 1, abort);
+                // One tile: the products into O alternate between two barriers.  The last
+                // scores were issued after the last product but two, so on the last one's
+                // barrier nothing but it can be outstanding, and a parity tells enough.
+                bool got;
+                if (TILES == 2) {
+                    got = mbar_wait_or_abort(&o_full[t], n_o[0]++ & 1, abort);
+                } else {
+                    const int e = (rg.count - 1) & 1;
+                    n_o[0] += (rg.count + 1) / 2;
+                    n_o[1] += rg.count / 2;
+                    got = mbar_wait_or_abort(&o_full[e], ((e ? n_o[1] : n_o[0]) - 1) & 1, abort);
+                }
                 if (!__all_sync(0xffffffffu, got))
                     break;
-                ++n_o;
                 tc_fence_after();
             }
             // ---- results
@@ -1080,11 +1104,11 @@ template <int D, int TILES> cudaError_t attend_tokens_impl(TokensLaunch p, cudaS
               map4(&maps.o, p.o, p.os, p.Hq, g, 32 / g, 32);
     if (p.n) {
         p.kv_rows = p.block_table ? p.num_pages * PAGE_SLOTS : p.B * p.Hkv * p.C;
-        ok = ok && encode_tmap_2d_f16(&maps.k, p.k, D, p.kv_rows, 64, HALF) &&
-             encode_tmap_2d_f16(&maps.v, p.v, D, p.kv_rows, 64, HALF);
+        ok = ok && encode_tmap_2d_f16(&maps.k, p.k, D, p.kv_rows, 64, BOX) &&
+             encode_tmap_2d_f16(&maps.v, p.v, D, p.kv_rows, 64, BOX);
     } else {
-        ok = ok && map4(&maps.k, p.k, p.ks, p.Hkv, 1, HALF) &&
-             map4(&maps.v, p.v, p.vs, p.Hkv, 1, HALF);
+        ok = ok && map4(&maps.k, p.k, p.ks, p.Hkv, 1, BOX) &&
+             map4(&maps.v, p.v, p.vs, p.Hkv, 1, BOX);
     }
     if (!ok)
         return cudaErrorInvalidValue;
@@ -1122,7 +1146,7 @@ static bool few_tokens(int T, int B, int g) { return T <= (long)B * (TM / g); }
 
 int plan_tokens_splits(int T, int B, int Hq, int Hkv, int C, int requested)
 {
-    const int blocks = (C + TK - 1) / TK;
+    const int blocks = (C + 127) / 128;
     int s = requested;
     if (s <= 0) {
         // the items that certainly exist, against the CTAs that run at once

@@ -363,3 +363,28 @@ def test_chunk_non_finite_values_behind_a_row(kvc, m, splits):
                 ref[0][-1, 3] = ref[0][-1, 77] = 0
             check_rows(o[w, h], lse[h, w], ref, f"b={b} h={h}")
     assert device_status_clean(kvc)
+
+
+@pytest.mark.parametrize("D,most", [(128, 8), (64, 3), (128, 40)])
+def test_chunk_many_items_per_cta(kvc, D, most):
+    """More (sequence, head) items than run at once, with odd and even block counts and heads
+    evicted apart: what one item leaves in a CTA's pipeline must not reach the next."""
+    B, Hkv, g, C = 72, 8, 2, 640
+    rng = np.random.default_rng(D + most)
+    m = rng.integers(0, most + 1, B).tolist()
+    n = [[int(x) for x in rng.integers(mb, C + 1, Hkv)] for mb in m]
+    gen = _gen(D)
+    cache, K, V = _cache(kvc, gen, n, C, D, True)
+    T, Hq = sum(m), g * Hkv
+    q = _randn(gen, T, Hq, D)
+    ws = torch.empty(max(kvc.kvc_chunk_workspace_size(cache, q) // 4, 4), device="cuda")
+    o, lse = torch.full_like(q, 7.0), torch.full((Hq, T), 7.0, device="cuda")
+    for _ in range(3):
+        kvc.kvc_chunk_attend(cache, q, _cu(m), o, lse=lse, workspace=ws)
+    assert device_status_clean(kvc)
+    check_chunk(q, K, V, n, m, o, lse, Hq)
+    first = o.clone()
+    for _ in range(5):
+        kvc.kvc_chunk_attend(cache, q, _cu(m), o, lse=lse, workspace=ws)
+        assert torch.equal(o, first)          # the same inputs give the same bits
+    assert device_status_clean(kvc)
