@@ -787,13 +787,13 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
             }
             // ---- results
             const int head = it.hk * g + r_head;
-            const long tok = it.start + rg.tok + r_tok;
-            const long qseq = p.cu ? 0 : it.b;
-            uint16_t *o_row = p.o + qseq * p.os[0] + head * p.os[1] + tok * p.os[2];
-            float *part = nullptr;
-            if (p.splits > 1)
-                part = p.part_o + ((tok * p.Hq + head) * p.splits + it.split) * D;
-            if (lane == 0)
+            const int tok = it.start + rg.tok + r_tok;
+            const long row = (long)tok * p.Hq + head;       // of the parts
+            auto o_row = [&] {
+                return p.o + (p.cu ? 0 : it.b) * p.os[0] + head * p.os[1] + tok * p.os[2];
+            };
+            const bool part = p.splits > 1;
+            if (elect_one())
                 bulk_wait_read<0>();   // the last item's stores have read the area
             __syncwarp();
             float *hand = reinterpret_cast<float *>(s_out + (4 + quarter) * Cfg::OUT_BYTES) + lane;
@@ -825,20 +825,20 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
             unsigned bad = 0;
             float fa = 1.f, fb = 0.f;        // weights of the two parts of the blocks
             float inv = 1.f, lsum = l;
-            char *const row_to = real ? part ? reinterpret_cast<char *>(part)
-                                             : reinterpret_cast<char *>(o_row)
-                                      : nullptr;
             // The area's rows are swizzled as TMA does it: 16-byte chunk ch of row r lies at
             // chunk ch ^ (r / 2 % 4).
             uint8_t *const area = s_out + warp * Cfg::OUT_BYTES;
-            auto chunk = [&](uint8_t *buf, int row, int ch) {
-                return reinterpret_cast<uint4 *>(buf + row * 64 + ((ch ^ (row >> 1 & 3)) << 4));
+            auto chunk = [&](uint8_t *buf, int ch) {
+                return reinterpret_cast<uint4 *>(buf + lane * 64 + ((ch ^ (lane >> 1 & 3)) << 4));
             };
             if (!it.two && !part && rg.count > 0 && full) {
                 // The common case: all 32 rows are real and whole tokens, so one TMA store
                 // takes 32 channels of them.  A short loop: this code runs once per item and
                 // comes from the instruction cache's far levels.
                 inv = l > 0.f ? rcp(l) : 0.f;
+                const int o_y = __shfl_sync(0xffffffffu, it.hk * g, 0);
+                const int o_z = __shfl_sync(0xffffffffu, it.start + rg.tok + w_tok, 0);
+                const int o_w = __shfl_sync(0xffffffffu, p.cu ? 0 : it.b, 0);
                 const float2 inv2 = make_float2(inv, inv), zero2 = make_float2(0.f, 0.f);
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
@@ -846,7 +846,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                     float v[32];
                     tmem_ld32(o_col + c, v);
                     if (c >= 32 * Cfg::OUT_BUFS) {
-                        if (lane == 0)
+                        if (elect_one())
                             bulk_wait_read<Cfg::OUT_BUFS - 1>();
                         __syncwarp();
                     }
@@ -863,15 +863,14 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                         z1 = ffma2(v3, zero2, z1);
                         const float2 w0 = fmul2(v0, inv2), w1 = fmul2(v1, inv2);
                         const float2 w2 = fmul2(v2, inv2), w3 = fmul2(v3, inv2);
-                        *chunk(buf, lane, u / 8) =
+                        *chunk(buf, u / 8) =
                             make_uint4(pack_half2(w0.x, w0.y), pack_half2(w1.x, w1.y),
                                        pack_half2(w2.x, w2.y), pack_half2(w3.x, w3.y));
                     }
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        tma_store_4d(&maps.o, buf, c, it.hk * g, it.start + rg.tok + w_tok,
-                                     (int)qseq);
+                    if (elect_one()) {
+                        tma_store_4d(&maps.o, buf, c, o_y, o_z, o_w);
                         bulk_commit();
                     }
                     const float2 z = fadd2(z0, z1);
@@ -926,63 +925,51 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                     probe = ffma2(make_float2(v[u], v[u + 1]), make_float2(0.f, 0.f), probe);
                 if (probe.x + probe.y != 0.f)
                     bad |= 1u << (c / 32);
-                // 16 fp32 or 32 binary16 channels of every row into the area, then whole rows
-                // to memory
-                const int halves = part ? 2 : 1;
+                // parts of rows, and tiles that end inside a warp's rows: each thread stores
+                // its own row
+                if (real && part) {
+                    float *to = p.part_o + (row * p.splits + it.split) * D + c;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (h >= halves)
-                        break;
-                    __syncwarp();
+                    for (int u = 0; u < 32; u += 4)
+                        *reinterpret_cast<float4 *>(to + u) =
+                            make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
+                } else if (real) {
+                    uint16_t *to = o_row() + c;
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const float *x = v + 16 * h + 4 * u, *y = v + 8 * u;
-                        *chunk(area, lane, u) =
-                            part ? make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]),
-                                              __float_as_uint(x[2]), __float_as_uint(x[3]))
-                                 : make_uint4(pack_half2(y[0] * inv, y[1] * inv),
-                                              pack_half2(y[2] * inv, y[3] * inv),
-                                              pack_half2(y[4] * inv, y[5] * inv),
-                                              pack_half2(y[6] * inv, y[7] * inv));
-                    }
-                    __syncwarp();
-                    const int at = part ? 4 * (c + 16 * h) : 2 * c;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = 8 * i + lane / 4;
-                        char *to = reinterpret_cast<char *>(__shfl_sync(
-                            0xffffffffu, reinterpret_cast<unsigned long long>(row_to), row));
-                        const uint4 x = *chunk(area, row, lane % 4);
-                        if (to)
-                            *reinterpret_cast<uint4 *>(to + at + 16 * (lane % 4)) = x;
-                    }
+                    for (int u = 0; u < 32; u += 8)
+                        *reinterpret_cast<uint4 *>(to + u) =
+                            make_uint4(pack_half2(v[u] * inv, v[u + 1] * inv),
+                                       pack_half2(v[u + 2] * inv, v[u + 3] * inv),
+                                       pack_half2(v[u + 4] * inv, v[u + 5] * inv),
+                                       pack_half2(v[u + 6] * inv, v[u + 7] * inv));
                 }
             }
-            fence_async_smem();   // the area's next use may be a TMA store
             }
             if (!ok)
                 break;
             const bool again = real && bad && lsum < INFINITY;   // false for a sum that is NaN
             if (__any_sync(0xffffffffu, again)) {
-                if (lane == 0)
+                if (elect_one())
                     bulk_wait_all();   // what is stored again comes after what was stored
                 __syncwarp();
-                const uint16_t *q = p.q + qseq * p.qs[0] + head * p.qs[1] + tok * p.qs[2];
+                const uint16_t *q = p.q + (p.cu ? 0 : it.b) * p.qs[0] + head * p.qs[1] +
+                                    tok * p.qs[2];
                 for (int c0 = 0; c0 < D; c0 += 32)
                     if (again && bad >> (c0 / 32) & 1)
                         row_again(p, it, q, it.j0 * TK, min(last, it.j1 * TK - 1),
-                                  m == -INFINITY ? 0.f : m, c0, inv, o_row, part);
+                                  m == -INFINITY ? 0.f : m, c0, inv, o_row(),
+                                  part ? p.part_o + (row * p.splits + it.split) * D : nullptr);
             }
             if (real) {
                 if (part)
-                    p.part_ml[(tok * p.Hq + head) * p.splits + it.split] = make_float2(m, lsum);
+                    p.part_ml[row * p.splits + it.split] = make_float2(m, lsum);
                 else if (p.lse)
-                    p.lse[qseq * p.ls[0] + head * p.ls[1] + tok] =
+                    p.lse[(p.cu ? 0 : it.b) * p.ls[0] + head * p.ls[1] + tok] =
                         lsum > 0.f ? (m + __log2f(lsum)) * LN2 : lsum == 0.f ? -INFINITY : lsum;
             }
             tc_fence_before();
         }
-        if (lane == 0)
+        if (elect_one())
             bulk_wait_read<0>();   // no store reads shared memory after the CTA has left
     }
 
