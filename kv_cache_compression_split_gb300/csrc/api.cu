@@ -753,7 +753,7 @@ static kvc_status check_chunk(const kvc_chunk_args *a)
 static int chunk_splits(const kvc_chunk_args *a)
 {
     const kvc_slot_cache &c = *a->cache;
-    return plan_tokens_splits(a->T, c.B, a->Hq, c.Hkv, c.C, a->num_splits);
+    return plan_tokens_splits(a->T, c.B, a->Hq, c.Hkv, c.D, c.C, a->num_splits);
 }
 
 size_t kvc_chunk_workspace_size(const kvc_chunk_args *a)

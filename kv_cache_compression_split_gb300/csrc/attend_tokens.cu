@@ -80,7 +80,7 @@ template <int D, int TILES> struct TokCfg {
     static constexpr int REGS = TILES == 2 ? 168 : 128;
     static constexpr int REGS_ROW = TILES == 2 ? 208 : 168, REGS_IO = 88;
     static_assert(128 * (TILES * REGS_ROW + REGS_IO) <= NTHR * REGS, "register split");
-    static_assert(CTAS * SMEM <= 227 * 1024 + (CTAS - 1) * 1024, "shared memory");
+    static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory");
 };
 
 template <int N> struct Int {
@@ -1131,14 +1131,14 @@ template <int D, int TILES> cudaError_t attend_tokens_impl(TokensLaunch p, cudaS
 // Whether the batch's sequences bring few tokens: at most one tile of rows each on average.
 static bool few_tokens(int T, int B, int g) { return T <= (long)B * (TM / g); }
 
-int plan_tokens_splits(int T, int B, int Hq, int Hkv, int C, int requested)
+int plan_tokens_splits(int T, int B, int Hq, int Hkv, int D, int C, int requested)
 {
     const int blocks = (C + 127) / 128;
     int s = requested;
     if (s <= 0) {
         // the items that certainly exist, against the CTAs that run at once
         const int g = Hq / Hkv;
-        const bool few = few_tokens(T, B, g);
+        const bool few = D == 64 || few_tokens(T, B, g);
         const long items = ((long)T / ((few ? 1 : 2) * (TM / g)) + B) * Hkv;
         s = (int)((few ? 2 : 1) * sm_count() / (items > 0 ? items : 1));
     }
@@ -1148,10 +1148,18 @@ int plan_tokens_splits(int T, int B, int Hq, int Hkv, int C, int requested)
 
 cudaError_t launch_attend_tokens(const TokensLaunch &p, cudaStream_t s)
 {
-    const bool few = p.cu ? few_tokens(p.L, p.B, p.Hq / p.Hkv) : p.L <= TM / (p.Hq / p.Hkv);
-    if (few)
+    // Which form: two tiles share the K and V blocks and win once an item is long; the one-tile
+    // form's second CTA per SM works through the start and the end of the first one's items.
+    // Uniform prompts of 16 / 2 heads of 128, one against two tiles, us: 16 x 512 tokens 31 / 35,
+    // 8 x 1024 42 / 46, 8 x 2048 118 / 119, 4 x 4096 205 / 193, 2 x 8192 374 / 341; 16 / 16
+    // heads: 39 / 45, 51 / 52, 123 / 124, 217 / 199, 397 / 367.  Heads of 64 channels, whose
+    // time goes to the exponentials, are faster with one tile throughout (2 x 8192: 276 / 298).
+    // A chunk's item is as long as the cache: one tile while the chunks fit one.
+    const bool one = p.D == 64 || (p.n ? few_tokens(p.L, p.B, p.Hq / p.Hkv)
+                                       : p.L <= 1024L * (p.cu ? p.B : 1));
+    if (one)
         return p.D == 128 ? attend_tokens_impl<128, 1>(p, s) : attend_tokens_impl<64, 1>(p, s);
-    return p.D == 128 ? attend_tokens_impl<128, 2>(p, s) : attend_tokens_impl<64, 2>(p, s);
+    return attend_tokens_impl<128, 2>(p, s);
 }
 
 } // namespace kvc

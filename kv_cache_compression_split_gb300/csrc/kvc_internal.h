@@ -137,7 +137,7 @@ struct TokensLaunch {
 cudaError_t launch_attend_tokens(const TokensLaunch &p, cudaStream_t s);
 
 // Key ranges per unit of a chunk of T tokens (requested > 0: that many, within the cache).
-int plan_tokens_splits(int T, int B, int Hq, int Hkv, int C, int requested);
+int plan_tokens_splits(int T, int B, int Hq, int Hkv, int D, int C, int requested);
 
 // Page tables, slot map, positions and lengths of a ragged batch of new tokens.
 struct PlanLaunch {
