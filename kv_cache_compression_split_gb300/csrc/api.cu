@@ -750,17 +750,17 @@ static kvc_status check_chunk(const kvc_chunk_args *a)
     return KVC_OK;
 }
 
-static int chunk_splits(const kvc_chunk_args *a)
+static TokensPlan chunk_plan(const kvc_chunk_args *a)
 {
     const kvc_slot_cache &c = *a->cache;
-    return plan_tokens_splits(a->T, c.B, a->Hq, c.Hkv, c.D, c.C, a->num_splits);
+    return plan_tokens(a->T, c.B, a->Hq, c.Hkv, c.D, c.C, a->num_splits);
 }
 
 size_t kvc_chunk_workspace_size(const kvc_chunk_args *a)
 {
     if (check_chunk(a) != KVC_OK)
         return 0;
-    const int s = chunk_splits(a);
+    const int s = chunk_plan(a).splits;
     return s > 1 ? (size_t)a->T * a->Hq * s * (a->cache->D + 2) * sizeof(float) : 0;
 }
 
@@ -776,7 +776,9 @@ kvc_status kvc_chunk_attend(const kvc_chunk_args *a, cudaStream_t stream)
         return KVC_ERR_INVALID_ARG;
     const kvc_slot_cache &c = *a->cache;
     TokensLaunch p{};
-    p.splits = chunk_splits(a);
+    const TokensPlan plan = chunk_plan(a);
+    p.tiles = plan.tiles;
+    p.splits = plan.splits;
     if (p.splits > 1) {
         if (!a->workspace || a->workspace_bytes < kvc_chunk_workspace_size(a) ||
             !aligned16(a->workspace))

@@ -983,19 +983,19 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
         flag_error(p.status, DEV_TIMEOUT);
 }
 
-// Merges the splits of a row, a CTA per row: each warp takes every fourth split, all its
-// loads in flight together, and the warps' sums meet in shared memory.  Launched so that it
-// may start while the attention still runs; it waits before it reads the parts.
-constexpr int MERGE_WARPS = 4;
+// Merges the splits of a row.  A warp per row, or (WARPS = 4, many splits) a CTA per row
+// whose warps take every fourth split and meet in shared memory; four parts' loads are in
+// flight together.  Launched so that it may start while the attention still runs; it
+// waits before it reads the parts.
 constexpr int MAX_SPLITS = 64;
-template <int D>
-__global__ void __launch_bounds__(32 * MERGE_WARPS) k_combine_tokens(const TokensLaunch p)
+template <int D, int WARPS>
+__global__ void __launch_bounds__(128) k_combine_tokens(const TokensLaunch p)
 {
     constexpr int V = D / 32;             // channels per lane
-    constexpr int U = MAX_SPLITS / MERGE_WARPS / 4;
-    __shared__ float s_acc[MERGE_WARPS][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long row = blockIdx.x;
+    constexpr int U = 4;
+    __shared__ __align__(16) float s_acc[WARPS][D];
+    const int warp = WARPS == 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long row = WARPS == 1 ? (long)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
     const int tok = (int)(row / p.Hq), head = (int)(row % p.Hq);
     int lo = 0, hi = p.B;   // the last sequence that starts at or before the token
     while (lo < hi) {
@@ -1005,7 +1005,7 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) k_combine_tokens(const Token
         else
             hi = mid;
     }
-    if (lo >= p.B)
+    if (lo >= p.B || tok >= p.L)
         return;
     int start, len;
     seq_range(p, lo, start, len);
@@ -1032,43 +1032,51 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) k_combine_tokens(const Token
 #pragma unroll
     for (int v = 0; v < V; ++v)
         acc[v] = 0.f;
-    for (int s0 = warp; s0 < p.splits; s0 += U * MERGE_WARPS) {
-        float x[U][V];
+    for (int s0 = warp; s0 < p.splits; s0 += U * WARPS) {
+        float x[U][V], w[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int s = s0 + u * MERGE_WARPS;
-            const float w = __shfl_sync(0xffffffffu, s & 32 ? w1 : w0, s & 31);
-            const bool read = s < p.splits && w != 0.f;
+            const int s = s0 + u * WARPS;
+            w[u] = __shfl_sync(0xffffffffu, s & 32 ? w1 : w0, s & 31);
+            const bool read = s < p.splits && w[u] != 0.f;
             const float *src = p.part_o + (row * p.splits + s) * D + V * lane;
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                x[u][v] = read ? src[v] : 0.f;
+            for (int v = 0; v < V; v += 2) {
+                const float2 y = read ? *reinterpret_cast<const float2 *>(src + v)
+                                      : make_float2(0.f, 0.f);
+                x[u][v] = y.x;
+                x[u][v + 1] = y.y;
+            }
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int s = s0 + u * MERGE_WARPS;
-            const float w = __shfl_sync(0xffffffffu, s & 32 ? w1 : w0, s & 31);
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                acc[v] = s < p.splits ? fmaf(w, x[u][v], acc[v]) : acc[v];
+                acc[v] = s0 + u * WARPS < p.splits ? fmaf(w[u], x[u][v], acc[v]) : acc[v];
+    }
+    if (WARPS > 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            s_acc[warp][V * lane + v] = acc[v];
+        __syncthreads();
+        if (warp > 0)
+            return;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            acc[v] = 0.f;
+#pragma unroll
+            for (int i = 0; i < WARPS; ++i)
+                acc[v] += s_acc[i][V * lane + v];
         }
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        s_acc[warp][V * lane + v] = acc[v];
-    __syncthreads();
     const float inv = l != 0.f ? 1.f / l : 0.f;
-    uint16_t *o = p.o + head * p.os[1] + (long)tok * p.os[2];
-    for (int d = 2 * threadIdx.x; d < D; d += 64 * MERGE_WARPS) {
-        float a = 0.f, b = 0.f;
-#pragma unroll
-        for (int w = 0; w < MERGE_WARPS; ++w) {
-            a += s_acc[w][d];
-            b += s_acc[w][d + 1];
-        }
-        *reinterpret_cast<uint32_t *>(o + d) = pack_half2(a * inv, b * inv);
-    }
-    if (p.lse && threadIdx.x == 0)
+    uint16_t *o = p.o + head * p.os[1] + (long)tok * p.os[2] + V * lane;
+    if constexpr (V == 4)
+        *reinterpret_cast<uint2 *>(o) = make_uint2(pack_half2(acc[0] * inv, acc[1] * inv),
+                                                   pack_half2(acc[2] * inv, acc[3] * inv));
+    else
+        *reinterpret_cast<uint32_t *>(o) = pack_half2(acc[0] * inv, acc[1] * inv);
+    if (p.lse && lane == 0)
         p.lse[head * p.ls[1] + tok] = l > 0.f ? (ms + __log2f(l)) * LN2 : l == 0.f ? -INFINITY : l;
 }
 
@@ -1114,36 +1122,57 @@ template <int D, int TILES> cudaError_t attend_tokens_impl(TokensLaunch p, cudaS
     e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1)
         return e;
+    const long rows = (long)p.L * p.Hq;
+    // a CTA per row where rows are few and parts many (1024 rows of 16 parts, the whole call:
+    // 18.1 us against 19.8 with a warp per row; 8192 rows of 8 parts: 38 against 31)
+    const bool many = p.splits > 16 || (p.splits > 4 && rows <= 4096);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((long)p.L * p.Hq));
-    cfg.blockDim = dim3(32 * MERGE_WARPS);
+    cfg.gridDim = dim3((unsigned)(many ? rows : (rows + 3) / 4));
+    cfg.blockDim = dim3(128);
     cfg.stream = s;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_combine_tokens<D>, p);
+    return many ? cudaLaunchKernelEx(&cfg, k_combine_tokens<D, 4>, p)
+                : cudaLaunchKernelEx(&cfg, k_combine_tokens<D, 1>, p);
 }
 
 } // namespace
 
-// Whether the batch's sequences bring few tokens: at most one tile of rows each on average.
-static bool few_tokens(int T, int B, int g) { return T <= (long)B * (TM / g); }
-
-int plan_tokens_splits(int T, int B, int Hq, int Hkv, int D, int C, int requested)
+// Form and splits of a chunk, by what a call takes in microseconds: a start, then each
+// round of CTAs its key blocks and an item's start and end, then the merge.  The numbers
+// are fitted to a sweep of forms and splits over 16 shapes (1 to 32 sequences, 1 to 300
+// tokens each, 512 to 32768 slots); the choice was within 10% of the best one of the
+// sweep on all but two of them.  The slots that a unit holds are known on the GPU alone:
+// the capacity stands for them.
+TokensPlan plan_tokens(int T, int B, int Hq, int Hkv, int D, int C, int requested)
 {
-    const int blocks = (C + 127) / 128;
-    int s = requested;
-    if (s <= 0) {
-        // the items that certainly exist, against the CTAs that run at once
-        const int g = Hq / Hkv;
-        const bool few = D == 64 || few_tokens(T, B, g);
-        const long items = ((long)T / ((few ? 1 : 2) * (TM / g)) + B) * Hkv;
-        s = (int)((few ? 2 : 1) * sm_count() / (items > 0 ? items : 1));
+    const int tpt = TM / (Hq / Hkv), sms = sm_count();
+    const double mean = (double)T / B, rows = (double)T * Hq;
+    TokensPlan best{1, 1};
+    double least = 1e300;
+    for (int tiles = D == 128 ? 2 : 1; tiles >= 1; --tiles) {
+        const int keys = 64 * tiles;
+        const int blocks = (C + keys - 1) / keys;
+        const double items = B * ceil(mean / (tiles * tpt)) * Hkv;
+        const int most = requested > 0 ? requested : MAX_SPLITS;
+        for (int s = requested > 0 ? requested : 1; s <= most; ++s) {
+            const int splits = s < MAX_SPLITS ? s : MAX_SPLITS;
+            const double ctas = items * splits, per = (blocks + splits - 1) / splits;
+            double us = tiles == 2 ? ceil(ctas / sms) * (1.31 * per + 4.6)
+                                   : ceil(ctas / (2.0 * sms)) * (0.7 * per + 3.5) *
+                                         (ctas > sms ? 1.25 : 1.0);
+            if (splits > 1)
+                us += 2.8 + 0.18 * splits + rows * splits * D * 8 / 3e6;
+            if (us < least && (splits == 1 || splits <= blocks || requested > 0)) {
+                least = us;
+                best = TokensPlan{tiles, splits};
+            }
+        }
     }
-    s = s < blocks ? s : blocks;
-    return s < 1 ? 1 : s > MAX_SPLITS ? MAX_SPLITS : s;
+    return best;
 }
 
 cudaError_t launch_attend_tokens(const TokensLaunch &p, cudaStream_t s)
@@ -1154,9 +1183,8 @@ cudaError_t launch_attend_tokens(const TokensLaunch &p, cudaStream_t s)
     // 8 x 1024 42 / 46, 8 x 2048 118 / 119, 4 x 4096 205 / 193, 2 x 8192 374 / 341; 16 / 16
     // heads: 39 / 45, 51 / 52, 123 / 124, 217 / 199, 397 / 367.  Heads of 64 channels, whose
     // time goes to the exponentials, are faster with one tile throughout (2 x 8192: 276 / 298).
-    // A chunk's item is as long as the cache: one tile while the chunks fit one.
-    const bool one = p.D == 64 || (p.n ? few_tokens(p.L, p.B, p.Hq / p.Hkv)
-                                       : p.L <= 1024L * (p.cu ? p.B : 1));
+    // A chunk's form comes with its plan.
+    const bool one = p.D == 64 || (p.n ? p.tiles == 1 : p.L <= 1024L * (p.cu ? p.B : 1));
     if (one)
         return p.D == 128 ? attend_tokens_impl<128, 1>(p, s) : attend_tokens_impl<64, 1>(p, s);
     return attend_tokens_impl<128, 2>(p, s);

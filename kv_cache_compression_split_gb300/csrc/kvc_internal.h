@@ -128,6 +128,7 @@ struct TokensLaunch {
     const int32_t *block_table; // chunk: paged layout (nullptr: dense)
     int num_pages;
     int kv_rows;               // chunk: rows of the K / V arrays (set by the launcher)
+    int tiles;                 // chunk: tiles per item
     int splits;                // key ranges per item, merged by a second launch when above 1
     float *part_o;             // [L * Hq, splits, D]
     float2 *part_ml;           // [L * Hq, splits]: reference and sum
@@ -136,8 +137,12 @@ struct TokensLaunch {
 };
 cudaError_t launch_attend_tokens(const TokensLaunch &p, cudaStream_t s);
 
-// Key ranges per unit of a chunk of T tokens (requested > 0: that many, within the cache).
-int plan_tokens_splits(int T, int B, int Hq, int Hkv, int D, int C, int requested);
+// Form (tiles per item) and key ranges per unit of a chunk of T tokens in all (requested > 0:
+// that many ranges).
+struct TokensPlan {
+    int tiles, splits;
+};
+TokensPlan plan_tokens(int T, int B, int Hq, int Hkv, int D, int C, int requested);
 
 // Page tables, slot map, positions and lengths of a ragged batch of new tokens.
 struct PlanLaunch {
