@@ -756,12 +756,17 @@ static TokensPlan chunk_plan(const kvc_chunk_args *a)
     return plan_tokens(a->T, c.B, a->Hq, c.Hkv, c.D, c.C, a->num_splits);
 }
 
+// Parts of every row: D values, the reference and the sum.
+static size_t chunk_bytes(const kvc_chunk_args *a, int splits)
+{
+    return splits > 1 ? (size_t)a->T * a->Hq * splits * (a->cache->D + 2) * sizeof(float) : 0;
+}
+
 size_t kvc_chunk_workspace_size(const kvc_chunk_args *a)
 {
     if (check_chunk(a) != KVC_OK)
         return 0;
-    const int s = chunk_plan(a).splits;
-    return s > 1 ? (size_t)a->T * a->Hq * s * (a->cache->D + 2) * sizeof(float) : 0;
+    return chunk_bytes(a, chunk_plan(a).splits);
 }
 
 kvc_status kvc_chunk_attend(const kvc_chunk_args *a, cudaStream_t stream)
@@ -780,7 +785,7 @@ kvc_status kvc_chunk_attend(const kvc_chunk_args *a, cudaStream_t stream)
     p.tiles = plan.tiles;
     p.splits = plan.splits;
     if (p.splits > 1) {
-        if (!a->workspace || a->workspace_bytes < kvc_chunk_workspace_size(a) ||
+        if (!a->workspace || a->workspace_bytes < chunk_bytes(a, p.splits) ||
             !aligned16(a->workspace))
             return KVC_ERR_WORKSPACE;
         p.part_o = static_cast<float *>(a->workspace);

@@ -265,7 +265,9 @@ __global__ void __launch_bounds__(THREADS) k_append_plan(const PlanLaunch p)
         if (p.table_out != p.table)   // entries that change are written again below
             copy_i32(p.table_out, p.table, (long)units * per, gtid);
         // ---- scan: pages asked for and given back by the units before each unit
-        const int count = min(max(*p.count, 0), p.num_pages);
+        const int given = *p.count, count = min(max(given, 0), p.num_pages);
+        if (given != count && gtid == 0)
+            flag_error(p.status, DEV_CAPACITY);
         int held[SPAN], now[SPAN];     // pages before and after
         int ask = 0, back = 0;
 #pragma unroll

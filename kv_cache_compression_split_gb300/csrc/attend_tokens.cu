@@ -1005,13 +1005,12 @@ __global__ void __launch_bounds__(128) k_combine_tokens(const TokensLaunch p)
         else
             hi = mid;
     }
-    if (lo >= p.B || tok >= p.L)
-        return;
-    int start, len;
-    seq_range(p, lo, start, len);
+    int start = 0, len = 0;
+    if (lo < p.B)
+        seq_range(p, lo, start, len);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tok < start || tok >= start + len)
         return;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     // every warp reads all references and sums (two per lane)
     const float2 *ml = p.part_ml + row * p.splits;
     const float2 none = make_float2(-INFINITY, 0.f);
@@ -1145,31 +1144,35 @@ template <int D, int TILES> cudaError_t attend_tokens_impl(TokensLaunch p, cudaS
 // round of CTAs its key blocks and an item's start and end, then the merge.  The numbers
 // are fitted to a sweep of forms and splits over 16 shapes (1 to 32 sequences, 1 to 300
 // tokens each, 512 to 32768 slots); the choice was within 10% of the best one of the
-// sweep on all but two of them.  The slots that a unit holds are known on the GPU alone:
-// the capacity stands for them.
+// sweep on all but three of them (20% there, under 4 us).  The slots that a unit holds are
+// known on the GPU alone: the capacity stands for them.
 TokensPlan plan_tokens(int T, int B, int Hq, int Hkv, int D, int C, int requested)
 {
     const int tpt = TM / (Hq / Hkv), sms = sm_count();
-    const double mean = (double)T / B, rows = (double)T * Hq;
+    const long rows = (long)T * Hq;
+    const int mean = (T + B - 1) / B;
     TokensPlan best{1, 1};
-    double least = 1e300;
+    float least = INFINITY;
     for (int tiles = D == 128 ? 2 : 1; tiles >= 1; --tiles) {
-        const int keys = 64 * tiles;
+        const int keys = 64 * tiles, slots = sms * (3 - tiles);
         const int blocks = (C + keys - 1) / keys;
-        const double items = B * ceil(mean / (tiles * tpt)) * Hkv;
-        const int most = requested > 0 ? requested : MAX_SPLITS;
-        for (int s = requested > 0 ? requested : 1; s <= most; ++s) {
+        const long items = (long)B * Hkv * ((mean + tiles * tpt - 1) / (tiles * tpt));
+        for (int s = requested > 0 ? requested : 1;; s += 1 + s / 16) {
             const int splits = s < MAX_SPLITS ? s : MAX_SPLITS;
-            const double ctas = items * splits, per = (blocks + splits - 1) / splits;
-            double us = tiles == 2 ? ceil(ctas / sms) * (1.31 * per + 4.6)
-                                   : ceil(ctas / (2.0 * sms)) * (0.7 * per + 3.5) *
-                                         (ctas > sms ? 1.25 : 1.0);
+            const long ctas = items * splits;
+            const long rounds = (ctas + slots - 1) / slots;
+            const int per = (blocks + splits - 1) / splits;
+            float us = tiles == 2 ? rounds * (1.31f * per + 4.6f)
+                                  : rounds * (0.7f * per + 3.5f) * (ctas > sms ? 1.25f : 1.f);
             if (splits > 1)
-                us += 2.8 + 0.18 * splits + rows * splits * D * 8 / 3e6;
-            if (us < least && (splits == 1 || splits <= blocks || requested > 0)) {
+                us += 2.8f + 0.18f * splits + (float)rows * splits * D * (8.f / 3e6f);
+            if (us < least) {
                 least = us;
                 best = TokensPlan{tiles, splits};
             }
+            // more splits than fill the card twice only add to the merge
+            if (requested > 0 || s >= MAX_SPLITS || s >= blocks || ctas >= 2 * slots)
+                break;
         }
     }
     return best;
