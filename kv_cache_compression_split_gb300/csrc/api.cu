@@ -92,7 +92,7 @@ struct KernelDeviceEntry {
 std::vector<KernelDeviceEntry> g_kernel_entries;   // guarded by g_mu
 } // namespace
 
-cudaError_t set_smem_once(const void *func, int bytes, bool wide_cluster)
+cudaError_t set_smem_once(const void *func, int bytes)
 {
     const int dev = current_device();
     if (dev < 0)
@@ -101,10 +101,8 @@ cudaError_t set_smem_once(const void *func, int bytes, bool wide_cluster)
     for (const KernelDeviceEntry &e : g_kernel_entries)
         if (e.func == func && e.dev == dev && !e.occupancy)
             return cudaSuccess;
-    cudaError_t err =
+    const cudaError_t err =
         cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (err == cudaSuccess && wide_cluster)
-        err = cudaFuncSetAttribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (err == cudaSuccess)
         g_kernel_entries.push_back({func, dev, 1, false});
     return err;

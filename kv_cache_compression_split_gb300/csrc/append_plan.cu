@@ -22,13 +22,14 @@ namespace kvc {
 
 namespace {
 
-constexpr int CTAS = 16;       // one cluster
+constexpr int CTAS = 8;        // one cluster (16 CTAs start 2.6 us later)
 constexpr int THREADS = 1024;
 constexpr int CU_CACHE = 2048; // sequence starts held in shared memory
 constexpr int HEADS = 8;       // heads of a token whose loads are in flight together
-// Tokens whose slot map the cluster writes itself; more go to a second kernel on all SMs
-// (scattered words: TODO).
-constexpr int CLUSTER_TOKENS = 2048;
+// Tokens whose slot map the cluster writes itself: beyond the first of each unit, single
+// words in many lines, which eight SMs take long over (8 x 1024 tokens of 8 heads: 79 us,
+// 12 us with the second kernel; 128 x 4 tokens 17.4 against 16.8; 64 x 1 11.9 against 12.4).
+constexpr int CLUSTER_TOKENS = 512;
 constexpr int PLAN_MAX_SPAN = KVC_PLAN_MAX_UNITS / (CTAS * THREADS);
 
 __device__ __forceinline__ int ld_cluster_s32(const int *local, uint32_t rank)
@@ -50,45 +51,39 @@ __device__ __forceinline__ bool fits(const PlanLaunch &p, int n, int m)
     return n >= 0 && n <= p.C - m;
 }
 
-// Exclusive scans of two counts over the CTA's threads, and their totals.
-__device__ __forceinline__ void scan2(int &x, int &y, int &tx, int &ty)
+// Exclusive scans of three counts over the CTA's threads, and their totals.
+__device__ __forceinline__ void scan3(int (&x)[3], int (&total)[3])
 {
-    __shared__ int s_x[32], s_y[32];
+    __shared__ int s_x[3][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int ix = x, iy = y;
+    int in[3] = {x[0], x[1], x[2]};
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int ux = __shfl_up_sync(0xffffffffu, ix, off);
-        const int uy = __shfl_up_sync(0xffffffffu, iy, off);
-        if (lane >= off) {
-            ix += ux;
-            iy += uy;
+    for (int off = 1; off < 32; off <<= 1)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const int y = __shfl_up_sync(0xffffffffu, in[k], off);
+            in[k] += lane >= off ? y : 0;
         }
-    }
-    if (lane == 31) {
-        s_x[warp] = ix;
-        s_y[warp] = iy;
-    }
+    if (lane == 31)
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            s_x[k][warp] = in[k];
     __syncthreads();
-    if (warp == 0) {
-        int wx = s_x[lane], wy = s_y[lane];
+    if (warp < 3) {
+        int w = s_x[warp][lane];
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int ux = __shfl_up_sync(0xffffffffu, wx, off);
-            const int uy = __shfl_up_sync(0xffffffffu, wy, off);
-            if (lane >= off) {
-                wx += ux;
-                wy += uy;
-            }
+            const int y = __shfl_up_sync(0xffffffffu, w, off);
+            w += lane >= off ? y : 0;
         }
-        s_x[lane] = wx;
-        s_y[lane] = wy;
+        s_x[warp][lane] = w;
     }
     __syncthreads();
-    x = ix - x + (warp ? s_x[warp - 1] : 0);
-    y = iy - y + (warp ? s_y[warp - 1] : 0);
-    tx = s_x[31];
-    ty = s_y[31];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        x[k] = in[k] - x[k] + (warp ? s_x[k][warp - 1] : 0);
+        total[k] = s_x[k][31];
+    }
 }
 
 // dst[i] = src[i] for i in [0, n), by the whole cluster, 16 bytes at a time where both are
@@ -132,13 +127,8 @@ __device__ __forceinline__ int last_at_most(const int *v, int n, int x)
     return lo;
 }
 
-// Whether unit u takes its m new tokens, once its pages are granted.
-__device__ __forceinline__ bool takes(const PlanLaunch &p, int u, int n, int m)
-{
-    return fits(p, n, m) && (!p.table || p.pages_out[u] * (long)PAGE_SLOTS >= n + m);
-}
-
-// Row of unit u's slot, once its pages are granted; -1 when its table entry is not a page.
+// Row of the cache's arrays that slot `slot` of unit u is, by its page table; -1 (and
+// reported) when the entry is not a page.
 __device__ __forceinline__ int slot_row(const PlanLaunch &p, int u, int slot)
 {
     if (!p.table)
@@ -150,18 +140,221 @@ __device__ __forceinline__ int slot_row(const PlanLaunch &p, int u, int slot)
     return -1;
 }
 
-// Slot map and positions of token t for every head.  `starts` are the sequences' first
-// tokens (cu, or a copy).  Ranges that run backwards cannot be bisected: then the first
-// sequence that holds the token is looked for one by one.
-// AFTER: the counts are already the new ones, and the first token of each unit is done: its
-// entry says whether the unit takes its tokens.
-template <bool AFTER>
-__device__ __forceinline__ void plan_token(const PlanLaunch &p, int t, const int *starts,
-                                           bool backwards)
+// A thread owns SPAN consecutive units, so CTAS * THREADS * SPAN units at most.  What the
+// CTA's units are, for its threads that write new pages, returned pages and tokens: those
+// are dealt evenly over the threads, who find their unit by bisecting the sums.
+template <int SPAN> struct PlanSmem {
+    static constexpr int N = THREADS * SPAN;
+    int grow[N + 1], back[N + 1], toks[N + 1];   // pages taken, given back, tokens, before each unit
+    int held[N];                                 // pages before
+    int base[N];                                 // first new slot; -1: the unit is refused
+    int start[N], pos[N];                        // first new token and its position
+};
+
+template <int SPAN>
+__global__ void __launch_bounds__(THREADS) k_append_plan(const PlanLaunch p)
 {
+    extern __shared__ __align__(16) uint8_t smem[];
+    using Smem = PlanSmem<SPAN>;
+    Smem &sm = *reinterpret_cast<Smem *>(smem);
+    __shared__ int s_sum[4];   // this CTA's pages asked for, given back, granted; a bad range
+    const int rank = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+    const int gtid = rank * THREADS + tid;
+    const int units = p.B * p.Hkv;
+    const int per = p.C / PAGE_SLOTS;
+    const int u0 = gtid * SPAN, cta_u0 = rank * Smem::N;
+    const bool paged = p.table != nullptr;
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    // ---- everything of the old state that is read: it may be replaced after the cluster
+    // barrier below
+    const int given = paged ? *p.count : 0, count = min(max(given, 0), p.num_pages);
+    if (given != count && gtid == 0)
+        flag_error(p.status, DEV_CAPACITY);
+    int held[SPAN], now[SPAN], n[SPAN], m[SPAN], seqlen[SPAN];   // now: pages after
+    int sum[3] = {0, 0, 0};
+    bool fit[SPAN], broken = false;
+#pragma unroll
+    for (int i = 0; i < SPAN; ++i) {
+        held[i] = now[i] = n[i] = m[i] = seqlen[i] = 0;
+        fit[i] = false;
+        const int u = u0 + i, b = u / p.Hkv;
+        if (u < units) {
+            const int c0 = p.cu[b], c1 = p.cu[b + 1];
+            n[i] = p.n[u];
+            seqlen[i] = p.seqlen[b];
+            held[i] = now[i] = paged ? p.pages[u] : 0;
+            const bool bad = c0 < 0 || c1 < c0 || c1 > p.T;
+            broken |= bad;
+            m[i] = bad ? 0 : c1 - c0;
+            sm.start[tid * SPAN + i] = c0;
+            fit[i] = fits(p, n[i], m[i]) && held[i] >= 0 && held[i] <= per;
+            if (fit[i] && paged) {
+                const int need = (n[i] + m[i] + PAGE_SLOTS - 1) / PAGE_SLOTS;
+                now[i] = p.release || need > held[i] ? need : held[i];
+            }
+            if (!fit[i] || bad)
+                flag_error(p.status, DEV_CAPACITY);
+        }
+        sum[0] += max(0, now[i] - held[i]);
+        sum[1] += max(0, held[i] - now[i]);
+        sum[2] += m[i];
+    }
+    if (paged && p.table_out != p.table)   // entries that change are written again below
+        copy_i32(p.table_out, p.table, (long)units * per, gtid);
+    broken = __syncthreads_or(broken);
+    int total[3];
+    scan3(sum, total);
+#pragma unroll
+    for (int i = 0; i < SPAN; ++i) {
+        const int x = tid * SPAN + i;
+        sm.held[x] = held[i];
+        sm.grow[x] = sum[0];
+        sm.back[x] = sum[1];
+        sm.toks[x] = sum[2];
+        sm.pos[x] = seqlen[i];
+        sum[0] += max(0, now[i] - held[i]);
+        sum[1] += max(0, held[i] - now[i]);
+        sum[2] += m[i];
+    }
+    if (tid == 0) {
+        s_sum[0] = sm.grow[Smem::N] = total[0];
+        s_sum[1] = sm.back[Smem::N] = total[1];
+        s_sum[2] = 0;
+        s_sum[3] = broken;
+        sm.toks[Smem::N] = total[2];
+    }
+    cluster_sync_all();
+    // pages asked for and given back in all, and before this CTA's first unit
+    const bool one = lane < CTAS;
+    const int r_ask = one ? ld_cluster_s32(&s_sum[0], lane) : 0;
+    const int r_back = one ? ld_cluster_s32(&s_sum[1], lane) : 0;
+    broken = __any_sync(0xffffffffu, one && ld_cluster_s32(&s_sum[3], lane) != 0);
+    const int asked = __reduce_add_sync(0xffffffffu, r_ask);
+    const int before = __reduce_add_sync(0xffffffffu, lane < rank ? r_ask : 0);
+    const int back0 = __reduce_add_sync(0xffffffffu, lane < rank ? r_back : 0);
+    const int n_back = __reduce_add_sync(0xffffffffu, r_back);
+    cluster_arrive();   // a CTA may leave once every other one has read its sums
+
+    // ---- grants: a unit that the stack cannot serve in full keeps what it has.  Units are
+    // served in order, so those served are the ones up to some unit and those that ask for
+    // nothing.
+    int granted = 0;
+#pragma unroll
+    for (int i = 0; i < SPAN; ++i) {
+        const int x = tid * SPAN + i, u = u0 + i, g = max(0, now[i] - held[i]);
+        bool ok = fit[i];
+        if (g && before + sm.grow[x] + g > count) {
+            ok = false;
+            now[i] = held[i];
+            flag_error(p.status, DEV_CAPACITY);
+        } else {
+            granted += g;
+        }
+        sm.base[x] = ok ? n[i] : -1;
+        if (u < units) {
+            p.n_out[u] = ok ? n[i] + m[i] : n[i];
+            if (paged)
+                p.pages_out[u] = now[i];
+            if (u % p.Hkv == 0)
+                p.seqlen_out[u / p.Hkv] = seqlen[i] + m[i];
+        }
+    }
+    int taken = asked, mine = total[0];   // pages taken in all, and by this CTA
+    if (asked > count) {   // the same on every CTA of the cluster
+        cluster_wait();
+        granted = __reduce_add_sync(0xffffffffu, granted);
+        if (lane == 0)
+            atomicAdd(&s_sum[2], granted);
+        cluster_sync_all();
+        taken = __reduce_add_sync(0xffffffffu, one ? ld_cluster_s32(&s_sum[2], lane) : 0);
+        mine = s_sum[2];
+        cluster_arrive();
+    }
+    const int left = count - taken;   // pages left on the stack
+    if (paged && gtid == 0)
+        *p.count_out = min(left + n_back, p.num_pages);
+    // ---- new pages of the CTA's units, the next ones of the stack
+    for (int x = tid; x < mine; x += THREADS) {
+        const int i = last_at_most(sm.grow, Smem::N, x);
+        p.table_out[(size_t)(cta_u0 + i) * per + sm.held[i] + x - sm.grow[i]] =
+            p.free_list[count - 1 - before - x];
+    }
+    if (paged && p.free_out != p.free_list)
+        copy_i32(p.free_out, p.free_list, left, gtid);
+    // ---- tokens of no sequence
+    const int first = broken ? p.T : min(p.cu[0], p.T), end = broken ? p.T : max(0, p.cu[p.B]);
+    for (long x = gtid; x < (long)first * p.Hkv; x += CTAS * THREADS)
+        p.slot_map[x] = -1;
+    for (long x = (long)end * p.Hkv + gtid; x < (long)p.T * p.Hkv; x += CTAS * THREADS)
+        p.slot_map[x] = -1;
+    if (broken) {   // ranges may overlap what was just filled
+        cluster_wait();
+        cluster_sync_all();
+        cluster_arrive();
+    }
+    __syncthreads();   // the CTA's pages are in the table, its units' slots known
+    // ---- slot map and positions: every token of the CTA's units, or the first one of each
+    // (k_plan_tokens follows with the others)
+    const bool all = p.T <= CLUSTER_TOKENS;
+    for (int x = tid; x < (all ? total[2] : Smem::N); x += THREADS) {
+        const int i = all ? last_at_most(sm.toks, Smem::N, x) : x;
+        const int u = cta_u0 + i, step = all ? x - sm.toks[i] : 0;
+        if (step >= sm.toks[i + 1] - sm.toks[i])
+            continue;
+        int row = -1;
+        if (sm.base[i] >= 0) {
+            const int slot = sm.base[i] + step;
+            row = slot_row(p, u, slot);
+            p.pos[(size_t)u * p.C + slot] = sm.pos[i] + step;
+        }
+        p.slot_map[(size_t)(sm.start[i] + step) * p.Hkv + u % p.Hkv] = row;
+    }
+    // ---- returned pages go on the stack in unit order, when every page has been taken
+    if (n_back > 0 && p.free_out == p.free_list) {
+        cluster_wait();
+        cluster_sync_all();
+        cluster_arrive();
+    }
+    for (int x = tid; x < total[1]; x += THREADS) {
+        const int i = last_at_most(sm.back, Smem::N, x);
+        const int gave = sm.back[i + 1] - sm.back[i];
+        const size_t e = (size_t)(cta_u0 + i) * per + sm.held[i] - gave + x - sm.back[i];
+        const int pg = p.table[e], to = left + back0 + x;
+        p.table_out[e] = -1;
+        if (to < p.num_pages)
+            p.free_out[to] = pg;
+        else
+            flag_error(p.status, DEV_CAPACITY);
+    }
+    cluster_wait();
+}
+
+// The other tokens of a large batch, a thread per token and eight heads' loads in flight
+// together.  Launched so that its CTAs may start while the plan still runs: they wait for
+// it before they read what it wrote.  The counts are the new ones by then, and the first
+// token of each unit is done: its entry says whether the unit takes its tokens.  Ranges
+// that run backwards cannot be bisected: then the first sequence that holds the token is
+// looked for one by one.
+__global__ void __launch_bounds__(256) k_plan_tokens(const PlanLaunch p)
+{
+    __shared__ int s_cu[CU_CACHE];
+    bool backwards = false;
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+        const int c0 = p.cu[b], c1 = p.cu[b + 1];
+        backwards |= c1 < c0;
+        if (b < CU_CACHE)
+            s_cu[b] = c0;
+    }
+    backwards = __syncthreads_or(backwards);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int t = blockIdx.x * blockDim.x + threadIdx.x;
+    if (t >= p.T)
+        return;
     int b = 0, start = 0, m = 0;
     if (!backwards) {
-        b = last_at_most(starts, p.B - 1, t);   // of sequences without tokens, the last
+        // of sequences without tokens, the last
+        b = last_at_most(p.B <= CU_CACHE ? s_cu : p.cu, p.B - 1, t);
         m = new_tokens(p, b, start);
     } else {
         for (; b < p.B; ++b) {
@@ -170,32 +363,25 @@ __device__ __forceinline__ void plan_token(const PlanLaunch &p, int t, const int
                 break;
         }
     }
-    const bool inside = b < p.B && t >= start && t < start + m;
     const int step = t - start;
-    if (AFTER && inside && step == 0)
-        return;
-    const int P = inside ? (AFTER ? p.seqlen_out[b] - m : p.seqlen[b]) + step : 0;
-    int *map = p.slot_map + (size_t)t * p.Hkv;
+    if (b >= p.B || step <= 0 || step >= m)
+        return;   // of no sequence, or the first one: written by the plan
     const int per = p.C / PAGE_SLOTS;
+    const int P = p.seqlen_out[b] - m + step;
+    int *map = p.slot_map + (size_t)t * p.Hkv;
     for (int h0 = 0; h0 < p.Hkv; h0 += HEADS) {
         const int nh = min(HEADS, p.Hkv - h0), u = b * p.Hkv + h0;
         // each step loads for all heads before any value is used
-        int n[HEADS], x[HEADS], row[HEADS];
+        int n[HEADS], first[HEADS], row[HEADS];
 #pragma unroll
         for (int h = 0; h < HEADS; ++h) {
-            const bool here = inside && h < nh;
-            n[h] = here ? (AFTER ? p.n_out : p.n)[u + h] : -1;
-            // what tells whether the unit takes its tokens: its pages, or its first entry
-            x[h] = !here ? -1
-                   : AFTER ? p.slot_map[(size_t)start * p.Hkv + h0 + h]
-                           : p.table ? p.pages_out[u + h] : per;
+            n[h] = h < nh ? p.n_out[u + h] - m : -1;
+            first[h] = h < nh ? p.slot_map[(size_t)start * p.Hkv + h0 + h] : -1;
         }
         unsigned ok = 0;   // heads that take the token
 #pragma unroll
         for (int h = 0; h < HEADS; ++h) {
-            n[h] -= AFTER ? m : 0;
-            const bool room = !p.table || x[h] * (long)PAGE_SLOTS >= n[h] + m;
-            ok |= (unsigned)(fits(p, n[h], m) && (AFTER ? x[h] >= 0 : room)) << h;
+            ok |= (unsigned)(first[h] >= 0 && fits(p, n[h], m)) << h;
             n[h] += step;   // the token's slot
         }
 #pragma unroll
@@ -230,205 +416,6 @@ __device__ __forceinline__ void plan_token(const PlanLaunch &p, int t, const int
     }
 }
 
-// A thread owns SPAN consecutive units, so CTAS * THREADS * SPAN units at most.
-template <int SPAN> struct PlanSmem {
-    int cu[CU_CACHE];
-    int grow[THREADS * SPAN + 1];   // pages taken by the CTA's units before each unit
-    int back[THREADS * SPAN + 1];   // pages given back
-    int held[THREADS * SPAN];
-};
-
-template <int SPAN>
-__global__ void __launch_bounds__(THREADS) k_append_plan(const PlanLaunch p)
-{
-    extern __shared__ __align__(16) uint8_t smem[];
-    PlanSmem<SPAN> &sm = *reinterpret_cast<PlanSmem<SPAN> *>(smem);
-    __shared__ int s_sum[3];   // this CTA's pages asked for, given back and granted
-    const int rank = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
-    const int gtid = rank * THREADS + tid, gsize = CTAS * THREADS;
-    const int units = p.B * p.Hkv;
-    const int per = p.C / PAGE_SLOTS;
-    const int u0 = gtid * SPAN, cta_u0 = rank * THREADS * SPAN;
-    int left = 0, n_back = 0;      // pages left on the stack, pages given back
-
-    asm volatile("griddepcontrol.launch_dependents;");
-
-    bool backwards = false;
-    for (int b = tid; b < p.B; b += THREADS) {
-        const int c0 = p.cu[b], c1 = p.cu[b + 1];
-        backwards |= c1 < c0;
-        if (b < CU_CACHE)
-            sm.cu[b] = c0;
-    }
-
-    if (p.table) {
-        if (p.table_out != p.table)   // entries that change are written again below
-            copy_i32(p.table_out, p.table, (long)units * per, gtid);
-        // ---- scan: pages asked for and given back by the units before each unit
-        const int given = *p.count, count = min(max(given, 0), p.num_pages);
-        if (given != count && gtid == 0)
-            flag_error(p.status, DEV_CAPACITY);
-        int held[SPAN], now[SPAN];     // pages before and after
-        int ask = 0, back = 0;
-#pragma unroll
-        for (int i = 0; i < SPAN; ++i) {
-            held[i] = now[i] = 0;
-            if (u0 + i < units) {
-                int st;
-                const int m = new_tokens(p, (u0 + i) / p.Hkv, st), n = p.n[u0 + i];
-                const int h = p.pages[u0 + i];
-                held[i] = now[i] = h;
-                if (fits(p, n, m) && h >= 0 && h <= per) {
-                    const int need = (n + m + PAGE_SLOTS - 1) / PAGE_SLOTS;
-                    now[i] = p.release || need > h ? need : h;
-                } else {
-                    flag_error(p.status, DEV_CAPACITY);
-                }
-                ask += max(0, now[i] - h);
-                back += max(0, h - now[i]);
-            }
-        }
-        int tx, ty;
-        scan2(ask, back, tx, ty);
-#pragma unroll
-        for (int i = 0; i < SPAN; ++i) {
-            sm.held[tid * SPAN + i] = held[i];
-            sm.grow[tid * SPAN + i] = ask;
-            sm.back[tid * SPAN + i] = back;
-            ask += max(0, now[i] - held[i]);
-            back += max(0, held[i] - now[i]);
-        }
-        if (tid == 0) {
-            s_sum[0] = tx;
-            s_sum[1] = ty;
-            s_sum[2] = 0;
-            sm.grow[THREADS * SPAN] = tx;
-            sm.back[THREADS * SPAN] = ty;
-        }
-        cluster_sync_all();
-        // pages asked for and given back in all, and before this CTA's first unit
-        const int r_ask = lane < CTAS ? ld_cluster_s32(&s_sum[0], lane) : 0;
-        const int r_back = lane < CTAS ? ld_cluster_s32(&s_sum[1], lane) : 0;
-        const int total = __reduce_add_sync(0xffffffffu, r_ask);
-        const int before = __reduce_add_sync(0xffffffffu, lane < rank ? r_ask : 0);
-        const int back0 = __reduce_add_sync(0xffffffffu, lane < rank ? r_back : 0);
-        n_back = __reduce_add_sync(0xffffffffu, r_back);
-        // ---- grants: a unit that the stack cannot serve in full keeps what it has.  Units
-        // are served in order, so those served are the ones up to some unit and those that
-        // ask for nothing.
-        int granted = 0;
-#pragma unroll
-        for (int i = 0; i < SPAN; ++i) {
-            const int g = max(0, now[i] - held[i]);
-            if (g && before + sm.grow[tid * SPAN + i] + g > count) {
-                now[i] = held[i];
-                flag_error(p.status, DEV_CAPACITY);
-            } else {
-                granted += g;
-            }
-            if (u0 + i < units)
-                p.pages_out[u0 + i] = now[i];
-        }
-        int taken = total, mine = tx;   // pages taken in all, and by this CTA
-        if (total > count) {   // the same on every CTA of the cluster
-            granted = __reduce_add_sync(0xffffffffu, granted);
-            if (lane == 0)
-                atomicAdd(&s_sum[2], granted);
-            cluster_sync_all();
-            taken = __reduce_add_sync(0xffffffffu,
-                                      lane < CTAS ? ld_cluster_s32(&s_sum[2], lane) : 0);
-            mine = s_sum[2];
-        }
-        left = count - taken;
-        // ---- new pages of the CTA's units, the next ones of the stack
-        for (int x = tid; x < mine; x += THREADS) {
-            const int i = last_at_most(sm.grow, THREADS * SPAN, x);
-            p.table_out[(size_t)(cta_u0 + i) * per + sm.held[i] + x - sm.grow[i]] =
-                p.free_list[count - 1 - before - x];
-        }
-        if (p.free_out != p.free_list)
-            copy_i32(p.free_out, p.free_list, left, gtid);
-        cluster_sync_all();   // every new page is taken, every page count written
-        // ---- returned pages go on the stack in unit order
-        for (int x = tid; x < ty; x += THREADS) {
-            const int i = last_at_most(sm.back, THREADS * SPAN, x);
-            const int gave = sm.back[i + 1] - sm.back[i];
-            const size_t e = (size_t)(cta_u0 + i) * per + sm.held[i] - gave + x - sm.back[i];
-            const int pg = p.table[e], to = left + back0 + x;
-            p.table_out[e] = -1;
-            if (to < p.num_pages)
-                p.free_out[to] = pg;
-            else
-                flag_error(p.status, DEV_CAPACITY);
-        }
-    } else {
-        for (int u = gtid; u < units; u += gsize) {
-            int st;
-            if (!fits(p, p.n[u], new_tokens(p, u / p.Hkv, st)))
-                flag_error(p.status, DEV_CAPACITY);
-        }
-    }
-
-    // ---- slot map and positions
-    backwards = __syncthreads_or(backwards);
-    if (p.T <= CLUSTER_TOKENS) {
-        // a thread per token, warps dealt to the CTAs in turn
-        for (int t = ((tid >> 5) * CTAS + rank) * 32 + lane; t < p.T; t += gsize)
-            plan_token<false>(p, t, p.B <= CU_CACHE ? sm.cu : p.cu, backwards);
-    } else {
-        // the first token of each unit; k_plan_tokens follows with the others
-        for (int u = gtid; u < units; u += gsize) {
-            int start;
-            const int b = u / p.Hkv, m = new_tokens(p, b, start), n = p.n[u];
-            if (m == 0)
-                continue;
-            int row = -1;
-            if (takes(p, u, n, m)) {
-                row = slot_row(p, u, n);
-                p.pos[(size_t)u * p.C + n] = p.seqlen[b];
-            }
-            p.slot_map[(size_t)start * p.Hkv + u - b * p.Hkv] = row;
-        }
-    }
-    cluster_sync_all();   // the old counts have been read everywhere
-
-    // ---- counts
-    for (int u = gtid; u < units; u += gsize) {
-        int st;
-        const int m = new_tokens(p, u / p.Hkv, st), n = p.n[u];
-        p.n_out[u] = takes(p, u, n, m) ? n + m : n;
-    }
-    for (int b = gtid; b < p.B; b += gsize) {
-        int st;
-        const int m = new_tokens(p, b, st);
-        const int before = p.cu[b], after = p.cu[b + 1];
-        if (after != before && m == 0)
-            flag_error(p.status, DEV_CAPACITY);   // a range outside the batch
-        p.seqlen_out[b] = p.seqlen[b] + m;
-    }
-    if (p.table && gtid == 0)
-        *p.count_out = min(left + n_back, p.num_pages);
-}
-
-// The other tokens of a large batch, a thread per token.  Launched so that its CTAs may
-// start while the plan still runs: they wait for it before they read what it wrote.
-__global__ void __launch_bounds__(256) k_plan_tokens(const PlanLaunch p)
-{
-    __shared__ int s_cu[CU_CACHE];
-    bool backwards = false;
-    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
-        const int c0 = p.cu[b], c1 = p.cu[b + 1];
-        backwards |= c1 < c0;
-        if (b < CU_CACHE)
-            s_cu[b] = c0;
-    }
-    backwards = __syncthreads_or(backwards);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int t = blockIdx.x * blockDim.x + threadIdx.x;
-    if (t < p.T)
-        plan_token<true>(p, t, p.B <= CU_CACHE ? s_cu : p.cu, backwards);
-}
-
 // Rows of the packed new tokens to the cache.  Each thread copies 16 bytes of K and
 // of V per step.
 __global__ void __launch_bounds__(256) k_append_packed(const PackedLaunch p)
@@ -459,7 +446,7 @@ __global__ void __launch_bounds__(256) k_append_packed(const PackedLaunch p)
 template <int SPAN> static cudaError_t plan_impl(const PlanLaunch &p, cudaStream_t s)
 {
     const void *f = reinterpret_cast<const void *>(k_append_plan<SPAN>);
-    cudaError_t e = set_smem_once(f, sizeof(PlanSmem<SPAN>), true);
+    cudaError_t e = set_smem_once(f, sizeof(PlanSmem<SPAN>));
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg{};

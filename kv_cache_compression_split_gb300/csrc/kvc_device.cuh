@@ -65,6 +65,17 @@ __device__ __forceinline__ void cluster_sync_all()
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The two halves of cluster_sync_all.
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // fp32 load from the shared memory of CTA `rank` of this cluster, at the offset
 // that `local` has in this CTA's shared memory.
 __device__ __forceinline__ float ld_cluster_f32(const float *local, uint32_t rank)

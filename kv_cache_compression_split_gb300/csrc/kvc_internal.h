@@ -22,8 +22,7 @@ int sm_count();
 
 // Raise the dynamic shared-memory limit of kernel `func` to `bytes` on the current
 // device, once per (kernel, device); thread safe.  Returns the attribute call's error.
-// wide_cluster: the kernel may also run in clusters of 16 CTAs.
-cudaError_t set_smem_once(const void *func, int bytes, bool wide_cluster = false);
+cudaError_t set_smem_once(const void *func, int bytes);
 
 // CTAs of `func` (threads per CTA, dynamic shared memory) resident on all SMs of the
 // current device together (at least one per SM), cached per (kernel, device).
