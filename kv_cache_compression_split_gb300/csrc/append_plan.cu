@@ -7,14 +7,20 @@
 // unit order, so every unit needs the sum of grow over the units before it; the
 // returned pages go on what is left of the stack, placed by the same sum of back.
 // Integer work of a few bytes per unit and token: latency bound.  One thread-block
-// cluster does it in one launch, because the sums run over all units and the
-// outputs may be the inputs: every CTA scans its range of units, the totals cross
-// through distributed shared memory, and cluster barriers part the reads of the
-// old state from the writes of the new.
+// cluster scans the units, since the sums run over all of them: every CTA its range, the
+// totals through distributed shared memory.  All that is read of the old state is read
+// before the cluster barrier, so the outputs may be the inputs, and a second barrier is
+// needed only where returned pages go on the stack that others still take from.  What
+// has many words is dealt evenly over threads that find their unit by bisecting the sums.
+// 512 sequences of 8 heads, one new token each: 10.6 us, of which an empty batch takes 7
+// (the cluster's start, one round of loads, the barrier) and the copy of the 0.5 MB table
+// and the 0.5 MB stack to other arrays most of the rest; 96 ragged prompts, 33 K tokens:
+// 12.3 us (a kernel on all SMs writes their slot map).
 //
 // kvc_append_packed: one 16-byte chunk of a K and of a V row per thread and step,
 // written to the row that the slot map names.  HBM bound: 2 D bytes read and
-// written per row, twice.
+// written per row, twice.  35 K tokens of 8 heads of 128: 291 MB in 46.5 us, 6.2 TB/s,
+// 0.92 of the measured copy rate.
 #include "kvc_device.cuh"
 #include "kvc_internal.h"
 

@@ -34,6 +34,17 @@
 // small area of shared memory per warp, so that a warp stores whole rows: a thread that
 // stores its own row touches 32 lines per instruction, which took 7000 clocks a tile.
 //
+// What bounds it.  Per 128 x 128 block of D = 128 the two products take 1070 clocks of the
+// tensor pipe (a 128 x 128 x 16 product was measured at 64.5 to 67 clocks), the
+// exponentials 520 of the SFU.  The two-tile form spends 1245 clocks a block once it runs:
+// a row's thread needs 1300 for its block (reading 30, maximum 300, exponentials and
+// packing 830, storing 35) while the tensor cores do the other tile's.  8192 tokens of
+// 64 / 8 heads: 690 us, 1590 TFLOP/s, under the power cap (about 1.5 GHz): 0.85 of the
+// measured burst rate, 0.94 of the sustained one.  Shorter prompts pay about 4000 clocks
+// per item between its last product and the next one's.  A batch of few tokens over
+// long caches is HBM bound in the middle (64 KB per SM in 2700 clocks) and spends the
+// rest on the start, the last round and the merge: 131 MB in 35 us.
+//
 // Non-finite values.  A masked score is replaced, not added to, so keys behind a
 // row's range never matter.  A masked value row would enter as 0 * v: rows behind the
 // sequence's last key are cleared in shared memory, and a row whose result is not
@@ -489,7 +500,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 mbar_wait(q_full, (n_q - 1) & 1);
         }
     } else if (warp == W_MMA) {
-        // ------------------------------------------------ MMA issuer (lane 0 issues)
+        // ------------------------------------------------ MMA issuer (an elected lane issues)
         int n_it = 0, n_q = 0;
         int n_p[2] = {0, 0};
         const Int<0> T0;
