@@ -43,7 +43,8 @@
  *     device status word per GPU.  Every call is asynchronous on `stream` and
  *     returns after enqueueing its kernels.
  *   - fp16 means IEEE binary16, passed as uint16_t bit patterns.  All data
- *     must be finite.  Pointers must be 16-byte aligned.
+ *     must be finite (kvc_prompt_attend and kvc_chunk_attend say what becomes of
+ *     values that are not).  Pointers must be 16-byte aligned.
  *   - Head dim D is 64 or 128; Hq is a multiple of Hkv with 1 <= Hq/Hkv <= 8;
  *     query head h reads KV head h / (Hq/Hkv).  Softmax scale defaults to
  *     1/sqrt(D).
@@ -565,7 +566,7 @@ KVC_API kvc_status kvc_prompt_attend(const kvc_prompt_args *args, cudaStream_t s
  *            computed apart and merged
  * A row that sees no slot gives o = 0 and lse = -inf.  A unit whose n leaves [0, C]
  * counts as empty and sets KVC_DEV_CAPACITY; so does a sequence whose range leaves
- * [0, T]; a read through a page outside the pool yields no data and sets it too.
+ * [0, T]; slots of a page outside the pool read as zeros and set it too.
  * Rows of the cache behind n may hold anything.
  * Source: "Rethinking KV Cache Compression" guide, §16 "Prefill、decode、TP 的性能账"
  * and "前置背景、复现方法与结论边界" (the paged cache of continuous batching).

@@ -265,3 +265,58 @@ def test_prompt_lse_feeds_the_heavy_hitter_scores(kvc):
     assert torch.allclose(s1, s2, rtol=1e-4, atol=0)
     assert abs(s1.double().sum().item() - B * Hq * L) < 1e-4 * B * Hq * L
     assert device_status_clean(kvc)
+
+
+def test_captured_step_with_a_padded_batch(kvc):
+    """Plan, packed append and chunk attention captured once for a fixed number of token places
+    and replayed: the lengths are on the device, places behind the last sequence stay idle, and
+    pages are taken and given back in place, step after step."""
+    Hq, Hkv, D, C, B, T = 8, 2, 64, 512, 4, 40
+    g = torch.Generator(device="cuda").manual_seed(9)
+    cache = kvc.SlotCache.empty_paged(B, Hkv, C, D, 70)
+    pool = kvc.PagePool.empty(cache)
+    x = torch.zeros(T, Hq + 2 * Hkv, D, dtype=torch.float16, device="cuda")
+    q, k, v = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    slots = torch.empty(T, Hkv, dtype=torch.int32, device="cuda")
+    o = torch.zeros(T, Hq, D, dtype=torch.float16, device="cuda")
+    ws = torch.empty(max(kvc.kvc_chunk_workspace_size(cache, q) // 4, 4), device="cuda")
+
+    def step():
+        kvc.kvc_append_plan(cache, cu, slots, pool=pool, release=True)
+        kvc.kvc_append_packed(cache, k, v, slots)
+        kvc.kvc_chunk_attend(cache, q, cu, o, workspace=ws)
+
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        step()                      # nothing yet: every sequence brings no token
+        s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            step()
+    rng = np.random.default_rng(4)
+    total = np.zeros(B, int)
+    for it in range(12):
+        m = rng.integers(0, 11, B)
+        x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+        cu.copy_(_cu(m))
+        o.fill_(7.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        total += m
+        assert cache.seqlen.tolist() == total.tolist()
+        for b in range(B):
+            w = slice(int(cu[b]), int(cu[b + 1]))
+            for h in range(Hq):
+                K, V = _gather(cache, b, h // (Hq // Hkv))
+                last = K.shape[0] - m[b] + torch.arange(int(m[b]))
+                check_rows(o[w, h], None, attend_rows(q[w, h], K, V, last), f"step {it} b={b} h={h}")
+        assert (o[int(cu[B]):] == 7.0).all() and (slots[int(cu[B]):] == -1).all()
+        held = [cache.block_table[b, h, :int(pool.pages[b, h])].tolist()
+                for b in range(B) for h in range(Hkv)]
+        assert sorted(sum(held, []) + pool.free[:int(pool.count)].tolist()) == list(range(70))
+        if it % 4 == 3:
+            kvc.kvc_random_evict(cache, 4, 0.3, 11, it)
+    assert device_status_clean(kvc)

@@ -54,6 +54,12 @@ PACKED = [
     (16, 2, 128, [511, 17, 640]),
     (2, 2, 128, [1111]),
     (8, 8, 64, [700, 3]),
+    # above 1024 tokens on average: two tiles per item with 128 channels
+    (8, 1, 128, [1500, 5, 1800]),
+    (16, 2, 128, [1061, 1120]),
+    (7, 1, 128, [1111, 1040]),
+    (3, 3, 128, [1025]),
+    (8, 2, 64, [1500]),
 ]
 
 
@@ -191,6 +197,11 @@ CHUNKS = [
     (6, 2, 128, 2048, True, [[2048, 1500]], [129]),
     (8, 8, 128, 700, False, [[600, 700, 512, 384, 129, 128, 127, 640]], [127]),
     (2, 1, 128, 4096, True, [[4000], [10], [0], [3333]], [1, 10, 0, 4]),
+    # batches that two tiles per item suit: long chunks, and many sequences over long caches
+    (32, 4, 128, 1536, True, [[1500, 1499, 1408, 1345], [777, 900, 1024, 600]], [600, 555]),
+    (6, 2, 128, 1400, False, [[1399, 1300], [1400, 400]], [400, 333]),
+    (64, 8, 128, 4096, True, [[4096 - 3 * i] * 8 for i in range(16)],
+     [16, 17, 1, 0, 15, 16, 33, 16, 16, 9, 16, 16, 16, 20, 16, 16]),
 ]
 
 
@@ -302,7 +313,8 @@ def test_graph_replay_follows_device_lengths(kvc):
     assert device_status_clean(kvc)
 
 
-@pytest.mark.parametrize("Hq,Hkv,D,L", [(8, 1, 128, 300), (4, 4, 64, 200), (6, 2, 128, 90)])
+@pytest.mark.parametrize("Hq,Hkv,D,L", [(8, 1, 128, 300), (4, 4, 64, 200), (6, 2, 128, 90),
+                                        (8, 1, 128, 1300), (3, 3, 128, 1200)])
 def test_prompt_non_finite_rows_stay_with_the_rows_that_attend_them(kvc, Hq, Hkv, D, L):
     """Infinities and NaN in single key and value rows: rows before them, which do not attend
     them, are what they are without them; rows from them on are what the formula gives: NaN
@@ -337,7 +349,7 @@ def test_prompt_non_finite_rows_stay_with_the_rows_that_attend_them(kvc, Hq, Hkv
 
 
 @pytest.mark.parametrize("splits", [1, 4])
-@pytest.mark.parametrize("m", [[3, 1], [60, 1], [150, 2]])
+@pytest.mark.parametrize("m", [[3, 1], [60, 1], [150, 2], [400, 390]])
 def test_chunk_non_finite_values_behind_a_row(kvc, m, splits):
     """The chunk's later value rows are infinite or NaN: the earlier rows do not attend them."""
     gen = _gen(sum(m))
@@ -387,4 +399,81 @@ def test_chunk_many_items_per_cta(kvc, D, most):
     for _ in range(5):
         kvc.kvc_chunk_attend(cache, q, _cu(m), o, lse=lse, workspace=ws)
         assert torch.equal(o, first)          # the same inputs give the same bits
+    assert device_status_clean(kvc)
+
+
+def test_prompt_lens_outside_the_padding_are_empty(kvc):
+    gen = _gen(21)
+    q, k, v = _randn(gen, 3, 2, 40, 64), _randn(gen, 3, 1, 40, 64), _randn(gen, 3, 1, 40, 64)
+    o = torch.full_like(q, 7.0)
+    lens = torch.tensor([41, -1, 40], dtype=torch.int32, device="cuda")
+    kvc.kvc_prompt_attend(q, k, v, o, lens=lens)
+    torch.cuda.synchronize()
+    assert kvc.kvc_read_device_status() == kvc.KVC_DEV_CAPACITY
+    assert (o[:2] == 7.0).all()
+    for h in range(2):
+        check_rows(o[2, h], None, attend_rows(q[2, h], k[2, 0], v[2, 0], torch.arange(40)))
+
+
+def test_element_offsets_beyond_32_bits(kvc):
+    """Rows 8 million elements apart in a prompt, and pages at the end of pools of more than
+    2^31 elements in a chunk."""
+    gen = _gen(22)
+    T, D, step = 300, 128, 8_000_000
+    wide = torch.zeros(T * step, dtype=torch.float16, device="cuda")
+    view = wide.as_strided((T, 4, D), (step, D, 1))
+    x = _randn(gen, T, 4, D)
+    view.copy_(x)
+    o = torch.empty(T, 2, D, dtype=torch.float16, device="cuda")
+    kvc.kvc_prompt_attend(view[:, :2], view[:, 2:3], view[:, 3:], o, cu_seqlens=_cu([T]))
+    check_prompt(x[:, :2], x[:, 2:3], x[:, 3:], o, None, _cu([T]), [T], 2, 1)
+    del wide, view
+    num = 280_000
+    n = [[500, 77]]
+    small, K, V = _cache(kvc, gen, n, 512, D, True)
+    big = kvc.SlotCache(K=torch.empty(num, 64, D, dtype=torch.float16, device="cuda"),
+                        V=torch.empty(num, 64, D, dtype=torch.float16, device="cuda"),
+                        pos=small.pos, n=small.n, seqlen=small.seqlen,
+                        block_table=torch.where(small.block_table >= 0,
+                                                num - 1 - small.block_table, -1).int())
+    for j in range(small.num_pages):
+        big.K[num - 1 - j], big.V[num - 1 - j] = small.K[j], small.V[j]
+    assert big.K.numel() > 2 ** 31
+    q = _randn(gen, 3, 8, D)
+    o = torch.empty_like(q)
+    ws = torch.empty(max(kvc.kvc_chunk_workspace_size(big, q) // 4, 4), device="cuda")
+    kvc.kvc_chunk_attend(big, q, _cu([3]), o, workspace=ws)
+    check_chunk(q, K, V, n, [3], o, None, 8)
+    # the packed append at the same end
+    new = _randn(gen, 5, 2, D)
+    slots = torch.arange(num * 64 - 10, num * 64, dtype=torch.int32, device="cuda").reshape(5, 2)
+    kvc.kvc_append_packed(big, new, new, slots)
+    assert torch.equal(big.K.view(-1, D)[-10:], new.reshape(-1, D))
+    assert torch.equal(big.V.view(-1, D)[-10:], new.reshape(-1, D))
+    assert device_status_clean(kvc)
+
+
+def test_two_streams_at_once(kvc):
+    """Calls on two streams, each with its own workspace, do not disturb each other."""
+    gen = _gen(23)
+    n = [[900, 1000], [700, 1024], [513, 64]]
+    cache, K, V = _cache(kvc, gen, n, 1024, 128, True)
+    m = [3, 1, 5]
+    qs = [_randn(gen, 9, 8, 128) for _ in range(2)]
+    os_ = [torch.empty_like(q) for q in qs]
+    wss = [torch.empty(max(kvc.kvc_chunk_workspace_size(cache, q, 4) // 4, 4), device="cuda") for q in qs]
+    L = 700
+    x = _randn(gen, L, 10, 128)
+    po, cu, cum = torch.empty(L, 8, 128, dtype=torch.float16, device="cuda"), _cu([L]), _cu(m)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for i in range(2):
+            kvc.kvc_chunk_attend(cache, qs[i], cum, os_[i], workspace=wss[i], num_splits=4,
+                                 stream=streams[i])
+        kvc.kvc_prompt_attend(x[:, :8], x[:, 8:9], x[:, 9:], po, cu_seqlens=cu, stream=streams[0])
+    torch.cuda.synchronize()
+    for i in range(2):
+        check_chunk(qs[i], K, V, n, m, os_[i], None, 8)
+    check_prompt(x[:, :8], x[:, 8:9], x[:, 9:], po, None, cu, [L], 8, 1)
     assert device_status_clean(kvc)
