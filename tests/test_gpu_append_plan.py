@@ -320,3 +320,64 @@ def test_captured_step_with_a_padded_batch(kvc):
         if it % 4 == 3:
             kvc.kvc_random_evict(cache, 4, 0.3, 11, it)
     assert device_status_clean(kvc)
+
+
+def test_captured_calls_on_forked_streams(kvc):
+    """A graph in which two streams fork from one and join again, with these calls at the fork,
+    on both branches and behind the join."""
+    Hq, Hkv, D, C, B = 8, 2, 128, 512, 3
+    g = torch.Generator(device="cuda").manual_seed(31)
+    lens = [100, 64, 300]
+    T = sum(lens)
+    x = torch.randn(T, Hq + 2 * Hkv, D, generator=g, device="cuda").half()
+    q, k, v = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+    caches = [kvc.SlotCache.empty_paged(B, Hkv, C, D, 60) for _ in range(2)]
+    pools = [kvc.PagePool.empty(c) for c in caches]
+    slots = [torch.empty(T, Hkv, dtype=torch.int32, device="cuda") for _ in range(2)]
+    os_ = [torch.empty(T, Hq, D, dtype=torch.float16, device="cuda") for _ in range(3)]
+    ws = [torch.empty(max(kvc.kvc_chunk_workspace_size(caches[0], q, 3) // 4, 4), device="cuda")
+          for _ in range(2)]
+    cu = _cu(lens)
+    s0, s1 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def both():
+        kvc.kvc_prompt_attend(q, k, v, os_[2], cu_seqlens=cu, stream=s0)
+        s1.wait_stream(s0)
+        for i, s in enumerate((s0, s1)):
+            kvc.kvc_append_plan(caches[i], cu, slots[i], pool=pools[i], stream=s)
+            kvc.kvc_append_packed(caches[i], k, v, slots[i], stream=s)
+            kvc.kvc_chunk_attend(caches[i], q, cu, os_[i], workspace=ws[i], num_splits=3, stream=s)
+        s0.wait_stream(s1)
+        kvc.kvc_append_packed(caches[0], k, v, slots[0], stream=s0)
+
+    def fresh():
+        for c, p in zip(caches, pools):
+            c.n.zero_()
+            c.seqlen.zero_()
+            c.block_table.fill_(-1)
+            p.pages.zero_()
+            p.free.copy_(torch.arange(59, -1, -1))
+            p.count.fill_(60)
+        torch.cuda.synchronize()
+
+    with torch.cuda.stream(s0):
+        both()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s0):
+            both()
+    for _ in range(3):
+        fresh()
+        for o in os_:
+            o.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for b in range(B):
+            w = slice(int(cu[b]), int(cu[b + 1]))
+            for h in range(Hq):
+                ref = attend_rows(q[w, h], k[w, h // 4], v[w, h // 4], torch.arange(lens[b]))
+                for o in os_:
+                    check_rows(o[w, h], None, ref, f"b={b} h={h}")
+    assert device_status_clean(kvc)
