@@ -454,14 +454,12 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                     }
                     ++n_it;
                 };
-                // The order in which the MMA warp takes them.  The first blocks go ahead of
-                // the query tile, whose place is free only when the last item's scores are
-                // done.
+                // The order in which the MMA warp takes them: the first keys, then the query
+                // tile (its place is free when the last item's scores are done), then values,
+                // which wait for a place in the ring behind the last item's.
                 const int ahead = TILES == 1 || it.two ? 2 : 1;
                 for (int i = 0; ok && i < ahead && i < n; ++i)
                     load(&maps.k, it.j0 + i);
-                if (ok)
-                    load(&maps.v, it.j0);
                 if (ok && n_q > 0)
                     ok = mbar_sleep_or_abort(q_empty, (n_q - 1) & 1, abort);
                 if (ok) {
@@ -475,8 +473,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                     ++n_q;
                 }
                 for (int i = 0; ok && i < n; ++i) {
-                    if (i > 0)
-                        load(&maps.v, it.j0 + i);
+                    load(&maps.v, it.j0 + i);
                     if (ok && i + ahead < n)
                         load(&maps.k, it.j0 + i + ahead);
                 }
