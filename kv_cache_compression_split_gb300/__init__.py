@@ -188,33 +188,57 @@ def _state_without_desc(obj):
 
 
 
-def _rows(t, what, dims, dev):
-    """Device address and strides of binary16 rows: a tensor of `dims` dimensions whose last
-    one is contiguous; the others may have any strides, which the call passes on."""
-    if t.dtype is not torch.float16:
-        raise ValueError(f"kvc: {what} must be float16, got {t.dtype}")
+_F16, _F32, _I32 = torch.float16, torch.float32, torch.int32
+
+
+class _Refused(Exception):
+    """Rows that a call does not take; _explain says why."""
+
+
+def _rows(t, shape, dev):
+    """Device address and strides of binary16 rows of this shape: the last dimension is
+    contiguous, the others may have any strides, which the call passes on."""
     st = t.stride()
-    if len(st) != dims or (st[-1] != 1 and t.shape[-1] > 1):
-        raise ValueError(f"kvc: {what} must have {dims} dimensions, the last one contiguous")
-    if t.get_device() != dev:
-        _wrong_device(t, dev)
-    if 1 in t.shape:   # a dimension of size 1 is never stepped over: any stride stands for it
-        st = tuple(8 if n == 1 else x for n, x in zip(t.shape, st))
+    if (t.dtype is not _F16 or t.shape != shape or t.get_device() != dev or
+            (st[-1] != 1 and shape[-1] != 1)):
+        raise _Refused
+    if 1 in shape:   # a dimension of size 1 is never stepped over: any stride stands for it
+        st = tuple([8 if n == 1 else x for n, x in zip(shape, st)])
     return t.data_ptr(), st
+
+
+def _explain(rows, dev, index):
+    """Raise what is wrong with one of these (name, tensor, shape): the rows of a call and the
+    int32 tensor that goes with them.  Types and shapes come before the device."""
+    for what, t, _ in rows:
+        if t.dtype is not _F16:
+            raise ValueError(f"kvc: {what} must be float16, got {t.dtype}")
+    for what, t, shape in rows:
+        if t.shape != shape:
+            raise ValueError(f"kvc: {what} must be of shape {tuple(shape)}, got "
+                             f"{tuple(t.shape)}: the arguments do not belong together")
+    what, t, shape = index
+    if t is not None and (t.dtype is not _I32 or t.shape != shape):
+        _typed(t, what, _I32, shape, dev)
+    for what, t, _ in rows:
+        if t.get_device() != dev:
+            _wrong_device(t, dev)
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError(f"kvc: the last dimension of {what} must be contiguous")
 
 
 def _typed(t, what, dtype, shape, dev):
     """Device address of a contiguous tensor of this type and shape (0 for None)."""
     if t is None:
         return 0
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"kvc: {what} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of "
                          f"{tuple(t.shape)}")
     if t.get_device() != dev:
         _wrong_device(t, dev)
-    if not t.is_contiguous():
-        raise ValueError("kvc: tensor arguments must be contiguous")
-    return t.data_ptr()
+    raise ValueError("kvc: tensor arguments must be contiguous")
 
 
 def _wrong_device(t, dev):
@@ -435,35 +459,43 @@ def kvc_prompt_attend(q, k, v, o, cu_seqlens=None, lens=None, lse=None,
     [T, Hkv, D], cu_seqlens [B + 1] int32, lse [Hq, T].  Padded: q, o [B, Hq, L, D], k, v
     [B, Hkv, >= L, D], optional lens [B] int32, lse [B, Hq, L].  Rows may be strided."""
     dev, stream = _device(stream)
+    shape = q.shape
     if cu_seqlens is not None:
         if lens is not None:
             raise ValueError("kvc_prompt_attend takes cu_seqlens (packed) or lens (padded)")
-        L, Hq, D = q.shape
+        L, Hq, D = shape
         Hkv = k.shape[1]
-        B, dims = cu_seqlens.numel() - 1, 3
-        kv, rows = (L, Hkv, D), (Hq, L)
+        kv = (L, Hkv, D)
+        B = cu_seqlens.numel() - 1
+        try:
+            qp, (q2, q1, _) = _rows(q, shape, dev)
+            kp, (k2, k1, _) = _rows(k, kv, dev)
+            vp, (v2, v1, _) = _rows(v, kv, dev)
+            op, (o2, o1, _) = _rows(o, shape, dev)
+        except _Refused:
+            _explain((("q", q, shape), ("k", k, kv), ("v", v, kv), ("o", o, shape)), dev,
+                     ("cu_seqlens", cu_seqlens, (B + 1,)))
+        args = _pack_prompt(B, Hq, Hkv, D, L, qp, kp, vp, op,
+                            0 if lse is None else _typed(lse, "lse", _F32, (Hq, L), dev),
+                            _typed(cu_seqlens, "cu_seqlens", _I32, (B + 1,), dev), 0, 0, q1, q2, 0,
+                            k1, k2, 0, v1, v2, 0, o1, o2, softmax_scale)
     else:
-        B, Hq, L, D = q.shape
+        B, Hq, L, D = shape
         Hkv = k.shape[1]
-        dims = 4
-        kv, rows = (B, Hkv, L, D), (B, Hq, L)
         if k.dim() == 4 and k.shape[2] > L:
             k = k[:, :, :L]
         if v.dim() == 4 and v.shape[2] > L:
             v = v[:, :, :L]
-    if k.shape != kv or v.shape != kv or o.shape != q.shape:
-        raise ValueError(f"kvc_prompt_attend: q {tuple(q.shape)}, k {tuple(k.shape)}, v "
-                         f"{tuple(v.shape)}, o {tuple(o.shape)} do not belong together")
-    cu = _typed(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
-    ln = _typed(lens, "lens", torch.int32, (B,), dev)
-    ls = _typed(lse, "lse", torch.float32, rows, dev)
-    (qp, qs), (kp, ks) = _rows(q, "q", dims, dev), _rows(k, "k", dims, dev)
-    (vp, vs), (op, os_) = _rows(v, "v", dims, dev), _rows(o, "o", dims, dev)
-    if dims == 3:
-        args = _pack_prompt(B, Hq, Hkv, D, L, qp, kp, vp, op, ls, cu, ln, 0, qs[1], qs[0], 0, ks[1],
-                            ks[0], 0, vs[1], vs[0], 0, os_[1], os_[0], softmax_scale)
-    else:
-        args = _pack_prompt(B, Hq, Hkv, D, L, qp, kp, vp, op, ls, cu, ln, *qs[:3], *ks[:3], *vs[:3],
+        kv = (B, Hkv, L, D)
+        try:
+            (qp, qs), (kp, ks) = _rows(q, shape, dev), _rows(k, kv, dev)
+            (vp, vs), (op, os_) = _rows(v, kv, dev), _rows(o, shape, dev)
+        except _Refused:
+            _explain((("q", q, shape), ("k", k, kv), ("v", v, kv), ("o", o, shape)), dev,
+                     ("lens", lens, (B,)))
+        args = _pack_prompt(B, Hq, Hkv, D, L, qp, kp, vp, op,
+                            0 if lse is None else _typed(lse, "lse", _F32, (B, Hq, L), dev), 0,
+                            _typed(lens, "lens", _I32, (B,), dev), *qs[:3], *ks[:3], *vs[:3],
                             *os_[:3], softmax_scale)
     _check((_lib or lib()).kvc_prompt_attend(args, stream), "kvc_prompt_attend")
 
@@ -483,17 +515,22 @@ def kvc_chunk_attend(cache: "SlotCache", q, cu_new, o, lse=None, workspace=None,
     int32 (rows may be strided), lse [Hq, T]."""
     dev, stream = _device(stream)
     d = cache.desc()
-    T, Hq, D = q.shape
-    if D != d.D or o.shape != q.shape:
-        raise ValueError(f"kvc_chunk_attend: q and o must be [T, Hq, {d.D}], got "
-                         f"{tuple(q.shape)} and {tuple(o.shape)}")
-    cu = _typed(cu_new, "cu_new", torch.int32, (d.B + 1,), dev)
-    ls = _typed(lse, "lse", torch.float32, (Hq, T), dev)
-    (qp, qs), (op, os_) = _rows(q, "q", 3, dev), _rows(o, "o", 3, dev)
-    ws = _ptr(workspace) or 0
-    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    args = _pack_chunk(Hq, T, C.addressof(d), qp, op, cu, ls, qs[1], qs[0], os_[1], os_[0], ws,
-                       size, num_splits, softmax_scale)
+    shape = q.shape
+    T, Hq, D = shape
+    if D != d.D:
+        raise ValueError(f"kvc_chunk_attend: q must be [T, Hq, {d.D}], got {tuple(shape)}")
+    try:
+        qp, (q2, q1, _) = _rows(q, shape, dev)
+        op, (o2, o1, _) = _rows(o, shape, dev)
+    except _Refused:
+        _explain((("q", q, shape), ("o", o, shape)), dev, ("cu_new", cu_new, (d.B + 1,)))
+    ws = size = 0
+    if workspace is not None:
+        ws, size = _ptr(workspace), workspace.nbytes
+    args = _pack_chunk(Hq, T, C.addressof(d), qp, op,
+                       _typed(cu_new, "cu_new", _I32, (d.B + 1,), dev),
+                       0 if lse is None else _typed(lse, "lse", _F32, (Hq, T), dev), q1, q2, o1, o2,
+                       ws, size, num_splits, softmax_scale)
     _check((_lib or lib()).kvc_chunk_attend(args, stream), "kvc_chunk_attend")
 
 
@@ -510,9 +547,9 @@ def kvc_append_plan(cache: "SlotCache", cu_new, slot_map, pool: "Optional[PagePo
     po = pool_out.desc(n, dev) if pool_out is not None else pi
     T = slot_map.shape[0]
     _check((_lib or lib()).kvc_append_plan(
-        C.addressof(d), pi, _typed(cu_new, "cu_new", torch.int32, (d.B + 1,), dev), T,
+        C.addressof(d), pi, _typed(cu_new, "cu_new", _I32, (d.B + 1,), dev), T,
         1 if release else 0, C.addressof(n), po,
-        _typed(slot_map, "slot_map", torch.int32, (T, d.Hkv), dev), stream), "kvc_append_plan")
+        _typed(slot_map, "slot_map", _I32, (T, d.Hkv), dev), stream), "kvc_append_plan")
 
 
 def kvc_append_packed(cache: "SlotCache", k_new, v_new, slot_map, stream=None):
@@ -520,14 +557,17 @@ def kvc_append_packed(cache: "SlotCache", k_new, v_new, slot_map, stream=None):
     slot_map [T, Hkv] names (kvc_append_plan writes it); n and pos are not touched."""
     dev, stream = _device(stream)
     d = cache.desc()
-    T = slot_map.shape[0]
-    shape = (T, d.Hkv, d.D)
-    if k_new.shape != shape or v_new.shape != shape:
-        raise ValueError(f"kvc_append_packed: k_new and v_new must be {shape}")
-    (kp, ks), (vp, vs) = _rows(k_new, "k_new", 3, dev), _rows(v_new, "v_new", 3, dev)
+    T, H = slot_map.shape[0], d.Hkv
+    shape = (T, H, d.D)
+    try:
+        kp, (k0, k1, _) = _rows(k_new, shape, dev)
+        vp, (v0, v1, _) = _rows(v_new, shape, dev)
+    except _Refused:
+        _explain((("k_new", k_new, shape), ("v_new", v_new, shape)), dev,
+                 ("slot_map", slot_map, (T, H)))
     _check((_lib or lib()).kvc_append_packed(
-        C.addressof(d), kp, _pack_2q(ks[0], ks[1]), vp, _pack_2q(vs[0], vs[1]), T,
-        _typed(slot_map, "slot_map", torch.int32, (T, d.Hkv), dev), stream), "kvc_append_packed")
+        C.addressof(d), kp, _pack_2q(k0, k1), vp, _pack_2q(v0, v1), T,
+        _typed(slot_map, "slot_map", _I32, (T, H), dev), stream), "kvc_append_packed")
 
 
 def kvc_read_device_status(stream=None) -> int:
@@ -632,10 +672,9 @@ class PagePool:
 
     def desc(self, cache: SlotCacheDesc, dev: int) -> bytes:
         """The kvc_page_pool struct (the fields of PagePoolDesc) for a cache's descriptor."""
-        i32 = torch.int32
-        return _pack_3p(_typed(self.pages, "pages", i32, (cache.B, cache.Hkv), dev),
-                        _typed(self.free, "free", i32, (cache.num_pages,), dev),
-                        _typed(self.count, "count", i32, (1,), dev))
+        return _pack_3p(_typed(self.pages, "pages", _I32, (cache.B, cache.Hkv), dev),
+                        _typed(self.free, "free", _I32, (cache.num_pages,), dev),
+                        _typed(self.count, "count", _I32, (1,), dev))
 
 
 @dataclass
