@@ -266,7 +266,7 @@ __device__ __forceinline__ float prob64(uint32_t taddr, const float (&x)[64], fl
 // row whose tensor-core result is not finite although its sum l is.
 __device__ __noinline__ void row_again(const TokensLaunch &p, const TokItem &it, const uint16_t *q,
                                        int first, int last, float ref, int c0, float scale,
-                                       uint16_t *o, float *part)
+                                       uint16_t *o, float4 *part, long stride)
 {
     float acc[32];
 #pragma unroll
@@ -285,11 +285,13 @@ __device__ __noinline__ void row_again(const TokensLaunch &p, const TokItem &it,
             acc[c] = fmaf(w, __half2float(__ushort_as_half(v[c0 + c])), acc[c]);
     }
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
+    for (int c = 0; c < 32; c += 4) {
         if (part)
-            part[c0 + c] = acc[c];
+            part[(c0 + c) / 4 * stride] = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
         else
-            o[c0 + c] = __half_as_ushort(__float2half_rn(acc[c] * scale));
+#pragma unroll
+            for (int x = c; x < c + 4; ++x)
+                o[c0 + x] = __half_as_ushort(__float2half_rn(acc[x] * scale));
     }
 }
 
@@ -796,7 +798,14 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
             // ---- results
             const int head = it.hk * g + r_head;
             const int tok = it.start + rg.tok + r_tok;
-            const long row = (long)tok * p.Hq + head;       // of the parts
+            // Parts: of a split and KV head, the references and sums of its rows, and its rows'
+            // values four channels at a time, so that a warp's rows are adjacent.
+            const long rows = (long)p.L * g;
+            auto part_at = [&](long per) {   // of `per` entries per row
+                return ((long)it.split * p.Hkv + it.hk) * per * rows +
+                       (long)(it.start + rg.tok) * g + r;
+            };
+            auto part_o = [&] { return reinterpret_cast<float4 *>(p.part_o) + part_at(D / 4); };
             auto o_row = [&] {
                 return p.o + (p.cu ? 0 : it.b) * p.os[0] + head * p.os[1] + tok * p.os[2];
             };
@@ -936,11 +945,10 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 // parts of rows, and tiles that end inside a warp's rows: each thread stores
                 // its own row
                 if (real && part) {
-                    float *to = p.part_o + (row * p.splits + it.split) * D + c;
+                    float4 *to = part_o() + c / 4 * rows;
 #pragma unroll
                     for (int u = 0; u < 32; u += 4)
-                        *reinterpret_cast<float4 *>(to + u) =
-                            make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
+                        to[u / 4 * rows] = make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
                 } else if (real) {
                     uint16_t *to = o_row() + c;
 #pragma unroll
@@ -966,11 +974,11 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                     if (again && bad >> (c0 / 32) & 1)
                         row_again(p, it, q, it.j0 * TK, min(last, it.j1 * TK - 1),
                                   m == -INFINITY ? 0.f : m, c0, inv, o_row(),
-                                  part ? p.part_o + (row * p.splits + it.split) * D : nullptr);
+                                  part ? part_o() : nullptr, rows);
             }
             if (real) {
                 if (part)
-                    p.part_ml[row * p.splits + it.split] = make_float2(m, lsum);
+                    p.part_ml[part_at(1)] = make_float2(m, lsum);
                 else if (p.lse)
                     p.lse[(p.cu ? 0 : it.b) * p.ls[0] + head * p.ls[1] + tok] =
                         lsum > 0.f ? (m + __log2f(lsum)) * LN2 : lsum == 0.f ? -INFINITY : lsum;
@@ -991,21 +999,26 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
         flag_error(p.status, DEV_TIMEOUT);
 }
 
-// Merges the splits of a row.  A warp per row, or (WARPS = 4, many splits) a CTA per row
-// whose warps take every fourth split and meet in shared memory; four parts' loads are in
-// flight together.  Launched so that it may start while the attention still runs; it
+// Merges the splits.  A warp takes eight rows of a KV head and 16 channels, a lane four
+// channels of a row.  WARPS = 4: the CTA's warps take every fourth split and meet in shared
+// memory; WARPS = 1: each has channels of its own.  References, sums and values of U splits
+// are in flight together, none waits for another.  The kernel runs once through code that
+// no cache holds, so a split too many in U costs as much as a round of loads: U = 8 for the
+// 8 splits of 2048 rows, two per warp, takes 1.7 us more than U = 4, and U = 4 for 38 splits
+// 1.1 us more than U = 8.  Launched so that it may start while the attention still runs; it
 // waits before it reads the parts.
 constexpr int MAX_SPLITS = 64;
-template <int D, int WARPS>
-__global__ void __launch_bounds__(128) k_combine_tokens(const TokensLaunch p)
+template <int D, int WARPS, int U>
+__global__ void __launch_bounds__(128) k_combine_tokens(const TokensLaunch p, const int g)
 {
-    constexpr int V = D / 32;             // channels per lane
-    constexpr int U = 4;
-    __shared__ __align__(16) float s_acc[WARPS][D];
-    const int warp = WARPS == 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long row = WARPS == 1 ? (long)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
-    const int tok = (int)(row / p.Hq), head = (int)(row % p.Hq);
-    int lo = 0, hi = p.B;   // the last sequence that starts at or before the token
+    __shared__ float2 s_ml[WARPS][32];
+    __shared__ float4 s_acc[WARPS][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split0 = WARPS > 1 ? warp : 0;
+    const int c4 = 4 * (WARPS > 1 ? blockIdx.z : 4 * blockIdx.z + warp) + (lane >> 3);
+    const int rows = p.L * g, row = blockIdx.x * 8 + (lane & 7);
+    const int tok = (unsigned)row / (unsigned)g, head = blockIdx.y * g + row - tok * g;
+    int lo = 0, hi = p.B;   // the first sequence that ends behind the token
     while (lo < hi) {
         const int mid = (lo + hi) / 2;
         if (p.cu[mid + 1] <= tok)
@@ -1013,78 +1026,73 @@ __global__ void __launch_bounds__(128) k_combine_tokens(const TokensLaunch p)
         else
             hi = mid;
     }
-    int start = 0, len = 0;
-    if (lo < p.B)
-        seq_range(p, lo, start, len);
+    bool real = false;
+    if (lo < p.B && row < rows) {
+        const int start = p.cu[lo], end = p.cu[lo + 1];
+        real = start >= 0 && start <= tok && end <= p.L;   // as the attention took it
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (tok < start || tok >= start + len)
-        return;
-    // every warp reads all references and sums (two per lane)
-    const float2 *ml = p.part_ml + row * p.splits;
-    const float2 none = make_float2(-INFINITY, 0.f);
-    const float2 x0 = lane < p.splits ? ml[lane] : none;
-    const float2 x1 = lane + 32 < p.splits ? ml[lane + 32] : none;
-    float ms = fmaxf(x0.x, x1.x);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, off));
-    // weight of each split; 0 where a range held no key of the row (its part is not read)
-    const float w0 = x0.y == 0.f ? 0.f : ex2(x0.x - ms);
-    const float w1 = x1.y == 0.f ? 0.f : ex2(x1.x - ms);
-    float l = w0 * x0.y + w1 * x1.y;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        l += __shfl_xor_sync(0xffffffffu, l, off);
-    float acc[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        acc[v] = 0.f;
-    for (int s0 = warp; s0 < p.splits; s0 += U * WARPS) {
-        float x[U][V], w[U];
+    const long step = (long)p.Hkv * rows;   // entries of a split
+    const float2 *ml = p.part_ml + split0 * step + (long)blockIdx.y * rows + row;
+    const float4 *part = reinterpret_cast<const float4 *>(p.part_o) + split0 * step * (D / 4) +
+                         ((long)blockIdx.y * (D / 4) + c4) * rows + row;
+    float m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float w, float lw, const float4 &x) {
+        l = fmaf(w, lw, l);
+        acc.x = fmaf(w, x.x, acc.x);
+        acc.y = fmaf(w, x.y, acc.y);
+        acc.z = fmaf(w, x.z, acc.z);
+        acc.w = fmaf(w, x.w, acc.w);
+    };
+#pragma unroll 1
+    for (int s0 = split0; s0 < p.splits; s0 += U * WARPS) {
+        float2 y[U];
+        float4 x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int s = s0 + u * WARPS;
-            w[u] = __shfl_sync(0xffffffffu, s & 32 ? w1 : w0, s & 31);
-            const bool read = s < p.splits && w[u] != 0.f;
-            const float *src = p.part_o + (row * p.splits + s) * D + V * lane;
-#pragma unroll
-            for (int v = 0; v < V; v += 2) {
-                const float2 y = read ? *reinterpret_cast<const float2 *>(src + v)
-                                      : make_float2(0.f, 0.f);
-                x[u][v] = y.x;
-                x[u][v + 1] = y.y;
-            }
+            const bool in = s0 + u * WARPS < p.splits && real;
+            y[u] = in ? *ml : make_float2(-INFINITY, 0.f);
+            x[u] = in ? *part : make_float4(0.f, 0.f, 0.f, 0.f);
+            ml += WARPS * step;
+            part += WARPS * step * (D / 4);
         }
+        float top = m;
 #pragma unroll
         for (int u = 0; u < U; ++u)
+            top = fmaxf(top, y[u].x);
+        // a range without a key of the row has the reference -inf, the sum 0 and zeros
+        const float ref = top == -INFINITY ? 0.f : top, f = ex2(m - ref);
+        m = top;
+        l *= f;
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                acc[v] = s0 + u * WARPS < p.splits ? fmaf(w[u], x[u][v], acc[v]) : acc[v];
+        for (int u = 0; u < U; ++u)
+            add(ex2(y[u].x - ref), y[u].y, x[u]);
     }
     if (WARPS > 1) {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            s_acc[warp][V * lane + v] = acc[v];
+        s_ml[warp][lane] = make_float2(m, l);
+        s_acc[warp][lane] = acc;
         __syncthreads();
         if (warp > 0)
             return;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            acc[v] = 0.f;
+        for (int i = 1; i < WARPS; ++i)
+            m = fmaxf(m, s_ml[i][lane].x);
+        l = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-            for (int i = 0; i < WARPS; ++i)
-                acc[v] += s_acc[i][V * lane + v];
-        }
+        for (int i = 0; i < WARPS; ++i)
+            add(ex2(s_ml[i][lane].x - ref), s_ml[i][lane].y, s_acc[i][lane]);
     }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    uint16_t *o = p.o + head * p.os[1] + (long)tok * p.os[2] + V * lane;
-    if constexpr (V == 4)
-        *reinterpret_cast<uint2 *>(o) = make_uint2(pack_half2(acc[0] * inv, acc[1] * inv),
-                                                   pack_half2(acc[2] * inv, acc[3] * inv));
-    else
-        *reinterpret_cast<uint32_t *>(o) = pack_half2(acc[0] * inv, acc[1] * inv);
-    if (p.lse && lane == 0)
-        p.lse[head * p.ls[1] + tok] = l > 0.f ? (ms + __log2f(l)) * LN2 : l == 0.f ? -INFINITY : l;
+    if (!real)
+        return;
+    const float inv = l != 0.f ? rcp(l) : 0.f;
+    *reinterpret_cast<uint2 *>(p.o + head * p.os[1] + (long)tok * p.os[2] + 4 * c4) =
+        make_uint2(pack_half2(acc.x * inv, acc.y * inv), pack_half2(acc.z * inv, acc.w * inv));
+    if (p.lse && c4 == 0)
+        p.lse[head * p.ls[1] + tok] = l > 0.f ? (m + __log2f(l)) * LN2 : l == 0.f ? -INFINITY : l;
 }
 
 template <int D, int TILES> cudaError_t attend_tokens_impl(TokensLaunch p, cudaStream_t s)
@@ -1129,12 +1137,12 @@ template <int D, int TILES> cudaError_t attend_tokens_impl(TokensLaunch p, cudaS
     e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1)
         return e;
-    const long rows = (long)p.L * p.Hq;
-    // a CTA per row where rows are few and parts many (1024 rows of 16 parts, the whole call:
-    // 18.1 us against 19.8 with a warp per row; 8192 rows of 8 parts: 38 against 31)
-    const bool many = p.splits > 16 || (p.splits > 4 && rows <= 4096);
+    // The warps share the splits of a row where there are few rows: 40 rows of 8 heads and 38
+    // splits, the whole call, 32.4 us against 36.2 with a warp for all of them; 512 rows and 8
+    // splits 29.7 against 25.2.
+    const bool many = p.splits > 4 && (long)p.L * p.Hq * D < 16L * 128 * sm_count();
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(many ? rows : (rows + 3) / 4));
+    cfg.gridDim = dim3((unsigned)(((long)p.L * g + 7) / 8), p.Hkv, many ? D / 16 : D / 64);
     cfg.blockDim = dim3(128);
     cfg.stream = s;
     cudaLaunchAttribute at{};
@@ -1142,18 +1150,21 @@ template <int D, int TILES> cudaError_t attend_tokens_impl(TokensLaunch p, cudaS
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return many ? cudaLaunchKernelEx(&cfg, k_combine_tokens<D, 4>, p)
-                : cudaLaunchKernelEx(&cfg, k_combine_tokens<D, 1>, p);
+    if (many)   // U by the splits of a warp
+        return p.splits > 16 ? cudaLaunchKernelEx(&cfg, k_combine_tokens<D, 4, 8>, p, g)
+                             : cudaLaunchKernelEx(&cfg, k_combine_tokens<D, 4, 4>, p, g);
+    return p.splits > 2 ? cudaLaunchKernelEx(&cfg, k_combine_tokens<D, 1, 4>, p, g)
+                        : cudaLaunchKernelEx(&cfg, k_combine_tokens<D, 1, 2>, p, g);
 }
 
 } // namespace
 
 // Form and splits of a chunk, by what a call takes in microseconds: a start, then each
 // round of CTAs its key blocks and an item's start and end, then the merge.  The numbers
-// are fitted to a sweep of forms and splits over 16 shapes (1 to 32 sequences, 1 to 300
-// tokens each, 512 to 32768 slots); the choice was within 10% of the best one of the
-// sweep on all but three of them (20% there, under 4 us).  The slots that a unit holds are
-// known on the GPU alone: the capacity stands for them.
+// are fitted to a sweep of forms and splits over 24 shapes (1 to 32 sequences, 1 to 600
+// tokens each, 512 to 32768 slots); the choice was within 4% of the best one of the sweep
+// on all of them but one (3 x 40 tokens over 3008 slots: 7%).  The slots that a unit holds
+// are known on the GPU alone: the capacity stands for them.
 TokensPlan plan_tokens(int T, int B, int Hq, int Hkv, int D, int C, int requested)
 {
     const int tpt = TM / (Hq / Hkv), sms = sm_count();
@@ -1170,10 +1181,10 @@ TokensPlan plan_tokens(int T, int B, int Hq, int Hkv, int D, int C, int requeste
             const long ctas = items * splits;
             const long rounds = (ctas + slots - 1) / slots;
             const int per = (blocks + splits - 1) / splits;
-            float us = tiles == 2 ? rounds * (1.31f * per + 4.6f)
-                                  : rounds * (0.7f * per + 3.5f) * (ctas > sms ? 1.25f : 1.f);
+            float us = tiles == 2 ? rounds * (1.19f * per + 3.9f)
+                                  : rounds * (0.83f * per + 1.5f) * (ctas > sms ? 1.3f : 1.f);
             if (splits > 1)
-                us += 2.8f + 0.18f * splits + (float)rows * splits * D * (8.f / 3e6f);
+                us += 3.1f + 0.08f * splits + (float)rows * splits * D * 1.35e-6f;
             if (us < least) {
                 least = us;
                 best = TokensPlan{tiles, splits};
