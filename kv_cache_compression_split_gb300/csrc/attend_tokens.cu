@@ -34,6 +34,11 @@
 // small area of shared memory per warp, so that a warp stores whole rows: a thread that
 // stores its own row touches 32 lines per instruction, which took 7000 clocks a tile.
 //
+// Code size.  The warps' roles run side by side, and what runs once per item comes from the
+// instruction cache's far levels.  So prompts and chunks are kernels of their own, and loops
+// that run a few times per item stay rolled: 74 KB instead of 105 took 187 us instead of 200
+// for eight prompts of 152 to 2047 tokens, 29.6 instead of 31.9 for a batch of drafts.
+//
 // What bounds it.  Per 128 x 128 block of D = 128 the two products take 1070 clocks of the
 // tensor pipe (a 128 x 128 x 16 product was measured at 64.5 to 67 clocks), the
 // exponentials 520 of the SFU.  The two-tile form spends 1245 clocks a block once it runs:
@@ -129,47 +134,54 @@ __device__ __forceinline__ void seq_range(const TokensLaunch &p, int b, int &sta
 // sequences of the last call, since the work is handed out in order.
 struct ItemWalk {
     int b0 = 0;
-    long base = 0;
+    unsigned base = 0;   // items before it
     // tiles: per item; keys: per block
-    __device__ bool find(const TokensLaunch &p, int tpt, int tiles, int keys, long idx, TokItem &it)
+    template <bool CHUNK>
+    __device__ bool find(const TokensLaunch &p, int tpt, int tiles, int keys, unsigned idx,
+                         TokItem &it)
     {
         const int lane = threadIdx.x & 31;
+        const unsigned splits = CHUNK ? p.splits : 1, Hkv = p.Hkv;
         if (idx < base) {
             b0 = 0;
             base = 0;
         }
+#pragma unroll 1
         for (; b0 < p.B; b0 += 32) {
             int s = 0, n = 0;
             if (b0 + lane < p.B)
                 seq_range(p, b0 + lane, s, n);
-            const int ranges = (n + tiles * tpt - 1) / (tiles * tpt);
-            const long mine = (long)ranges * p.Hkv * p.splits;
-            long sum = mine;
+            const unsigned ranges = (unsigned)(n + tiles * tpt - 1) / (unsigned)(tiles * tpt);
+            unsigned sum = ranges * Hkv * splits;
+            // ranges that overlap may add up to more than the grid: sums stop at the largest
+            // number
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                const long y = __shfl_up_sync(0xffffffffu, sum, off);
+                const unsigned y = __shfl_up_sync(0xffffffffu, sum, off);
                 if (lane >= off)
-                    sum += y;
+                    sum = sum + y < y ? 0xffffffffu : sum + y;
             }
-            const unsigned here = __ballot_sync(0xffffffffu, base + sum > idx);
+            sum = sum + base < base ? 0xffffffffu : sum + base;
+            const unsigned here = __ballot_sync(0xffffffffu, sum > idx);
             if (!here) {
-                base += __shfl_sync(0xffffffffu, sum, 31);
+                base = __shfl_sync(0xffffffffu, sum, 31);
                 continue;
             }
             const int src = __ffs(here) - 1;
-            const int r = (int)(idx - base - __shfl_sync(0xffffffffu, sum - mine, src));
+            const unsigned before = __shfl_sync(0xffffffffu, sum, max(src - 1, 0));
+            const unsigned r = idx - (src ? before : base);
             const int per = __shfl_sync(0xffffffffu, ranges, src);
             const int len = __shfl_sync(0xffffffffu, n, src);
             it.start = __shfl_sync(0xffffffffu, s, src);
             it.b = b0 + src;
-            it.split = r % p.splits;
-            const int q = r / p.splits;
-            it.hk = q % p.Hkv;
-            it.tok0 = (per - 1 - q / p.Hkv) * tiles * tpt;
+            const unsigned q = r / splits, range = q / Hkv;
+            it.split = r - q * splits;
+            it.hk = q - range * Hkv;
+            it.tok0 = (per - 1 - (int)range) * tiles * tpt;
             it.ntok = min(tiles * tpt, len - it.tok0);
             it.two = tiles == 2 && it.ntok <= tpt;
             int n_keys = len;
-            if (p.n) {
+            if (CHUNK) {
                 n_keys = p.n[it.b * p.Hkv + it.hk];
                 if (n_keys < 0 || n_keys > p.C) {
                     flag_error(p.status, DEV_CAPACITY);
@@ -179,7 +191,7 @@ struct ItemWalk {
             it.shift = n_keys - len;
             const int end = max(0, it.shift + it.tok0 + it.ntok);
             const int blocks = (end + keys - 1) / keys;
-            const int chunk = (blocks + p.splits - 1) / p.splits;
+            const int chunk = (blocks + splits - 1) / splits;
             it.j0 = min(blocks, it.split * chunk);
             it.j1 = min(blocks, it.j0 + chunk);
             return true;
@@ -205,10 +217,11 @@ template <int TK> struct TileRange {
     }
 };
 
+template <bool CHUNK>
 __device__ __forceinline__ const uint16_t *key_row(const TokensLaunch &p, const uint16_t *base,
                                                    const long *st, const TokItem &it, int j)
 {
-    if (!p.n)
+    if (!CHUNK)
         return base + (p.cu ? 0 : it.b) * st[0] + it.hk * st[1] + (long)(it.start + j) * st[2];
     const long row = SlotRows{p.block_table, p.C, p.num_pages}.row(it.b * p.Hkv + it.hk, j);
     return row < 0 ? nullptr : base + row * p.D;
@@ -264,6 +277,7 @@ __device__ __forceinline__ float prob64(uint32_t taddr, const float (&x)[64], fl
 
 // The 32 channels from c0 of one row, from memory, over the keys [first, last]: for a
 // row whose tensor-core result is not finite although its sum l is.
+template <bool CHUNK>
 __device__ __noinline__ void row_again(const TokensLaunch &p, const TokItem &it, const uint16_t *q,
                                        int first, int last, float ref, int c0, float scale,
                                        uint16_t *o, float4 *part, long stride)
@@ -272,11 +286,14 @@ __device__ __noinline__ void row_again(const TokensLaunch &p, const TokItem &it,
 #pragma unroll
     for (int c = 0; c < 32; ++c)
         acc[c] = 0.f;
+#pragma unroll 1
     for (int j = first; j <= last; ++j) {
-        const uint16_t *k = key_row(p, p.k, p.ks, it, j), *v = key_row(p, p.v, p.vs, it, j);
+        const uint16_t *k = key_row<CHUNK>(p, p.k, p.ks, it, j);
+        const uint16_t *v = key_row<CHUNK>(p, p.v, p.vs, it, j);
         if (!k)
             continue;
         float s = 0.f;
+#pragma unroll 1
         for (int d = 0; d < p.D; ++d)
             s = fmaf(__half2float(__ushort_as_half(q[d])), __half2float(__ushort_as_half(k[d])), s);
         const float w = ex2(s * p.scale_log2 - ref);
@@ -295,7 +312,7 @@ __device__ __noinline__ void row_again(const TokensLaunch &p, const TokItem &it,
     }
 }
 
-template <int D, int TILES>
+template <int D, int TILES, bool CHUNK>
 __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS)
     k_attend_tokens(const __grid_constant__ TokMaps maps, const __grid_constant__ TokensLaunch p)
 {
@@ -322,6 +339,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int g = p.Hq / p.Hkv, tpt = TM / g;
+    const bool packed = CHUNK || p.cu;
 
     asm volatile("griddepcontrol.launch_dependents;");
     if (threadIdx.x == 0) {
@@ -381,7 +399,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
             prefetch_tmap(&maps.o);
         }
         ItemWalk walk;
-        long idx = blockIdx.x;
+        int idx = blockIdx.x;
         int n_it = 0, n_q = 0;   // ring slots and query loads
         bool ok = true;
         int n_clc = 0;
@@ -392,7 +410,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 // the next item while this one runs: take over a CTA that has not started
                 if (lane == 0)
                     clc_request(clc, clc_full);
-                if (!walk.find(p, tpt, TILES, TK, idx, it))
+                if (!walk.find<CHUNK>(p, tpt, TILES, TK, idx, it))
                     it.j0 = it.j1 = it.two = 0;   // the grid is an upper bound
             }
             if (idx < 0 || it.b >= 0) {
@@ -412,12 +430,13 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
             const int n = it.j1 - it.j0;
             const int unit = it.b * p.Hkv + it.hk;
             const int per = p.C / PAGE_SLOTS;
-            if (p.block_table)   // the item's part of the page table into L1
+            if (CHUNK && p.block_table)   // the item's part of the page table into L1
+#pragma unroll 1
                 for (int i = TK / BOX * it.j0 + 32 * lane; i < min(per, TK / BOX * it.j1); i += 1024)
                     asm volatile("prefetch.global.L1 [%0];" ::"l"(p.block_table +
                                                                   (size_t)unit * per + i));
             if (lane == 0 && n > 0) {
-                const int n_keys = p.n ? it.shift + (p.cu ? p.cu[it.b + 1] - p.cu[it.b] : 0) : 0;
+                const int n_keys = CHUNK ? it.shift + p.cu[it.b + 1] - p.cu[it.b] : 0;
                 auto load = [&](const CUtensorMap *map, int j) {
                     const int st = n_it % NS;
                     if (n_it >= NS)
@@ -428,7 +447,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                     uint8_t *dst = ring + st * Cfg::TILE_BYTES;
                     for (int h = 0; h < TK / BOX; ++h) {
                         const int j_key = j * TK + h * BOX;
-                        if (p.n) {
+                        if (CHUNK) {
                             // a box without a key, or without a page, reads as zeros: its
                             // row lies behind the last one
                             int row = p.kv_rows;
@@ -451,7 +470,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                             for (int c = 0; c < Cfg::NBOX; ++c)
                                 tma_load_4d(dst + c * Cfg::BOX_BYTES + h * (BOX * 128), map,
                                             &kv_full[st], 64 * c, it.hk, it.start + j_key,
-                                            p.cu ? 0 : it.b);
+                                            packed ? 0 : it.b);
                         }
                     }
                     ++n_it;
@@ -460,6 +479,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 // tile (its place is free when the last item's scores are done), then values,
                 // which wait for a place in the ring behind the last item's.
                 const int ahead = TILES == 1 || it.two ? 2 : 1;
+#pragma unroll 1
                 for (int i = 0; ok && i < ahead && i < n; ++i)
                     load(&maps.k, it.j0 + i);
                 if (ok && n_q > 0)
@@ -467,11 +487,12 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 if (ok) {
                     const int tiles = it.ntok > tpt ? 2 : 1;
                     mbar_arrive_expect_tx(q_full, tiles * Cfg::NBOX * tpt * g * 128);
+#pragma unroll 1
                     for (int t = 0; t < tiles; ++t)
                         for (int c = 0; c < Cfg::NBOX; ++c)
                             tma_load_4d(sq + t * Cfg::QTILE_BYTES + c * Cfg::QBOX_BYTES, &maps.q,
                                         q_full, 64 * c, it.hk * g, it.start + it.tok0 + t * tpt,
-                                        p.cu ? 0 : it.b);
+                                        packed ? 0 : it.b);
                     ++n_q;
                 }
                 for (int i = 0; ok && i < n; ++i) {
@@ -493,6 +514,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
         if (lane == 0) {
             if (!ok && idx >= 0)
                 mbar_wait(clc_full, n_clc & 1);
+#pragma unroll 1
             for (int i = n_it > NS ? n_it - NS : 0; i < n_it; ++i)
                 mbar_wait(&kv_full[i % NS], (i / NS) & 1);
             if (n_q > 0)
@@ -543,6 +565,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                         umma_f16_ts(od, pd + 8 * kk, vd + kk * (2048 >> 4), Cfg::IDESC_PV,
                                     kk > 0 ? 1u : acc);
                 } else {
+#pragma unroll 1
                     for (int kk = 0; kk < steps; ++kk)
                         umma_f16_ts(od, pd + 8 * kk, vd + kk * (2048 >> 4), Cfg::IDESC_PV,
                                     kk > 0 ? 1u : acc);
@@ -571,6 +594,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
             wait(q_full, n_q & 1);
             ++n_q;
             // first scores of both tiles
+#pragma unroll 1
             for (int i = 0; ok && i < ahead && i < n; ++i, ++n_it) {
                 wait(&kv_full[n_it % NS], (n_it / NS) & 1);
                 if (!ok)
@@ -602,6 +626,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 const int keys = min(TK, r1.end - j * TK);
                 if (keys & 15) {   // rows behind the last key of the item: cleared
                     const int rows = 16 - (keys & 15);
+#pragma unroll 1
                     for (int x = lane; x < rows * Cfg::NBOX * 8; x += 32) {
                         const int c = x / (rows * 8), y = x % (rows * 8);
                         *reinterpret_cast<uint4 *>(ring + (vs % NS) * Cfg::TILE_BYTES +
@@ -755,7 +780,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                         tc_fence_after();
                     }
                     if (i > 0) {
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
                             float v[32];
                             tmem_ld32(o_col + c, v);
@@ -807,9 +832,9 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
             };
             auto part_o = [&] { return reinterpret_cast<float4 *>(p.part_o) + part_at(D / 4); };
             auto o_row = [&] {
-                return p.o + (p.cu ? 0 : it.b) * p.os[0] + head * p.os[1] + tok * p.os[2];
+                return p.o + (packed ? 0 : it.b) * p.os[0] + head * p.os[1] + tok * p.os[2];
             };
-            const bool part = p.splits > 1;
+            const bool part = CHUNK && p.splits > 1;
             if (elect_one())
                 bulk_wait_read<0>();   // the last item's stores have read the area
             __syncwarp();
@@ -817,6 +842,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
             if (TILES == 2 && it.two && t == 1) {
                 // second part of the blocks: handed over 32 channels at a time, once the
                 // first part's warp has read what was there
+#pragma unroll 1
                 for (int c = 0; c < D; c += 32, ++n_m) {
                     const bool got =
                         n_m == 0 || mbar_wait_or_abort(&mrg_empty[quarter], (n_m - 1) & 1, abort);
@@ -855,7 +881,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 inv = l > 0.f ? rcp(l) : 0.f;
                 const int o_y = __shfl_sync(0xffffffffu, it.hk * g, 0);
                 const int o_z = __shfl_sync(0xffffffffu, it.start + rg.tok + w_tok, 0);
-                const int o_w = __shfl_sync(0xffffffffu, p.cu ? 0 : it.b, 0);
+                const int o_w = __shfl_sync(0xffffffffu, packed ? 0 : it.b, 0);
                 const float2 inv2 = make_float2(inv, inv), zero2 = make_float2(0.f, 0.f);
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
@@ -968,11 +994,12 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 if (elect_one())
                     bulk_wait_all();   // what is stored again comes after what was stored
                 __syncwarp();
-                const uint16_t *q = p.q + (p.cu ? 0 : it.b) * p.qs[0] + head * p.qs[1] +
+                const uint16_t *q = p.q + (packed ? 0 : it.b) * p.qs[0] + head * p.qs[1] +
                                     tok * p.qs[2];
+#pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32)
                     if (again && bad >> (c0 / 32) & 1)
-                        row_again(p, it, q, it.j0 * TK, min(last, it.j1 * TK - 1),
+                        row_again<CHUNK>(p, it, q, it.j0 * TK, min(last, it.j1 * TK - 1),
                                   m == -INFINITY ? 0.f : m, c0, inv, o_row(),
                                   part ? part_o() : nullptr, rows);
             }
@@ -980,7 +1007,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 if (part)
                     p.part_ml[part_at(1)] = make_float2(m, lsum);
                 else if (p.lse)
-                    p.lse[(p.cu ? 0 : it.b) * p.ls[0] + head * p.ls[1] + tok] =
+                    p.lse[(packed ? 0 : it.b) * p.ls[0] + head * p.ls[1] + tok] =
                         lsum > 0.f ? (m + __log2f(lsum)) * LN2 : lsum == 0.f ? -INFINITY : lsum;
             }
             tc_fence_before();
@@ -1095,7 +1122,8 @@ __global__ void __launch_bounds__(128) k_combine_tokens(const TokensLaunch p, co
         p.lse[head * p.ls[1] + tok] = l > 0.f ? (m + __log2f(l)) * LN2 : l == 0.f ? -INFINITY : l;
 }
 
-template <int D, int TILES> cudaError_t attend_tokens_impl(TokensLaunch p, cudaStream_t s)
+template <int D, int TILES, bool CHUNK>
+cudaError_t attend_tokens_impl(TokensLaunch p, cudaStream_t s)
 {
     using Cfg = TokCfg<D, TILES>;
     const int g = p.Hq / p.Hkv, tpt = TM / g;
@@ -1112,7 +1140,7 @@ template <int D, int TILES> cudaError_t attend_tokens_impl(TokensLaunch p, cudaS
     };
     bool ok = map4(&maps.q, p.q, p.qs, p.Hq, g, tpt) &&
               map4(&maps.o, p.o, p.os, p.Hq, g, 32 / g, 32);
-    if (p.n) {
+    if (CHUNK) {
         p.kv_rows = p.block_table ? p.num_pages * PAGE_SLOTS : p.B * p.Hkv * p.C;
         ok = ok && encode_tmap_2d_f16(&maps.k, p.k, D, p.kv_rows, 64, BOX) &&
              encode_tmap_2d_f16(&maps.v, p.v, D, p.kv_rows, 64, BOX);
@@ -1123,7 +1151,7 @@ template <int D, int TILES> cudaError_t attend_tokens_impl(TokensLaunch p, cudaS
     if (!ok)
         return cudaErrorInvalidValue;
     cudaError_t e =
-        set_smem_once(reinterpret_cast<const void *>(k_attend_tokens<D, TILES>), Cfg::SMEM);
+        set_smem_once(reinterpret_cast<const void *>(k_attend_tokens<D, TILES, CHUNK>), Cfg::SMEM);
     if (e != cudaSuccess)
         return e;
     // packed: every sequence ends in at most one partial range
@@ -1133,9 +1161,9 @@ template <int D, int TILES> cudaError_t attend_tokens_impl(TokensLaunch p, cudaS
     const long items = ranges * p.Hkv * p.splits;
     if (items > 0x7fffffffL)
         return cudaErrorInvalidValue;
-    k_attend_tokens<D, TILES><<<(unsigned)items, Cfg::NTHR, Cfg::SMEM, s>>>(maps, p);
+    k_attend_tokens<D, TILES, CHUNK><<<(unsigned)items, Cfg::NTHR, Cfg::SMEM, s>>>(maps, p);
     e = cudaGetLastError();
-    if (e != cudaSuccess || p.splits == 1)
+    if (!CHUNK || e != cudaSuccess || p.splits == 1)
         return e;
     // The warps share the splits of a row where there are few rows: 40 rows of 8 heads and 38
     // splits, the whole call, 32.4 us against 36.2 with a warp for all of them; 512 rows and 8
@@ -1206,10 +1234,14 @@ cudaError_t launch_attend_tokens(const TokensLaunch &p, cudaStream_t s)
     // heads: 39 / 45, 51 / 52, 123 / 124, 217 / 199, 397 / 367.  Heads of 64 channels, whose
     // time goes to the exponentials, are faster with one tile throughout (2 x 8192: 276 / 298).
     // A chunk's form comes with its plan.
-    const bool one = p.D == 64 || (p.n ? p.tiles == 1 : p.L <= 1024L * (p.cu ? p.B : 1));
-    if (one)
-        return p.D == 128 ? attend_tokens_impl<128, 1>(p, s) : attend_tokens_impl<64, 1>(p, s);
-    return attend_tokens_impl<128, 2>(p, s);
+    const bool one = p.n ? p.tiles == 1 : p.L <= 1024L * (p.cu ? p.B : 1);
+    if (p.n)
+        return p.D == 64 ? attend_tokens_impl<64, 1, true>(p, s)
+               : one     ? attend_tokens_impl<128, 1, true>(p, s)
+                         : attend_tokens_impl<128, 2, true>(p, s);
+    return p.D == 64 ? attend_tokens_impl<64, 1, false>(p, s)
+           : one     ? attend_tokens_impl<128, 1, false>(p, s)
+                     : attend_tokens_impl<128, 2, false>(p, s);
 }
 
 } // namespace kvc
