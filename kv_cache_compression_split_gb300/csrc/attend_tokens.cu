@@ -1228,13 +1228,16 @@ TokensPlan plan_tokens(int T, int B, int Hq, int Hkv, int D, int C, int requeste
 cudaError_t launch_attend_tokens(const TokensLaunch &p, cudaStream_t s)
 {
     // Which form: two tiles share the K and V blocks and win once an item is long; the one-tile
-    // form's second CTA per SM works through the start and the end of the first one's items.
-    // Uniform prompts of 16 / 2 heads of 128, one against two tiles, us: 16 x 512 tokens 31 / 35,
-    // 8 x 1024 42 / 46, 8 x 2048 118 / 119, 4 x 4096 205 / 193, 2 x 8192 374 / 341; 16 / 16
-    // heads: 39 / 45, 51 / 52, 123 / 124, 217 / 199, 397 / 367.  Heads of 64 channels, whose
-    // time goes to the exponentials, are faster with one tile throughout (2 x 8192: 276 / 298).
-    // A chunk's form comes with its plan.
-    const bool one = p.n ? p.tiles == 1 : p.L <= 1024L * (p.cu ? p.B : 1);
+    // form's second CTA per SM works through the start and the end of the first one's items,
+    // and its smaller items fill the card when there are few.  Uniform prompts of 16 / 2 heads
+    // of 128, one against two tiles, us: 16 x 512 tokens 27.4 / 29.2, 8 x 1024 40.1 / 41.6,
+    // 8 x 2048 113 / 110, 4 x 4096 200 / 185, 2 x 8192 379 / 349, but 1 x 2048 29.7 / 32.9;
+    // 16 / 16 heads: 35.9 / 37.9, 44.1 / 45.6, 118 / 114, 214 / 193, 404 / 364, but 1 x 2048
+    // 25.8 / 29.8.  Heads of 64 channels, whose time goes to the exponentials, were faster with
+    // one tile throughout (2 x 8192: 276 / 298).  A chunk's form comes with its plan.
+    const long seqs = p.cu ? p.B : 1, pair = 2 * (TM / (p.Hq / p.Hkv));
+    const bool few = (p.L / pair + seqs) * p.Hkv * (p.cu ? 1 : p.B) <= sm_count();
+    const bool one = p.n ? p.tiles == 1 : p.L <= 1024 * seqs || few;
     if (p.n)
         return p.D == 64 ? attend_tokens_impl<64, 1, true>(p, s)
                : one     ? attend_tokens_impl<128, 1, true>(p, s)
