@@ -840,16 +840,10 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
             __syncwarp();
             float *hand = reinterpret_cast<float *>(s_out + (4 + quarter) * Cfg::OUT_BYTES) + lane;
             if (TILES == 2 && it.two && t == 1) {
-                // second part of the blocks: handed over 32 channels at a time, once the
-                // first part's warp has read what was there
+                // second part of the blocks: handed over 32 channels at a time.  Each is read
+                // before the warp goes on: its area takes the next item's results.
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32, ++n_m) {
-                    const bool got =
-                        n_m == 0 || mbar_wait_or_abort(&mrg_empty[quarter], (n_m - 1) & 1, abort);
-                    if (!__all_sync(0xffffffffu, got)) {
-                        ok = false;
-                        break;
-                    }
                     if (c == 0)
                         s_ml[r] = make_float2(m, l);
                     if (rg.count > 0 && !idle) {
@@ -861,6 +855,11 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                     }
                     __syncwarp();
                     mbar_arrive_warp(&mrg_full[quarter]);
+                    const bool got = mbar_wait_or_abort(&mrg_empty[quarter], n_m & 1, abort);
+                    if (!__all_sync(0xffffffffu, got)) {
+                        ok = false;
+                        break;
+                    }
                 }
                 tc_fence_before();
                 continue;
