@@ -135,6 +135,24 @@ def test_prompt_range_outside_the_batch_is_an_empty_sequence(kvc):
     assert device_status_clean(kvc)
 
 
+def test_prompt_ranges_that_run_backwards(kvc):
+    """A range of negative length is an empty sequence; rows that one other range alone holds
+    are right."""
+    gen = _gen(31)
+    q, k, v = _randn(gen, 50, 4, 64), _randn(gen, 50, 2, 64), _randn(gen, 50, 2, 64)
+    o = torch.full_like(q, 7.0)
+    cu = torch.tensor([0, 40, 10, 50], dtype=torch.int32, device="cuda")
+    kvc.kvc_prompt_attend(q, k, v, o, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    assert kvc.kvc_read_device_status() == kvc.KVC_DEV_CAPACITY
+    for h in range(4):
+        check_rows(o[:10, h], None, attend_rows(q[:10, h], k[:10, h // 2], v[:10, h // 2],
+                                                torch.arange(10)))
+        check_rows(o[40:, h], None, attend_rows(q[40:, h], k[10:, h // 2], v[10:, h // 2],
+                                                torch.arange(30, 40)))
+    assert device_status_clean(kvc)
+
+
 # ---------------------------------------------------------------- chunks
 
 def _cache(kvc, gen, n, C, D, paged, spare=3):
@@ -220,6 +238,40 @@ def test_chunk(kvc, Hq, Hkv, D, C, paged, n, m, splits):
     assert device_status_clean(kvc)
     check_chunk(q, K, V, n, m, o, lse, Hq)
     assert (o[T:] == 7.0).all() and (lse[:, T:] == 7.0).all()
+
+
+@pytest.mark.parametrize("splits", [2, 4, 5, 16, 17, 33, 64])
+def test_chunk_merge_of_few_rows(kvc, splits):
+    """Every number of parts per warp of the merge, its rows ending inside a group of eight;
+    parts without a key of some row, and tokens of no sequence before and between."""
+    gen = _gen(40 + splits)
+    n, m = [[2500, 1700], [64, 4096]], [3, 2]
+    cache, K, V = _cache(kvc, gen, n, 4096, 128, True)
+    q = _randn(gen, 9, 10, 128)
+    o, lse = torch.full_like(q, 7.0), torch.full((10, 9), 7.0, device="cuda")
+    cu = torch.tensor([2, 5, 7], dtype=torch.int32, device="cuda")
+    ws = torch.full((kvc.kvc_chunk_workspace_size(cache, q, splits) // 4,), float("nan"),
+                    device="cuda")
+    kvc.kvc_chunk_attend(cache, q, cu, o, lse=lse, workspace=ws, num_splits=splits)
+    assert device_status_clean(kvc)
+    check_chunk(q[2:7], K, V, n, m, o[2:7], lse[:, 2:7], 10)
+    for x in (o[:2], o[7:], lse[:, :2], lse[:, 7:]):
+        assert (x == 7.0).all()
+
+
+@pytest.mark.parametrize("D,splits", [(128, 2), (128, 5), (128, 9), (64, 6)])
+def test_chunk_merge_of_many_rows(kvc, D, splits):
+    """More rows than the merge shares out among a block's warps."""
+    gen = _gen(50 + splits)
+    n, m = [[900, 640], [1000, 333]], [400 if D == 128 else 700, 33]
+    cache, K, V = _cache(kvc, gen, n, 1024, D, False)
+    q = _randn(gen, sum(m), 14, D)
+    o, lse = torch.full_like(q, 7.0), torch.full((14, sum(m)), 7.0, device="cuda")
+    ws = torch.full((kvc.kvc_chunk_workspace_size(cache, q, splits) // 4,), float("nan"),
+                    device="cuda")
+    kvc.kvc_chunk_attend(cache, q, _cu(m), o, lse=lse, workspace=ws, num_splits=splits)
+    assert device_status_clean(kvc)
+    check_chunk(q, K, V, n, m, o, lse, 14)
 
 
 def test_chunk_of_more_tokens_than_slots_has_empty_rows(kvc):
