@@ -43,12 +43,12 @@
 // tensor pipe (a 128 x 128 x 16 product was measured at 64.5 to 67 clocks), the
 // exponentials 520 of the SFU.  The two-tile form spends 1245 clocks a block once it runs:
 // a row's thread needs 1300 for its block (reading 30, maximum 300, exponentials and
-// packing 830, storing 35) while the tensor cores do the other tile's.  8192 tokens of
-// 64 / 8 heads: 690 us, 1590 TFLOP/s, under the power cap (about 1.5 GHz): 0.85 of the
-// measured burst rate, 0.94 of the sustained one.  Shorter prompts pay about 4000 clocks
-// per item between its last product and the next one's.  A batch of few tokens over
-// long caches is HBM bound in the middle (64 KB per SM in 2700 clocks) and spends the
-// rest on the start, the last round and the merge: 131 MB in 35 us.
+// packing 800, storing 35) while the tensor cores do the other tile's.  8192 tokens of
+// 64 / 8 heads: 650 to 690 us, 1600 to 1690 TFLOP/s, under the power cap (about 1.5 GHz):
+// 0.85 to 0.9 of the measured burst rate, 0.94 to 1.0 of the sustained one.  Shorter prompts
+// pay about 3000 clocks per item between its last product and the next one's.  A batch of few
+// tokens over long caches is HBM bound in the middle (64 KB per SM in 2700 clocks) and spends
+// the rest on the start, the last round and the merge: 131 MB in 30 us.
 //
 // Non-finite values.  A masked score is replaced, not added to, so keys behind a
 // row's range never matter.  A masked value row would enter as 0 * v: rows behind the
