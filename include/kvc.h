@@ -526,6 +526,7 @@ KVC_API kvc_status kvc_random_evict(const kvc_slot_cache *cache, int prompt_len,
  * output.  lse (optional) is fp32 with adjacent tokens: [B, Hq, L] padded,
  * [Hq, L] packed.  The padded lse is what kvc_h2o_accumulate(KVC_H2O_PREFILL) takes
  * as the rows' normalisers, so a prompt's heavy-hitter scores cost one more pass.
+ * o overlaps neither q, k nor v.
  * A non-finite key or value row affects the rows that attend it and no others.
  * A sequence whose range leaves [0, L] counts as empty and sets KVC_DEV_CAPACITY.
  * No workspace.  Source: "Rethinking KV Cache Compression" guide, §16 "Prefill、decode、TP 的
@@ -558,7 +559,8 @@ KVC_API kvc_status kvc_prompt_attend(const kvc_prompt_args *args, cudaStream_t s
  * is kvc_decode_attend; m_b = 0 leaves the sequence out.
  *   q, o     the T new tokens of all sequences, packed: sequence b's are
  *            [cu_new[b], cu_new[b+1]) (device int32 [B + 1]); strides in elements
- *            between heads and between tokens, positive multiples of 8
+ *            between heads and between tokens, positive multiples of 8; o overlaps
+ *            neither q nor the cache
  *   lse      optional [Hq, T] fp32
  *   workspace  kvc_chunk_workspace_size(args) bytes (16-byte aligned; may be NULL
  *            when that is 0); calls that may overlap on the GPU need one each
