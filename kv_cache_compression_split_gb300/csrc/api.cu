@@ -754,10 +754,10 @@ static TokensPlan chunk_plan(const kvc_chunk_args *a)
     return plan_tokens(a->T, c.B, a->Hq, c.Hkv, c.D, c.C, a->num_splits);
 }
 
-// Parts of every row: D values, the reference and the sum.
+// Parts of every row: D values, the reference and the sum; behind them a word.
 static size_t chunk_bytes(const kvc_chunk_args *a, int splits)
 {
-    return splits > 1 ? (size_t)a->T * a->Hq * splits * (a->cache->D + 2) * sizeof(float) : 0;
+    return splits > 1 ? (size_t)a->T * a->Hq * splits * (a->cache->D + 2) * sizeof(float) + 16 : 0;
 }
 
 size_t kvc_chunk_workspace_size(const kvc_chunk_args *a)
@@ -788,6 +788,7 @@ kvc_status kvc_chunk_attend(const kvc_chunk_args *a, cudaStream_t stream)
             return KVC_ERR_WORKSPACE;
         p.part_o = static_cast<float *>(a->workspace);
         p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)a->T * a->Hq * p.splits * c.D);
+        p.broken = reinterpret_cast<int *>(p.part_ml + (size_t)a->T * a->Hq * p.splits);
     }
     p.B = c.B;
     p.Hq = a->Hq;

@@ -501,6 +501,18 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                         load(&maps.k, it.j0 + i + ahead);
                 }
             }
+            if (CHUNK && idx == 0 && p.splits > 1) {
+                // once per call, for the merge: ranges out of order cannot be bisected
+                bool bad = false;
+#pragma unroll 1
+                for (int b = lane; b < p.B; b += 32) {
+                    const int c0 = p.cu[b], c1 = p.cu[b + 1];
+                    bad |= c0 < 0 || c1 < c0 || c1 > p.L;
+                }
+                bad = __any_sync(0xffffffffu, bad);
+                if (lane == 0)
+                    *p.broken = bad;
+            }
             int next = -1;
             if (lane == 0 && ok) {
                 ok = mbar_sleep_or_abort(clc_full, n_clc & 1, abort);
@@ -1058,6 +1070,12 @@ __global__ void __launch_bounds__(128) k_combine_tokens(const TokensLaunch p, co
         real = start >= 0 && start <= tok && end <= p.L;   // as the attention took it
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!real && row < rows && *p.broken)
+#pragma unroll 1
+        for (int b = 0; b < p.B && !real; ++b) {
+            const int start = p.cu[b], end = p.cu[b + 1];
+            real = start >= 0 && start <= tok && tok < end && end <= p.L;
+        }
     const long step = (long)p.Hkv * rows;   // entries of a split
     const float2 *ml = p.part_ml + split0 * step + (long)blockIdx.y * rows + row;
     const float4 *part = reinterpret_cast<const float4 *>(p.part_o) + split0 * step * (D / 4) +

@@ -129,8 +129,9 @@ struct TokensLaunch {
     int kv_rows;               // chunk: rows of the K / V arrays (set by the launcher)
     int tiles;                 // chunk: tiles per item
     int splits;                // key ranges per item, merged by a second launch when above 1
-    float *part_o;             // [L * Hq, splits, D]
-    float2 *part_ml;           // [L * Hq, splits]: reference and sum
+    float *part_o;             // [splits, Hkv, D / 4, L * g, 4]: sums of the values, fp32
+    float2 *part_ml;           // [splits, Hkv, L * g]: reference and sum
+    int *broken;               // whether some sequence's range is bad, for the merge
     float scale_log2;
     int *status;
 };

@@ -274,6 +274,26 @@ def test_chunk_merge_of_many_rows(kvc, D, splits):
     check_chunk(q, K, V, n, m, o, lse, 14)
 
 
+@pytest.mark.parametrize("splits", [1, 3, 20])
+def test_chunk_ranges_that_run_backwards(kvc, splits):
+    """A range of negative length is an empty sequence; the others', in any order, are right."""
+    gen = _gen(33)
+    n = [[150, 640], [700, 3], [64, 1500]]
+    cache, K, V = _cache(kvc, gen, n, 1536, 128, True)
+    q = _randn(gen, 30, 4, 128)
+    o, lse = torch.full_like(q, 7.0), torch.full((4, 30), 7.0, device="cuda")
+    cu = torch.tensor([20, 30, 0, 10], dtype=torch.int32, device="cuda")
+    ws = torch.full((max(kvc.kvc_chunk_workspace_size(cache, q, splits) // 4, 4),), float("nan"),
+                    device="cuda")
+    kvc.kvc_chunk_attend(cache, q, cu, o, lse=lse, workspace=ws, num_splits=splits)
+    torch.cuda.synchronize()
+    assert kvc.kvc_read_device_status() == kvc.KVC_DEV_CAPACITY
+    for b, w in ((0, slice(20, 30)), (2, slice(0, 10))):
+        check_chunk(q[w], K[b:b + 1], V[b:b + 1], n[b:b + 1], [10], o[w], lse[:, w], 4, f"{b}")
+    assert (o[10:20] == 7.0).all() and (lse[:, 10:20] == 7.0).all()
+    assert device_status_clean(kvc)
+
+
 def test_chunk_of_more_tokens_than_slots_has_empty_rows(kvc):
     """A unit that holds fewer slots than the chunk has tokens: the first rows see nothing."""
     gen = _gen(9)
