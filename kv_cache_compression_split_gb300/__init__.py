@@ -635,21 +635,31 @@ class SlotCache:
         return _state_without_desc(self)
 
     def desc(self) -> SlotCacheDesc:
-        # built once and kept while the fields' storage, shapes and strides stay the same (a
-        # field replaced or resized in place yields a new key, and the fields are checked again)
+        # built once and kept while the fields' storage and shapes stay the same and they are
+        # contiguous (a field replaced or resized in place is noticed, and the fields are
+        # checked again)
+        own = self.__dict__
         K, V, pos, n, sl, bt = self.K, self.V, self.pos, self.n, self.seqlen, self.block_table
-        key = (K.data_ptr(), K.shape, K.stride(), V.data_ptr(), V.shape, V.stride(),
-               pos.data_ptr(), pos.shape, pos.stride(), n.data_ptr(), n.shape, n.stride(),
-               sl.data_ptr(), sl.shape, sl.stride(),
-               None if bt is None else (bt.data_ptr(), bt.shape, bt.stride()))
-        d = self.__dict__.get("_desc")
-        if d is not None and self.__dict__.get("_desc_key") == key:
-            return d
+        key = own.get("_desc_key")
+        if key is not None:
+            k_p, v_p, kv, pos_p, pos_s, n_p, n_s, sl_p, sl_s, bt_p, bt_s = key
+            if (K.data_ptr() == k_p and V.data_ptr() == v_p and pos.data_ptr() == pos_p and
+                    n.data_ptr() == n_p and sl.data_ptr() == sl_p and K.shape == kv and
+                    V.shape == kv and pos.shape == pos_s and n.shape == n_s and
+                    sl.shape == sl_s and K.is_contiguous() and V.is_contiguous() and
+                    pos.is_contiguous() and n.is_contiguous() and sl.is_contiguous() and
+                    (bt_p is None if bt is None else
+                     bt.data_ptr() == bt_p and bt.shape == bt_s and bt.is_contiguous())):
+                return own["_desc"]
         d = SlotCacheDesc(self.B, self.Hkv, self.D, self.C, _ptr(self.K), _ptr(self.V),
                           _ptr(self.pos), _ptr(self.n), _ptr(self.seqlen),
                           _ptr(self.block_table), self.num_pages)
-        self.__dict__["_desc"], self.__dict__["_desc_key"] = d, key
-        self.__dict__["_desc_p"] = C.pointer(d)
+        own["_desc_key"] = (K.data_ptr(), V.data_ptr(), K.shape, pos.data_ptr(), pos.shape,
+                            n.data_ptr(), n.shape, sl.data_ptr(), sl.shape,
+                            None if bt is None else bt.data_ptr(),
+                            None if bt is None else bt.shape)
+        own["_desc"] = d
+        own["_desc_p"] = C.pointer(d)
         return d
 
 
