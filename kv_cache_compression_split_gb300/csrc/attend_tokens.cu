@@ -403,13 +403,16 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
         int n_it = 0, n_q = 0;   // ring slots and query loads
         bool ok = true;
         int n_clc = 0;
+        int asked = -1;   // the launch-control request whose answer is still to come
         for (int k = 0; ok; ++n_clc) {
             TokItem it;
             it.b = -1;
             if (idx >= 0) {
                 // the next item while this one runs: take over a CTA that has not started
-                if (lane == 0)
+                if (lane == 0) {
                     clc_request(clc, clc_full);
+                    asked = n_clc;
+                }
                 if (!walk.find<CHUNK>(p, tpt, TILES, TK, idx, it))
                     it.j0 = it.j1 = it.two = 0;   // the grid is an upper bound
             }
@@ -516,16 +519,19 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
             int next = -1;
             if (lane == 0 && ok) {
                 ok = mbar_sleep_or_abort(clc_full, n_clc & 1, abort);
-                if (ok)
+                if (ok) {
                     next = clc_answer(clc);
+                    asked = -1;
+                }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
             idx = __shfl_sync(0xffffffffu, next, 0);
         }
-        // every copy has landed before the CTA leaves
+        // every copy, and the answer to a request after which a wait ran out, has landed before
+        // the CTA leaves
         if (lane == 0) {
-            if (!ok && idx >= 0)
-                mbar_wait(clc_full, n_clc & 1);
+            if (asked >= 0)
+                mbar_wait(clc_full, asked & 1);
 #pragma unroll 1
             for (int i = n_it > NS ? n_it - NS : 0; i < n_it; ++i)
                 mbar_wait(&kv_full[i % NS], (i / NS) & 1);
