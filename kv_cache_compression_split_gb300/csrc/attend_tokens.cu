@@ -53,8 +53,7 @@
 // Non-finite values.  A masked score is replaced, not added to, so keys behind a
 // row's range never matter.  A masked value row would enter as 0 * v: rows behind the
 // sequence's last key are cleared in shared memory, and a row whose result is not
-// finite although its sum is computes its channels again from memory over the keys it
-// sees alone.
+// finite although its sum is gets it again from memory (rows_again).
 #include "kvc_device.cuh"
 #include "kvc_internal.h"
 
@@ -275,41 +274,204 @@ __device__ __forceinline__ float prob64(uint32_t taddr, const float (&x)[64], fl
     return a.x + a.y;
 }
 
-// The 32 channels from c0 of one row, from memory, over the keys [first, last]: for a
-// row whose tensor-core result is not finite although its sum l is.
-template <bool CHUNK>
-__device__ __noinline__ void row_again(const TokensLaunch &p, const TokItem &it, const uint16_t *q,
-                                       int first, int last, float ref, int c0, float scale,
-                                       uint16_t *o, float4 *part, long stride)
+// 4 (D = 128) or 2 (D = 64) channels of a row: a lane's share when a warp reads it whole.
+template <int CH> struct Channels {
+    uint32_t w[CH / 2];
+    __device__ void load(const uint16_t *row)
+    {
+        if constexpr (CH == 4) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(row);
+            w[0] = x.x;
+            w[1] = x.y;
+        } else {
+            w[0] = *reinterpret_cast<const uint32_t *>(row);
+        }
+    }
+    __device__ uint16_t bits(int c) const { return (uint16_t)(w[c / 2] >> 16 * (c & 1)); }
+    __device__ float value(int c) const { return __half2float(__ushort_as_half(bits(c))); }
+    // Not 0 when some channel is not finite (an exponent of ones).
+    __device__ uint32_t odd() const
+    {
+        uint32_t x = 0;
+#pragma unroll
+        for (int i = 0; i < CH / 2; ++i)
+            x |= ((w[i] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+        return x;
+    }
+};
+
+// The results of the rows `rows` (bits: lanes) of a warp whose tensor-core result is not
+// finite although their sum is: some value row of the keys [first, end) that the tile went
+// through is not.  The warp looks for such values first, every lane in its own channels.  A
+// channel in which a row attends one has its result by that alone: NaN, or an infinity where
+// all that it attends have one sign.  Only a row with a channel whose values of that kind all
+// lie behind it (they entered as 0 * v) is computed again, R rows together: a key's scores per
+// lane, then the lane's channels over the 32 keys.  So a value that is not finite costs the
+// rows behind it a pass over the values, and only the rows of its own tile are computed again:
+// 200 003 tokens of 8 heads over one of 128 channels take 46 ms, 600 ms with a NaN in the last
+// tile and 480 ms with one in the first.
+template <int D, bool CHUNK>
+__device__ __noinline__ void rows_again(const TokensLaunch &p, const TokItem &it, unsigned rows,
+                                        const uint16_t *q, int first, int end, int last, float ref,
+                                        float scale, uint16_t *o, float4 *part, long stride,
+                                        volatile uint32_t *active)
 {
-    float acc[32];
+    constexpr int CH = D / 32, U = 8, R = 2;
+    constexpr unsigned ALL = 0xffffffffu;
+    constexpr int NEVER = 0x7fffffff;
+    using Vec = Channels<CH>;
+    const int lane = threadIdx.x & 31, c0 = CH * lane;
+    auto from = [&](auto *ptr, int src) {
+        return reinterpret_cast<decltype(ptr)>(
+            __shfl_sync(ALL, reinterpret_cast<unsigned long long>(ptr), src));
+    };
+    // per channel: the first key with a NaN, +inf, -inf, and the last key with any of them
+    int nan_at[CH], pos_at[CH], neg_at[CH], any_at[CH];
 #pragma unroll
-    for (int c = 0; c < 32; ++c)
-        acc[c] = 0.f;
-#pragma unroll 1
-    for (int j = first; j <= last; ++j) {
-        const uint16_t *k = key_row<CHUNK>(p, p.k, p.ks, it, j);
-        const uint16_t *v = key_row<CHUNK>(p, p.v, p.vs, it, j);
-        if (!k)
-            continue;
-        float s = 0.f;
-#pragma unroll 1
-        for (int d = 0; d < p.D; ++d)
-            s = fmaf(__half2float(__ushort_as_half(q[d])), __half2float(__ushort_as_half(k[d])), s);
-        const float w = ex2(s * p.scale_log2 - ref);
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-            acc[c] = fmaf(w, __half2float(__ushort_as_half(v[c0 + c])), acc[c]);
+    for (int c = 0; c < CH; ++c) {
+        nan_at[c] = pos_at[c] = neg_at[c] = NEVER;
+        any_at[c] = -1;
     }
+#pragma unroll 1
+    for (int j = first; j < end; j += 2 * U) {
+        *active = globaltimer_lo();
+        Vec x[2 * U];
+        uint32_t odd = 0;
 #pragma unroll
-    for (int c = 0; c < 32; c += 4) {
-        if (part)
-            part[(c0 + c) / 4 * stride] = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+        for (int u = 0; u < 2 * U; ++u) {
+            const uint16_t *v = j + u < end ? key_row<CHUNK>(p, p.v, p.vs, it, j + u) : nullptr;
+            x[u] = Vec{};
+            if (v)
+                x[u].load(v + c0);
+        }
+#pragma unroll
+        for (int u = 0; u < 2 * U; ++u)
+            odd |= x[u].odd();
+        if (odd)
+#pragma unroll
+            for (int u = 0; u < 2 * U; ++u)
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const uint32_t h = x[u].bits(c);
+                    if ((h & 0x7c00u) != 0x7c00u)
+                        continue;
+                    any_at[c] = j + u;
+                    const bool nan = h & 0x3ffu, neg = h & 0x8000u;
+                    nan_at[c] = min(nan_at[c], nan ? j + u : NEVER);
+                    pos_at[c] = min(pos_at[c], nan || neg ? NEVER : j + u);
+                    neg_at[c] = min(neg_at[c], nan || !neg ? NEVER : j + u);
+                }
+    }
+    auto attended = [&](int c, int lim) {
+        return nan_at[c] <= lim || pos_at[c] <= lim || neg_at[c] <= lim;
+    };
+    auto store = [&](uint16_t *to, float4 *to4, int c, float x) {
+        if (to4)
+            reinterpret_cast<float *>(to4 + (c0 + c) / 4 * stride)[(c0 + c) % 4] = x;
         else
+            to[c0 + c] = __half_as_ushort(__float2half_rn(x));
+    };
+    unsigned again = 0;
+#pragma unroll 1
+    for (unsigned left = rows; left; left &= left - 1) {
+        const int src = __ffs(left) - 1, lim = __shfl_sync(ALL, last, src);
+        uint16_t *to = from(o, src);
+        float4 *to4 = from(part, src);
+        bool behind = false;
 #pragma unroll
-            for (int x = c; x < c + 4; ++x)
-                o[c0 + x] = __half_as_ushort(__float2half_rn(acc[x] * scale));
+        for (int c = 0; c < CH; ++c) {
+            const bool neg = neg_at[c] <= lim, pos = pos_at[c] <= lim;
+            const bool nan = nan_at[c] <= lim || (neg && pos);
+            behind |= !attended(c, lim) && any_at[c] > lim;
+            if (attended(c, lim))
+                store(to, to4, c, nan ? NAN : pos ? INFINITY : -INFINITY);
+        }
+        if (__any_sync(ALL, behind))
+            again |= 1u << src;
     }
+#pragma unroll 1
+    while (again) {
+        int src[R], lim[R], most = -1;   // rows that there are not: the last one once more
+        const uint16_t *qr[R];
+        float m[R], acc[R][CH];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            src[r] = again ? __ffs(again) - 1 : src[r ? r - 1 : 0];
+            again &= again - 1;
+            lim[r] = __shfl_sync(ALL, last, src[r]);
+            m[r] = __shfl_sync(ALL, ref, src[r]);
+            qr[r] = from(q, src[r]);
+            most = max(most, lim[r]);
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                acc[r][c] = 0.f;
+        }
+        const int stop = min(end, most + 1);
+#pragma unroll 1
+        for (int j0 = first; j0 < stop; j0 += 32) {
+            *active = globaltimer_lo();
+            const int j = j0 + lane;
+            const uint16_t *k = j < stop ? key_row<CHUNK>(p, p.k, p.ks, it, j) : nullptr;
+            const uint16_t *v = k ? key_row<CHUNK>(p, p.v, p.vs, it, j) : nullptr;
+            float w[R] = {};
+            if (k) {
+#pragma unroll 4
+                for (int d = 0; d < D; d += 8) {
+                    const uint4 b = *reinterpret_cast<const uint4 *>(k + d);
+                    const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const uint4 a = *reinterpret_cast<const uint4 *>(qr[r] + d);
+                        const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&aw[i]));
+                            const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&bw[i]));
+                            w[r] = fmaf(y.x, z.x, fmaf(y.y, z.y, w[r]));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    w[r] = j <= lim[r] ? ex2(w[r] * p.scale_log2 - m[r]) : 0.f;
+            }
+#pragma unroll 1
+            for (int i = 0; i < 32; i += U) {
+                Vec y[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const uint16_t *vr = from(v, i + u);
+                    y[u] = Vec{};
+                    if (vr)
+                        y[u].load(vr + c0);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const bool odd = y[u].odd();   // behind the row, or its channel has its result
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const float wi = __shfl_sync(ALL, w[r], i + u);
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            const float x = y[u].value(c);
+                            acc[r][c] = fmaf(wi, odd && !(fabsf(x) < INFINITY) ? 0.f : x, acc[r][c]);
+                        }
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float f = __shfl_sync(ALL, scale, src[r]);
+            uint16_t *to = from(o, src[r]);
+            float4 *to4 = from(part, src[r]);
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                if (!attended(c, lim[r]))
+                    store(to, to4, c, acc[r][c] * f);
+        }
+    }
+    *active = globaltimer_lo();
 }
 
 template <int D, int TILES, bool CHUNK>
@@ -336,6 +498,8 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
     TokItem *s_item = reinterpret_cast<TokItem *>(clc + 1);
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(s_item + NI);
     volatile int *abort = reinterpret_cast<int *>(s_tmem + 1);
+    // when a warp was last seen computing rows again
+    volatile uint32_t *active = s_tmem + 2;
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int g = p.Hq / p.Hkv, tpt = TM / g;
@@ -344,6 +508,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
     asm volatile("griddepcontrol.launch_dependents;");
     if (threadIdx.x == 0) {
         *abort = 0;
+        *active = 0;
         for (int i = 0; i < NS; ++i) {
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 1);
@@ -376,10 +541,18 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
 
+    // The others' waits run out only when no warp has been computing rows again for as long.
+    auto spin = [&](uint64_t *bar, uint32_t parity) {
+        return mbar_wait_or_abort(bar, parity, abort, active);
+    };
+    auto rest = [&](uint64_t *bar, uint32_t parity) {
+        return mbar_sleep_or_abort(bar, parity, abort, active);
+    };
+
     // The k-th item of the feed; false at the end (or after a wait that ran out).
     auto feed_get = [&](int k, TokItem &it) -> bool {
         const int slot = k % NI;
-        const bool got = mbar_sleep_or_abort(&it_full[slot], (k / NI) & 1, abort);
+        const bool got = rest(&it_full[slot], (k / NI) & 1);
         if (!__all_sync(0xffffffffu, got))
             return false;
         it = s_item[slot];
@@ -419,7 +592,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
             if (idx < 0 || it.b >= 0) {
                 const int slot = k % NI;
                 if (lane == 0) {
-                    ok = k < NI || mbar_sleep_or_abort(&it_empty[slot], ((k / NI) & 1) ^ 1, abort);
+                    ok = k < NI || rest(&it_empty[slot], ((k / NI) & 1) ^ 1);
                     if (ok) {
                         s_item[slot] = it;
                         mbar_arrive(&it_full[slot]);
@@ -443,7 +616,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 auto load = [&](const CUtensorMap *map, int j) {
                     const int st = n_it % NS;
                     if (n_it >= NS)
-                        ok = ok && mbar_sleep_or_abort(&kv_empty[st], ((n_it / NS) & 1) ^ 1, abort);
+                        ok = ok && rest(&kv_empty[st], ((n_it / NS) & 1) ^ 1);
                     if (!ok)
                         return;
                     mbar_arrive_expect_tx(&kv_full[st], Cfg::TILE_BYTES);
@@ -486,7 +659,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 for (int i = 0; ok && i < ahead && i < n; ++i)
                     load(&maps.k, it.j0 + i);
                 if (ok && n_q > 0)
-                    ok = mbar_sleep_or_abort(q_empty, (n_q - 1) & 1, abort);
+                    ok = rest(q_empty, (n_q - 1) & 1);
                 if (ok) {
                     const int tiles = it.ntok > tpt ? 2 : 1;
                     mbar_arrive_expect_tx(q_full, tiles * Cfg::NBOX * tpt * g * 128);
@@ -518,7 +691,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
             }
             int next = -1;
             if (lane == 0 && ok) {
-                ok = mbar_sleep_or_abort(clc_full, n_clc & 1, abort);
+                ok = rest(clc_full, n_clc & 1);
                 if (ok) {
                     next = clc_answer(clc);
                     asked = -1;
@@ -552,7 +725,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
         const uint64_t k_desc = sdesc_k_sw128(smem_u32(ring));
         const uint64_t v_desc = sdesc_mn_sw128(smem_u32(ring), Cfg::BOX_BYTES);
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, abort));
+            ok = ok && __all_sync(0xffffffffu, spin(bar, parity));
         };
         // t as a type: its TMEM columns and barrier are constants then
         auto qk = [&](auto t_, int tile, int st) {   // S_t = Q_tile K^T, K in ring stage st
@@ -755,7 +928,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 const int sb = TILES == 2 ? t : i & 1;
                 const uint32_t s_col = lanes + TK * sb;
                 const int ph = TILES == 2 || !sb ? n_s[0]++ : n_s[1]++;
-                const bool got = mbar_wait_or_abort(&s_full[sb], ph & 1, abort);
+                const bool got = spin(&s_full[sb], ph & 1);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
@@ -789,9 +962,9 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                     // tile: they may be ahead of it
                     if (TILES == 1 && i > 0) {
                         const int e = (i - 1) & 1;   // the product before: its barrier and phase
-                        const bool rest = mbar_wait_or_abort(
-                            &o_full[e], ((e ? n_o[1] : n_o[0]) + ((i - 1) >> 1)) & 1, abort);
-                        if (!__all_sync(0xffffffffu, rest)) {
+                        const bool done =
+                            spin(&o_full[e], ((e ? n_o[1] : n_o[0]) + ((i - 1) >> 1)) & 1);
+                        if (!__all_sync(0xffffffffu, done)) {
                             ok = false;
                             break;
                         }
@@ -827,12 +1000,12 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 // barrier nothing but it can be outstanding, and a parity tells enough.
                 bool got;
                 if (TILES == 2) {
-                    got = mbar_wait_or_abort(&o_full[t], n_o[0]++ & 1, abort);
+                    got = spin(&o_full[t], n_o[0]++ & 1);
                 } else {
                     const int e = (rg.count - 1) & 1;
                     n_o[0] += (rg.count + 1) / 2;
                     n_o[1] += rg.count / 2;
-                    got = mbar_wait_or_abort(&o_full[e], ((e ? n_o[1] : n_o[0]) - 1) & 1, abort);
+                    got = spin(&o_full[e], ((e ? n_o[1] : n_o[0]) - 1) & 1);
                 }
                 if (!__all_sync(0xffffffffu, got))
                     break;
@@ -873,7 +1046,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                     }
                     __syncwarp();
                     mbar_arrive_warp(&mrg_full[quarter]);
-                    const bool got = mbar_wait_or_abort(&mrg_empty[quarter], n_m & 1, abort);
+                    const bool got = spin(&mrg_empty[quarter], n_m & 1);
                     if (!__all_sync(0xffffffffu, got)) {
                         ok = false;
                         break;
@@ -882,7 +1055,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 tc_fence_before();
                 continue;
             }
-            unsigned bad = 0;
+            bool bad = false;
             float fa = 1.f, fb = 0.f;        // weights of the two parts of the blocks
             float inv = 1.f, lsum = l;
             // The area's rows are swizzled as TMA does it: 16-byte chunk ch of row r lies at
@@ -934,14 +1107,13 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                         bulk_commit();
                     }
                     const float2 z = fadd2(z0, z1);
-                    if (z.x + z.y != 0.f)
-                        bad |= 1u << (c / 32);
+                    bad |= z.x + z.y != 0.f;
                 }
             } else {
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 if (TILES == 2 && it.two) {
-                    const bool got = mbar_wait_or_abort(&mrg_full[quarter], n_m & 1, abort);
+                    const bool got = spin(&mrg_full[quarter], n_m & 1);
                     if (!__all_sync(0xffffffffu, got)) {
                         ok = false;
                         break;
@@ -983,8 +1155,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
 #pragma unroll
                 for (int u = 0; u < 32; u += 2)
                     probe = ffma2(make_float2(v[u], v[u + 1]), make_float2(0.f, 0.f), probe);
-                if (probe.x + probe.y != 0.f)
-                    bad |= 1u << (c / 32);
+                bad |= probe.x + probe.y != 0.f;
                 // parts of rows, and tiles that end inside a warp's rows: each thread stores
                 // its own row
                 if (real && part) {
@@ -1006,6 +1177,13 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
             }
             if (!ok)
                 break;
+            if (real) {
+                if (part)
+                    p.part_ml[part_at(1)] = make_float2(m, lsum);
+                else if (p.lse)
+                    p.lse[(packed ? 0 : it.b) * p.ls[0] + head * p.ls[1] + tok] =
+                        lsum > 0.f ? (m + __log2f(lsum)) * LN2 : lsum == 0.f ? -INFINITY : lsum;
+            }
             const bool again = real && bad && lsum < INFINITY;   // false for a sum that is NaN
             if (__any_sync(0xffffffffu, again)) {
                 if (elect_one())
@@ -1013,19 +1191,11 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 __syncwarp();
                 const uint16_t *q = p.q + (packed ? 0 : it.b) * p.qs[0] + head * p.qs[1] +
                                     tok * p.qs[2];
-#pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32)
-                    if (again && bad >> (c0 / 32) & 1)
-                        row_again<CHUNK>(p, it, q, it.j0 * TK, min(last, it.j1 * TK - 1),
-                                  m == -INFINITY ? 0.f : m, c0, inv, o_row(),
-                                  part ? part_o() : nullptr, rows);
-            }
-            if (real) {
-                if (part)
-                    p.part_ml[part_at(1)] = make_float2(m, lsum);
-                else if (p.lse)
-                    p.lse[(packed ? 0 : it.b) * p.ls[0] + head * p.ls[1] + tok] =
-                        lsum > 0.f ? (m + __log2f(lsum)) * LN2 : lsum == 0.f ? -INFINITY : lsum;
+                const int end = max(0, it.shift + it.tok0 + it.ntok);   // keys of the item
+                const TokItem item = it;   // it stays in registers
+                rows_again<D, CHUNK>(p, item, __ballot_sync(0xffffffffu, again), q, it.j0 * TK,
+                                     min(end, it.j1 * TK), last, m == -INFINITY ? 0.f : m, inv,
+                                     o_row(), part ? part_o() : nullptr, rows, active);
             }
             tc_fence_before();
         }

@@ -256,6 +256,59 @@ __device__ __forceinline__ bool mbar_sleep_or_abort(uint64_t *bar, uint32_t pari
     }
 }
 
+// The same two waits for a CTA in which warps may be at work that takes long but ends by
+// itself: they write the time to *active meanwhile, and a wait gives up when that lies past the
+// limit too.  Times are the clock's low words.  Their differences come round every 4.29 s; both
+// are past the limit of 2 s in more than half of that, so in a part of every round at once.
+__device__ __forceinline__ uint32_t globaltimer_lo()
+{
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+
+__device__ __forceinline__ bool wait_expired(uint32_t t0, volatile int *abort,
+                                             const volatile uint32_t *active)
+{
+    constexpr uint32_t LIMIT = (uint32_t)WAIT_LIMIT_NS;
+    constexpr uint32_t SKEW = 1u << 20;   // *active may be a tick ahead of now
+    const uint32_t now = globaltimer_lo();
+    if (now - t0 <= LIMIT || now - *active + SKEW <= LIMIT + SKEW)
+        return false;
+    *abort = 1;
+    return true;
+}
+
+__device__ __forceinline__ bool mbar_wait_or_abort(uint64_t *bar, uint32_t parity,
+                                                   volatile int *abort,
+                                                   const volatile uint32_t *active)
+{
+    if (mbar_try_wait(bar, parity))
+        return true;
+    const uint32_t t0 = globaltimer_lo();
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity))
+            return true;
+        if ((i & 255u) == 0 && (*abort || wait_expired(t0, abort, active)))
+            return false;
+    }
+}
+
+__device__ __forceinline__ bool mbar_sleep_or_abort(uint64_t *bar, uint32_t parity,
+                                                    volatile int *abort,
+                                                    const volatile uint32_t *active)
+{
+    if (mbar_try_wait_sleep(bar, parity))
+        return true;
+    const uint32_t t0 = globaltimer_lo();
+    for (;;) {
+        if (mbar_try_wait_sleep(bar, parity))
+            return true;
+        if (*abort || wait_expired(t0, abort, active))
+            return false;
+    }
+}
+
 // ---------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap *map)

@@ -1,0 +1,82 @@
+"""Prompt and chunk attention where they can go wrong at length: value rows that are not finite
+far from the rows that are computed again."""
+import numpy as np
+import pytest
+import torch
+
+from helpers import device_status_clean
+from token_refs import attend_rows, check_rows
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def kvc():
+    import kv_cache_compression_split_gb300 as k
+    k.lib()
+    return k
+
+
+def _cu(lens):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _randn(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda").half()
+
+
+@pytest.mark.parametrize("Hq,D,at", [(8, 128, 200_003 - 10), (8, 128, 5), (8, 64, 200_003 - 30),
+                                     (1, 128, 200_003 - 100)])
+def test_long_prompt_with_a_value_row_that_is_not_finite(kvc, Hq, D, at):
+    """An infinity and a NaN in one value row of 200 003, in the last tile or the first one: the
+    rows before it are what they are without it, the rows from it on have them in those two
+    channels, and no wait inside the kernel runs out meanwhile."""
+    L = 200_003
+    gen = _gen(at + D)
+    q, k, v = _randn(gen, L, Hq, D), _randn(gen, L, 1, D), _randn(gen, L, 1, D)
+    clean = v.clone()
+    v[at, 0, 5], v[at, 0, 41] = float("-inf"), float("nan")
+    o, lse = torch.full_like(q, 7.0), torch.full((Hq, L), 7.0, device="cuda")
+    kvc.kvc_prompt_attend(q, k, v, o, cu_seqlens=_cu([L]), lse=lse)
+    assert device_status_clean(kvc)
+    keep = torch.ones(D, dtype=torch.bool, device="cuda")
+    keep[5] = keep[41] = False
+    before = torch.arange(max(0, at - 130), at)
+    behind = torch.unique(torch.cat([torch.arange(at, min(L, at + 40)), torch.arange(at, L, 19_001)]))
+    for h in {0, Hq - 1}:
+        check_rows(o[before, h], lse[h, before],
+                   attend_rows(q[before, h], k[:at, 0], clean[:at, 0], before), f"before, h={h}")
+        ro, rl, to, tl = attend_rows(q[behind, h], k[:, 0], clean[:, 0], behind)
+        check_rows(o[behind, h][:, keep], lse[h, behind], (ro[:, keep], rl, to[:, keep], tl),
+                   f"behind, h={h}")
+    assert torch.isneginf(o[at:, :, 5]).all() and torch.isnan(o[at:, :, 41]).all()
+    assert torch.isfinite(o[:at]).all() and torch.isfinite(o[at:][:, :, keep]).all()
+
+
+@pytest.mark.parametrize("D,splits", [(128, 0), (128, 1), (64, 3)])
+def test_long_chunk_with_values_that_are_not_finite(kvc, D, splits):
+    """A chunk over 100 000 slots whose newest value row is NaN throughout: the chunk's other
+    tokens do not attend it."""
+    C, n, m, Hq = 100_032, 100_001, 9, 8
+    gen = _gen(D + splits)
+    cache = kvc.SlotCache.empty(1, 2, C, D)
+    cache.K.copy_(_randn(gen, 1, 2, C, D))
+    cache.V.copy_(_randn(gen, 1, 2, C, D))
+    cache.n.fill_(n)
+    clean = cache.V.clone()
+    cache.V[0, 0, n - 1] = float("nan")
+    cache.V[0, 1, n - 1, 7] = float("inf")
+    q = _randn(gen, m, Hq, D)
+    o, lse = torch.full_like(q, 7.0), torch.full((Hq, m), 7.0, device="cuda")
+    ws = torch.empty(max(kvc.kvc_chunk_workspace_size(cache, q, splits) // 4, 4), device="cuda")
+    kvc.kvc_chunk_attend(cache, q, _cu([m]), o, lse=lse, workspace=ws, num_splits=splits)
+    assert device_status_clean(kvc)
+    assert torch.isnan(o[-1, :4]).all() and torch.isposinf(o[-1, 4:, 7]).all()
+    last = n - m + torch.arange(m)
+    for h in range(Hq):
+        ref = attend_rows(q[:, h], cache.K[0, h // 4, :n], clean[0, h // 4, :n], last)
+        check_rows(o[:-1, h], lse[h, :-1], tuple(x[:-1] for x in ref), f"h={h}")
