@@ -29,8 +29,11 @@
 // O += P V with O in TMEM.  The MMA warp issues O_t(j) and S_t(j + 1) of one tile
 // back to back, so when S_t(j + 1) is complete O_t is at rest and its rows may be
 // rescaled by their threads.  They rarely are: the reference follows the maximum only
-// when that has grown by 2^8 (probabilities then stay below 2^8, far inside binary16
-// and with the same relative rounding, 2^-11, as below 1).  Results leave through a
+// when that has grown by 2^8, and it lies 2^7 below the maximum that set it.  Probabilities
+// then stay within 2^15, inside binary16, and are rounded by 2^-11 relative down to 2^-21 of
+// the row's largest and by 2^-32 of it below that: with the reference at the maximum itself a
+// weight under 2^-25 of the largest became 0, and 131 071 such keys were 0.3% of a row, whose
+// sum had them and whose values had not.  Results leave through a
 // small area of shared memory per warp, so that a warp stores whole rows: a thread that
 // stores its own row touches 32 lines per instruction, which took 7000 clocks a tile.
 //
@@ -67,7 +70,9 @@ constexpr int TM = 128;                   // rows of a tile
 constexpr int BOX = 64;                   // keys of one TMA box (a page of the cache)
 constexpr int NI = 2;                     // slots of the item feed
 constexpr float LN2 = 0.6931471805599453f;
-constexpr float GROWTH = 8.f;             // log2 growth of the maximum that moves the reference
+// The reference is log2 BELOW under the maximum that set it and moves when the maximum has
+// grown by log2 GROWTH: probabilities reach 2^15, inside binary16.
+constexpr float BELOW = 7.f, GROWTH = 8.f;
 
 template <int D, int TILES> struct TokCfg {
     static constexpr int W_TMA = 4 * TILES, W_MMA = W_TMA + 1;   // two more warps are idle
@@ -952,11 +957,11 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                     top = fmaxf(top, max64(hi));
                 }
                 const float mx = scale * top;
-                const bool grow = mx > m + GROWTH;
+                const bool grow = mx > m + (BELOW + GROWTH);
                 if (__any_sync(0xffffffffu, grow)) {
-                    const float f = grow ? ex2(m - mx) : 1.f;   // 0 at the row's first key
-                    if (grow)
-                        m = mx;
+                    const float to = grow ? mx - BELOW : m;
+                    const float f = grow ? ex2(m - to) : 1.f;   // 0 at the row's first key
+                    m = to;
                     l *= f;
                     // two tiles: the scores were computed after the last product into O; one
                     // tile: they may be ahead of it

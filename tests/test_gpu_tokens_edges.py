@@ -1,5 +1,5 @@
 """Prompt and chunk attention where they can go wrong at length: value rows that are not finite
-far from the rows that are computed again."""
+far from the rows that are computed again, and many keys of little weight beside a strong one."""
 import numpy as np
 import pytest
 import torch
@@ -80,3 +80,58 @@ def test_long_chunk_with_values_that_are_not_finite(kvc, D, splits):
     for h in range(Hq):
         ref = attend_rows(q[:, h], cache.K[0, h // 4, :n], clean[0, h // 4, :n], last)
         check_rows(o[:-1, h], lse[h, :-1], tuple(x[:-1] for x in ref), f"h={h}")
+
+
+def _weak(D, n, dev="cuda"):
+    """n keys of which the first has the score 17.5 (25.2 in powers of two) and the others 0, so
+    that their weights are below 2^-25 of the first one's, each; together they are 0.3% of the
+    131 072 keys' weight, with values a hundred times the first one's."""
+    k = torch.zeros(n, D, dtype=torch.float16, device=dev)
+    k[0, 0] = 3.5
+    v = torch.full((n, D), 100.0, dtype=torch.float16, device=dev)
+    v[:, 1::2] = -50.0
+    v[0] = 1.0
+    return k, v
+
+
+def _check_weak(o, lse, q, k, v, last):
+    """As check_rows, with weights rounded by 2^-32 of the row's largest at most where they are
+    not held to 2^-11 (the references in token_refs allow 2^-25)."""
+    ro, rl, to, tl = attend_rows(q, k, v, last, 1.0)
+    count = (last + 1).clamp(0, k.shape[0]).double().to(to.device)[:, None]
+    to = to - count * (2.0 ** -25 - 2.0 ** -32) * v.double().abs().max()
+    check_rows(o, lse, (ro, rl, to, tl))
+
+
+@pytest.mark.parametrize("Hq,D,L", [(1, 128, 131_072), (8, 128, 131_072), (2, 64, 131_072),
+                                    (8, 128, 1000)])
+def test_prompt_many_keys_of_little_weight(kvc, Hq, D, L):
+    k, v = _weak(D, L)
+    q = torch.zeros(L, Hq, D, dtype=torch.float16, device="cuda")
+    q[:, :, 0] = 5.0
+    o, lse = torch.full_like(q, 7.0), torch.full((Hq, L), 7.0, device="cuda")
+    kvc.kvc_prompt_attend(q, k[:, None], v[:, None], o, cu_seqlens=_cu([L]), lse=lse,
+                          softmax_scale=1.0)
+    assert device_status_clean(kvc)
+    rows = torch.unique(torch.cat([torch.arange(0, L, max(1, L // 20)), torch.arange(L - 5, L)]))
+    for h in range(Hq):
+        _check_weak(o[rows, h], lse[h, rows], q[rows, h], k, v, rows)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("splits", [0, 1, 3])
+def test_chunk_many_keys_of_little_weight(kvc, D, splits):
+    C, m = 131_072, 3
+    k, v = _weak(D, C)
+    cache = kvc.SlotCache.empty(1, 1, C, D)
+    cache.K[0, 0], cache.V[0, 0] = k, v
+    cache.n.fill_(C)
+    q = torch.zeros(m, 8, D, dtype=torch.float16, device="cuda")
+    q[:, :, 0] = 5.0
+    o, lse = torch.full_like(q, 7.0), torch.full((8, m), 7.0, device="cuda")
+    ws = torch.empty(max(kvc.kvc_chunk_workspace_size(cache, q, splits) // 4, 4), device="cuda")
+    kvc.kvc_chunk_attend(cache, q, _cu([m]), o, lse=lse, workspace=ws, num_splits=splits,
+                         softmax_scale=1.0)
+    assert device_status_clean(kvc)
+    for h in range(8):
+        _check_weak(o[:, h], lse[h], q[:, h], k, v, C - m + torch.arange(m))
