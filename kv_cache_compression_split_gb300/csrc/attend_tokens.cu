@@ -339,7 +339,7 @@ __device__ __noinline__ void rows_again(const TokensLaunch &p, const TokItem &it
     }
 #pragma unroll 1
     for (int j = first; j < end; j += 2 * U) {
-        *active = globaltimer_lo();
+        still_active(active);
         Vec x[2 * U];
         uint32_t odd = 0;
 #pragma unroll
@@ -414,7 +414,7 @@ __device__ __noinline__ void rows_again(const TokensLaunch &p, const TokItem &it
         const int stop = min(end, most + 1);
 #pragma unroll 1
         for (int j0 = first; j0 < stop; j0 += 32) {
-            *active = globaltimer_lo();
+            still_active(active);
             const int j = j0 + lane;
             const uint16_t *k = j < stop ? key_row<CHUNK>(p, p.k, p.ks, it, j) : nullptr;
             const uint16_t *v = k ? key_row<CHUNK>(p, p.v, p.vs, it, j) : nullptr;
@@ -476,7 +476,7 @@ __device__ __noinline__ void rows_again(const TokensLaunch &p, const TokItem &it
                     store(to, to4, c, acc[r][c] * f);
         }
     }
-    *active = globaltimer_lo();
+    still_active(active);
 }
 
 template <int D, int TILES, bool CHUNK>

@@ -257,7 +257,7 @@ __device__ __forceinline__ bool mbar_sleep_or_abort(uint64_t *bar, uint32_t pari
 }
 
 // The same two waits for a CTA in which warps may be at work that takes long but ends by
-// itself: they write the time to *active meanwhile, and a wait gives up when that lies past the
+// itself: they call still_active meanwhile, and a wait gives up when the last call lies past the
 // limit too.  Times are the clock's low words.  Their differences come round every 4.29 s; both
 // are past the limit of 2 s in more than half of that, so in a part of every round at once.
 __device__ __forceinline__ uint32_t globaltimer_lo()
@@ -267,13 +267,17 @@ __device__ __forceinline__ uint32_t globaltimer_lo()
     return t;
 }
 
+__device__ __forceinline__ void still_active(volatile uint32_t *active)
+{
+    *active = globaltimer_lo() - (1u << 20);   // not ahead of a reader's clock by a tick
+}
+
 __device__ __forceinline__ bool wait_expired(uint32_t t0, volatile int *abort,
                                              const volatile uint32_t *active)
 {
     constexpr uint32_t LIMIT = (uint32_t)WAIT_LIMIT_NS;
-    constexpr uint32_t SKEW = 1u << 20;   // *active may be a tick ahead of now
     const uint32_t now = globaltimer_lo();
-    if (now - t0 <= LIMIT || now - *active + SKEW <= LIMIT + SKEW)
+    if (now - t0 <= LIMIT || now - *active <= LIMIT)
         return false;
     *abort = 1;
     return true;
