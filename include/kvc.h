@@ -597,7 +597,8 @@ KVC_API kvc_status kvc_chunk_attend(const kvc_chunk_args *args, cudaStream_t str
  * slots n .. n + m_b - 1.  The call writes
  *   slot_map [T, Hkv]  the row of the cache's K / V arrays that token t's K/V of
  *                      head h go to (b h C + slot dense, page 64 + slot % 64 paged),
- *                      or -1: a token of a refused unit, or behind cu_new[B]
+ *                      or -1: a token of a refused unit, behind cu_new[B], or whose
+ *                      slot's table entry is no page (KVC_DEV_CAPACITY)
  *   next->pos          the new slots' positions seqlen[b] + i
  *   next->n, seqlen    n + m_b and seqlen + m_b
  * and, in the paged layout, gives every unit the pages it needs.  Unit (b, h) holds

@@ -336,10 +336,19 @@ __global__ void __launch_bounds__(THREADS) k_append_plan(const PlanLaunch p)
     cluster_wait();
 }
 
+// Whether a unit takes its tokens although the first one has no row: the entry of the first
+// new slot is then not a page, and the plan has set that slot's position.  A refused unit's
+// slot there is an older one, on a page that it holds.
+__device__ __forceinline__ bool takes_behind_bad_page(const PlanLaunch &p, int u, int slot, int pos)
+{
+    const int pg = p.table_out[(size_t)u * (p.C / PAGE_SLOTS) + slot / PAGE_SLOTS];
+    return (pg < 0 || pg >= p.num_pages) && p.pos[(size_t)u * p.C + slot] == pos;
+}
+
 // The other tokens of a large batch, a thread per token and eight heads' loads in flight
 // together.  Launched so that its CTAs may start while the plan still runs: they wait for
 // it before they read what it wrote.  The counts are the new ones by then, and the first
-// token of each unit is done: its entry says whether the unit takes its tokens.  Ranges
+// token of each unit is done: its row says that the unit takes its tokens.  Ranges
 // that run backwards cannot be bisected: then the first sequence that holds the token is
 // looked for one by one.
 __global__ void __launch_bounds__(256) k_plan_tokens(const PlanLaunch p)
@@ -387,7 +396,10 @@ __global__ void __launch_bounds__(256) k_plan_tokens(const PlanLaunch p)
         unsigned ok = 0;   // heads that take the token
 #pragma unroll
         for (int h = 0; h < HEADS; ++h) {
-            ok |= (unsigned)(first[h] >= 0 && fits(p, n[h], m)) << h;
+            bool takes = fits(p, n[h], m);
+            if (takes && first[h] < 0)
+                takes = p.table && takes_behind_bad_page(p, u + h, n[h], P - step);
+            ok |= (unsigned)takes << h;
             n[h] += step;   // the token's slot
         }
 #pragma unroll
