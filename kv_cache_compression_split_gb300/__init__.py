@@ -168,11 +168,22 @@ def _ptr(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+def _current_device():
+    """Index of the current device; -2, which no tensor's device equals, on a machine without
+    one (the checks of the arguments then say what is wrong)."""
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2
+
+
 def _desc_key(tensors):
-    """What a cache descriptor depends on: each field tensor's address, device, shape and
-    strides (None for an absent field)."""
-    return tuple(None if t is None else (t.data_ptr(), t.get_device(), t.shape, t.stride())
-                 for t in tensors)
+    """What a cache descriptor depends on: the current device, which the fields were checked
+    against, and each field tensor's address, device, shape and strides (None for an absent
+    field)."""
+    return (_current_device(),) + tuple(
+        None if t is None else (t.data_ptr(), t.get_device(), t.shape, t.stride())
+        for t in tensors)
 
 
 _DESC_CACHE_KEYS = ("_desc", "_desc_key", "_desc_p")
@@ -256,12 +267,10 @@ _pack_3p = struct.Struct("@3P").pack
 
 
 def _device(stream):
-    """Index of the current device, and the stream's handle (-2, which no tensor's device
-    equals, on a machine without one: the checks of the arguments then say what is wrong)."""
-    try:
-        dev = torch.cuda.current_device()
-    except (RuntimeError, AssertionError):
-        return -2, 0
+    """Index of the current device, and the stream's handle."""
+    dev = _current_device()
+    if dev < 0:
+        return dev, 0
     if stream is None:
         return dev, _raw_stream(dev) if _raw_stream is not None else _stream(None)
     return dev, _stream(stream)
@@ -514,7 +523,7 @@ def kvc_chunk_attend(cache: "SlotCache", q, cu_new, o, lse=None, workspace=None,
     holds their rows in the last slots (see kvc.h): q, o [T, Hq, D] packed by cu_new [B + 1]
     int32 (rows may be strided), lse [Hq, T]."""
     dev, stream = _device(stream)
-    d = cache.desc()
+    d = cache.desc(dev)
     shape = q.shape
     T, Hq, D = shape
     if D != d.D:
@@ -541,8 +550,8 @@ def kvc_append_plan(cache: "SlotCache", cu_new, slot_map, pool: "Optional[PagePo
     tokens (cu_new [B + 1] int32).  A paged cache takes its pages from `pool`.  `out` and
     `pool_out` receive the new state (default: the cache and the pool, in place)."""
     dev, stream = _device(stream)
-    d = cache.desc()
-    n = out.desc() if out is not None else d
+    d = cache.desc(dev)
+    n = out.desc(dev) if out is not None else d
     pi = pool.desc(d, dev) if pool is not None else None
     po = pool_out.desc(n, dev) if pool_out is not None else pi
     T = slot_map.shape[0]
@@ -556,7 +565,7 @@ def kvc_append_packed(cache: "SlotCache", k_new, v_new, slot_map, stream=None):
     """Packed rows k_new, v_new [T, Hkv, D] (rows may be strided) to the cache rows that
     slot_map [T, Hkv] names (kvc_append_plan writes it); n and pos are not touched."""
     dev, stream = _device(stream)
-    d = cache.desc()
+    d = cache.desc(dev)
     T, H = slot_map.shape[0], d.Hkv
     shape = (T, H, d.D)
     try:
@@ -634,18 +643,20 @@ class SlotCache:
     def __getstate__(self):
         return _state_without_desc(self)
 
-    def desc(self) -> SlotCacheDesc:
-        # built once and kept while the fields' storage and shapes stay the same and they are
-        # contiguous (a field replaced or resized in place is noticed, and the fields are
-        # checked again)
+    def desc(self, dev: Optional[int] = None) -> SlotCacheDesc:
+        # built once and kept while the current device (dev, where the caller has it), the
+        # fields' storage and shapes stay the same and they are contiguous (a field replaced or
+        # resized in place is noticed, and the fields are checked again)
         own = self.__dict__
+        if dev is None:
+            dev = _current_device()
         K, V, pos, n, sl, bt = self.K, self.V, self.pos, self.n, self.seqlen, self.block_table
         key = own.get("_desc_key")
         if key is not None:
-            k_p, v_p, kv, pos_p, pos_s, n_p, n_s, sl_p, sl_s, bt_p, bt_s = key
-            if (K.data_ptr() == k_p and V.data_ptr() == v_p and pos.data_ptr() == pos_p and
-                    n.data_ptr() == n_p and sl.data_ptr() == sl_p and K.shape == kv and
-                    V.shape == kv and pos.shape == pos_s and n.shape == n_s and
+            on, k_p, v_p, kv, pos_p, pos_s, n_p, n_s, sl_p, sl_s, bt_p, bt_s = key
+            if (on == dev and K.data_ptr() == k_p and V.data_ptr() == v_p and
+                    pos.data_ptr() == pos_p and n.data_ptr() == n_p and sl.data_ptr() == sl_p and
+                    K.shape == kv and V.shape == kv and pos.shape == pos_s and n.shape == n_s and
                     sl.shape == sl_s and K.is_contiguous() and V.is_contiguous() and
                     pos.is_contiguous() and n.is_contiguous() and sl.is_contiguous() and
                     (bt_p is None if bt is None else
@@ -654,7 +665,7 @@ class SlotCache:
         d = SlotCacheDesc(self.B, self.Hkv, self.D, self.C, _ptr(self.K), _ptr(self.V),
                           _ptr(self.pos), _ptr(self.n), _ptr(self.seqlen),
                           _ptr(self.block_table), self.num_pages)
-        own["_desc_key"] = (K.data_ptr(), V.data_ptr(), K.shape, pos.data_ptr(), pos.shape,
+        own["_desc_key"] = (dev, K.data_ptr(), V.data_ptr(), K.shape, pos.data_ptr(), pos.shape,
                             n.data_ptr(), n.shape, sl.data_ptr(), sl.shape,
                             None if bt is None else bt.data_ptr(),
                             None if bt is None else bt.shape)
@@ -770,13 +781,13 @@ class QuantCache:
         t = (self.k_blocks, self.v_blocks, self.k_res, self.v_res, self.len, self.block_table,
              self.k_gear, self.v_gear)
         key = _desc_key(t) + (self.bits, self.R, self.Cq_paged)
-        d = self.__dict__.get("_desc")
-        if d is not None and self.__dict__.get("_desc_key") == key:
-            return d
+        if self.__dict__.get("_desc_key") == key:
+            return self.__dict__["_desc"]
         d = QuantCacheDesc(self.B, self.Hkv, self.D, self.bits, self.R, self.Cq,
                            _ptr(self.k_blocks), _ptr(self.v_blocks), _ptr(self.k_res),
                            _ptr(self.v_res), _ptr(self.len), _ptr(self.block_table),
                            self.num_pages, _ptr(self.k_gear), _ptr(self.v_gear))
-        self.__dict__["_desc"], self.__dict__["_desc_key"] = d, key
+        self.__dict__["_desc"] = d
         self.__dict__["_desc_p"] = C.pointer(d)
+        self.__dict__["_desc_key"] = key      # last, as in SlotCache
         return d
