@@ -665,12 +665,13 @@ class SlotCache:
         d = SlotCacheDesc(self.B, self.Hkv, self.D, self.C, _ptr(self.K), _ptr(self.V),
                           _ptr(self.pos), _ptr(self.n), _ptr(self.seqlen),
                           _ptr(self.block_table), self.num_pages)
+        own["_desc"] = d
+        own["_desc_p"] = C.pointer(d)
+        # last: another thread that finds the key finds its descriptor
         own["_desc_key"] = (dev, K.data_ptr(), V.data_ptr(), K.shape, pos.data_ptr(), pos.shape,
                             n.data_ptr(), n.shape, sl.data_ptr(), sl.shape,
                             None if bt is None else bt.data_ptr(),
                             None if bt is None else bt.shape)
-        own["_desc"] = d
-        own["_desc_p"] = C.pointer(d)
         return d
 
 

@@ -1,4 +1,6 @@
 """CPU-only: cache descriptors and the device they were checked on."""
+import threading
+
 import pytest
 import torch
 
@@ -70,3 +72,37 @@ def test_the_calls_refuse_a_cache_of_another_device(kvc, monkeypatch):
                  lambda: kvc.kvc_append_packed(cache, q, q, DeviceTensor(64, (4, 2), 1))):
         with pytest.raises(ValueError, match="expected the current device cuda:1"):
             call()
+
+
+def test_a_descriptor_is_kept_before_its_key(kvc, monkeypatch):
+    """Whoever finds a new key finds the descriptor that goes with it."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    cache = _slot_cache(kvc)
+    first = cache.desc()
+
+    class Watch(dict):
+        def __setitem__(self, key, value):
+            seen.append(key)
+            super().__setitem__(key, value)
+
+    seen = []
+    cache.n = DeviceTensor(1 << 22, (2, 2))
+    state = Watch(cache.__dict__)
+    object.__setattr__(cache, "__dict__", state)
+    second = cache.desc()
+    assert second is not first and seen[-1] == "_desc_key" and "_desc" in seen
+    # and from other threads the two always go together
+    wrong = []
+
+    def reader():
+        for _ in range(2000):
+            d = cache.desc()
+            if d.n != cache.n.data_ptr():
+                wrong.append(d.n)
+
+    threads = [threading.Thread(target=reader) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
