@@ -609,10 +609,13 @@ KVC_API kvc_status kvc_chunk_attend(const kvc_chunk_args *args, cudaStream_t str
  * behind `need` back: their entries become -1 and, after all takes, they go on the
  * stack in unit order, each unit's lowest entry first.  Entries of the stack at and
  * behind the new count are unspecified.
- * A unit is refused, sets KVC_DEV_CAPACITY and keeps its n and pages when n + m_b
- * exceeds C or the stack cannot serve it in full (its sequence's seqlen still
- * advances, as in kvc_append).  A sequence whose range leaves [0, T] counts as
- * bringing none and sets the same bit.
+ * A unit is refused, sets KVC_DEV_CAPACITY and keeps its n and pages when n + m
+ * exceeds C, or when it needs pages and they, with those that the units before it
+ * need (refused for want of pages or not), are more than the stack holds: behind the
+ * first unit that the stack cannot serve in full every unit that needs a page is
+ * refused, whatever is left on it; units that need none are not.  The sequence's
+ * seqlen still advances, as in kvc_append.  A sequence whose range leaves [0, T]
+ * counts as bringing none and sets the same bit.
  * `next` gives the arrays to write: the cache itself and the same pool (the step in
  * place), or others of the same sizes, so that the next step can be planned while
  * this one's attention still reads the old state; then table, counts and stack are

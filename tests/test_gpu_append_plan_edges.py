@@ -66,3 +66,33 @@ def test_plan_table_entries_that_are_no_page(kvc, Hkv, scale, entry):
     assert kvc.kvc_read_device_status() == kvc.KVC_DEV_CAPACITY
     _check(want, cache, pool, slots, pos0)
     assert device_status_clean(kvc)
+
+
+@pytest.mark.parametrize("T", [None, 600])         # one kernel and two
+def test_plan_behind_a_unit_that_the_stack_cannot_serve(kvc, T):
+    """Three pages on the stack.  The first unit takes one, the second needs five and is refused,
+    the third needs two and is refused too although two are left, the fourth needs none and takes
+    its token, the fifth gives a page back."""
+    B, C = 5, 512
+    cache = kvc.SlotCache.empty_paged(B, 1, C, 64, B * C // 64)
+    pool = kvc.PagePool.empty(cache)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache.n.copy_(i32([[64], [10], [60], [3], [20]]))
+    cache.seqlen.copy_(i32([64, 10, 60, 3, 20]))
+    cache.block_table[:, 0, :2] = i32([[0, -1], [1, -1], [2, -1], [3, -1], [4, 5]])
+    pool.pages.copy_(i32([[1], [1], [1], [1], [2]]))
+    pool.free[:3] = i32([6, 7, 8])
+    pool.count.fill_(3)
+    m = [1, 300, 100, 1, 1]
+    T = T or sum(m)
+    slots = torch.full((T, 1), 12345, dtype=torch.int32, device="cuda")
+    kvc.kvc_append_plan(cache, _cu(m), slots, pool=pool, release=True)
+    torch.cuda.synchronize()
+    assert kvc.kvc_read_device_status() == kvc.KVC_DEV_CAPACITY
+    assert cache.n.flatten().tolist() == [65, 10, 60, 4, 21]
+    assert cache.seqlen.tolist() == [65, 310, 160, 4, 21]
+    assert pool.pages.flatten().tolist() == [2, 1, 1, 1, 1]
+    assert pool.free[:int(pool.count)].tolist() == [6, 7, 5]
+    want = [8 * 64] + [-1] * 400 + [3 * 64 + 3, 4 * 64 + 20] + [-1] * (T - 403)
+    assert slots.flatten().tolist() == want
+    assert device_status_clean(kvc)
