@@ -570,6 +570,11 @@ KVC_API kvc_status kvc_prompt_attend(const kvc_prompt_args *args, cudaStream_t s
  * counts as empty and sets KVC_DEV_CAPACITY; so does a sequence whose range leaves
  * [0, T]; slots of a page outside the pool read as zeros and set it too.
  * Rows of the cache behind n may hold anything.
+ * A unit that an append refused does not hold its chunk, which this call cannot tell:
+ * it sees the same slots j < n - m_b + i + 1 of what the unit does hold, so not the
+ * chunk's tokens, and for all but the last token not the newest older ones either,
+ * while other heads of the sequence may be right.  The append's KVC_DEV_CAPACITY is the
+ * sign: read the status word and drop that step's results.
  * Source: "Rethinking KV Cache Compression" guide, §16 "Prefill、decode、TP 的性能账"
  * and "前置背景、复现方法与结论边界" (the paged cache of continuous batching).
  */
@@ -609,7 +614,7 @@ KVC_API kvc_status kvc_chunk_attend(const kvc_chunk_args *args, cudaStream_t str
  * behind `need` back: their entries become -1 and, after all takes, they go on the
  * stack in unit order, each unit's lowest entry first.  Entries of the stack at and
  * behind the new count are unspecified.
- * A unit is refused, sets KVC_DEV_CAPACITY and keeps its n and pages when n + m
+ * A unit is refused, sets KVC_DEV_CAPACITY and keeps its n and pages when n + m_b
  * exceeds C, or when it needs pages and they, with those that the units before it
  * need (refused for want of pages or not), are more than the stack holds: behind the
  * first unit that the stack cannot serve in full every unit that needs a page is

@@ -521,7 +521,8 @@ def kvc_chunk_attend(cache: "SlotCache", q, cu_new, o, lse=None, workspace=None,
                      num_splits: int = 0, softmax_scale: float = 0.0, stream=None):
     """Attention of each sequence's chunk of new tokens over the slot cache, which already
     holds their rows in the last slots (see kvc.h): q, o [T, Hq, D] packed by cu_new [B + 1]
-    int32 (rows may be strided), lse [Hq, T]."""
+    int32 (rows may be strided), lse [Hq, T].  Where an append was refused
+    (kvc_read_device_status: KVC_DEV_CAPACITY) the results of that head are not its chunk's."""
     dev, stream = _device(stream)
     d = cache.desc(dev)
     shape = q.shape

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from helpers import device_status_clean
-from test_gpu_append_plan import _check, _cu, _expect, _state
+from test_gpu_append_plan import _check, _cu, _expect, _gather, _state
+from token_refs import attend_rows, check_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +97,41 @@ def test_plan_behind_a_unit_that_the_stack_cannot_serve(kvc, T):
     want = [8 * 64] + [-1] * 400 + [3 * 64 + 3, 4 * 64 + 20] + [-1] * (T - 403)
     assert slots.flatten().tolist() == want
     assert device_status_clean(kvc)
+
+
+def test_chunk_over_a_refused_unit(kvc):
+    """One head of a sequence has no room and is refused: the status word says so, the other
+    heads' rows are right, and that head's see the slots before n - m + i + 1 of what it holds."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    Hq, Hkv, D, C, m = 4, 2, 64, 128, [5, 30]
+    cache = kvc.SlotCache.empty_paged(2, Hkv, C, D, 8)
+    pool = kvc.PagePool.empty(cache)
+    x = torch.randn(250, Hq + 2 * Hkv, D, generator=g, device="cuda").half()
+
+    def enter(cu, t0, T):
+        slots = torch.empty(T, Hkv, dtype=torch.int32, device="cuda")
+        kvc.kvc_append_plan(cache, cu, slots, pool=pool)
+        w = x[t0:t0 + T]
+        kvc.kvc_append_packed(cache, w[:, Hq:Hq + Hkv], w[:, Hq + Hkv:], slots)
+        return slots
+
+    enter(_cu([100, 110]), 0, 210)
+    cache.n[1, 0] = 60                       # evicted: this head has room, the other has not
+    assert device_status_clean(kvc)
+    slots = enter(_cu(m), 210, 35)
+    torch.cuda.synchronize()
+    assert kvc.kvc_read_device_status() == kvc.KVC_DEV_CAPACITY
+    assert cache.n.tolist() == [[105, 105], [90, 110]]
+    assert (slots[5:, 1] == -1).all() and (slots[5:, 0] >= 0).all()
+    q = x[210:245, :Hq]
+    o, lse = torch.empty(35, Hq, D, dtype=torch.float16, device="cuda"), torch.empty(Hq, 35, device="cuda")
+    ws = torch.empty(max(kvc.kvc_chunk_workspace_size(cache, q) // 4, 4), device="cuda")
+    kvc.kvc_chunk_attend(cache, q, _cu(m), o, lse=lse, workspace=ws)
+    assert device_status_clean(kvc)
+    for b, w in ((0, slice(0, 5)), (1, slice(5, 35))):
+        for h in range(Hq):
+            K, V = _gather(cache, b, h // 2)
+            last = K.shape[0] - m[b] + torch.arange(m[b])
+            check_rows(o[w, h], lse[h, w], attend_rows(q[w, h], K, V, last), f"b={b} h={h}")
+            if (b, h // 2) != (1, 1):        # these hold the chunk
+                assert torch.equal(K[-m[b]:], x[210:245, Hq + h // 2][w])
