@@ -563,7 +563,10 @@ KVC_API kvc_status kvc_prompt_attend(const kvc_prompt_args *args, cudaStream_t s
  *            neither q nor the cache
  *   lse      optional [Hq, T] fp32
  *   workspace  kvc_chunk_workspace_size(args) bytes (16-byte aligned; may be NULL
- *            when that is 0); calls that may overlap on the GPU need one each
+ *            when that is 0); calls that may overlap on the GPU need one each.  Fewer
+ *            tokens may need more than many: a batch that fills the GPU by itself is not
+ *            split.  A workspace kept for calls of different T is as large as the
+ *            largest of their sizes, not as that of the largest T
  *   num_splits  0: chosen from the sizes; otherwise ranges per unit that are
  *            computed apart and merged
  * A row that sees no slot gives o = 0 and lse = -inf.  A unit whose n leaves [0, C]

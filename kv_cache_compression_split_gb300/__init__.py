@@ -510,7 +510,8 @@ def kvc_prompt_attend(q, k, v, o, cu_seqlens=None, lens=None, lse=None,
 
 
 def kvc_chunk_workspace_size(cache: "SlotCache", q, num_splits: int = 0) -> int:
-    """Bytes of workspace for kvc_chunk_attend (only q's shape is read)."""
+    """Bytes of workspace for kvc_chunk_attend (only q's shape is read).  Fewer tokens may need
+    more than many: a workspace kept for several T has the largest of their sizes."""
     cache.desc()
     args = _pack_chunk(q.shape[1], q.shape[0], C.addressof(cache.__dict__["_desc"]), 0, 0, 0, 0, 0, 0,
                        0, 0, 0, 0, num_splits, 0.0)

@@ -135,3 +135,36 @@ def test_chunk_many_keys_of_little_weight(kvc, D, splits):
     assert device_status_clean(kvc)
     for h in range(8):
         _check_weak(o[:, h], lse[h], q[:, h], k, v, C - m + torch.arange(m))
+
+
+def test_chunk_workspace_of_several_sizes(kvc):
+    """A small batch is split and needs a workspace where a large one needs none: the size of
+    the largest T does not do for the others (refused before anything is launched), the largest
+    of the sizes does for all."""
+    B, C, Hq, Hkv, D = 4, 4096, 32, 4, 128
+    gen = _gen(2)
+    cache = kvc.SlotCache.empty(B, Hkv, C, D)
+    cache.K.copy_(_randn(gen, B, Hkv, C, D))
+    cache.V.copy_(_randn(gen, B, Hkv, C, D))
+    n = [[1000, 3000, 4096, 70], [4000, 129, 2048, 800], [3333] * 4, [64, 4000, 500, 1]]
+    cache.n.copy_(torch.tensor(n, dtype=torch.int32))
+    q = _randn(gen, 2048, Hq, D)
+    sizes = {T: kvc.kvc_chunk_workspace_size(cache, q[:T]) for T in (4, 8, 64, 256, 2048)}
+    assert sizes[2048] < sizes[8] and sizes[2048] < max(sizes.values())
+    o = torch.full_like(q, 7.0)
+    small = torch.empty(sizes[2048] // 4 + 4, device="cuda")
+    with pytest.raises(kvc.KvcError) as e:
+        kvc.kvc_chunk_attend(cache, q[:8], _cu([2] * 4), o[:8], workspace=small)
+    assert e.value.status == kvc.KVC_ERR_WORKSPACE and (o == 7.0).all()
+    ws = torch.full((max(sizes.values()) // 4,), float("nan"), device="cuda")
+    for T in sizes:
+        m = T // B
+        kvc.kvc_chunk_attend(cache, q[:T], _cu([m] * B), o[:T], workspace=ws)
+        for b in range(B):
+            w = slice(b * m, b * m + m)
+            for h in range(0, Hq, 5):
+                nn = n[b][h // 8]
+                ref = attend_rows(q[w, h], cache.K[b, h // 8, :nn], cache.V[b, h // 8, :nn],
+                                  nn - m + torch.arange(m))
+                check_rows(o[w, h], None, ref, f"T={T} b={b} h={h}")
+    assert device_status_clean(kvc)
