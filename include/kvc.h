@@ -525,7 +525,8 @@ KVC_API kvc_status kvc_random_evict(const kvc_slot_cache *cache, int prompt_len,
  * a positive multiple of 8, so q, k and v may be column ranges of one projection's
  * output.  lse (optional) is fp32 with adjacent tokens: [B, Hq, L] padded,
  * [Hq, L] packed.  The padded lse is what kvc_h2o_accumulate(KVC_H2O_PREFILL) takes
- * as the rows' normalisers, so a prompt's heavy-hitter scores cost one more pass.
+ * as the rows' normalisers, so a prompt's heavy-hitter scores cost one more pass; the
+ * packed lse is not of that form, and packed prompts have no such pass.
  * o overlaps neither q, k nor v.
  * A non-finite key or value row affects the rows that attend it and no others.
  * A sequence whose range leaves [0, L] counts as empty and sets KVC_DEV_CAPACITY.
@@ -573,6 +574,11 @@ KVC_API kvc_status kvc_prompt_attend(const kvc_prompt_args *args, cudaStream_t s
  * counts as empty and sets KVC_DEV_CAPACITY; so does a sequence whose range leaves
  * [0, T]; slots of a page outside the pool read as zeros and set it too.
  * Rows of the cache behind n may hold anything.
+ * No heavy-hitter scores are kept up: the call returns no probabilities and takes no
+ * scores, and kvc_h2o_accumulate takes single decode rows or whole padded prompts.  So in
+ * a cache that is evicted by kvc_h2o_evict, what a chunk's tokens attend does not count:
+ * the chunk's slots have the score 0 and the older ones what they had, until decode steps
+ * add to them.
  * A unit that an append refused does not hold its chunk, which this call cannot tell:
  * it sees the same slots j < n - m_b + i + 1 of what the unit does hold, so not the
  * chunk's tokens, and for all but the last token not the newest older ones either,
@@ -629,7 +635,8 @@ KVC_API kvc_status kvc_chunk_attend(const kvc_chunk_args *args, cudaStream_t str
  * this one's attention still reads the old state; then table, counts and stack are
  * written in full.  An output array is either the same as its input or does not
  * overlap any input.  next->K and next->V are not used.  B * Hkv is at most
- * KVC_PLAN_MAX_UNITS.  One launch, no workspace, deterministic.
+ * KVC_PLAN_MAX_UNITS.  One launch, two for more than 512 tokens; no workspace,
+ * deterministic.
  * Source: "Rethinking KV Cache Compression" guide, §16 "前置背景、复现方法与结论边界"
  * (blocks allocated non-contiguously, batched continuously); "Practical Online KV
  * Cache Compaction for LLM Agents", §4.2 (compaction frees the tail).
