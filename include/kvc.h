@@ -629,7 +629,8 @@ KVC_API kvc_status kvc_chunk_attend(const kvc_chunk_args *args, cudaStream_t str
  * first unit that the stack cannot serve in full every unit that needs a page is
  * refused, whatever is left on it; units that need none are not.  The sequence's
  * seqlen still advances, as in kvc_append.  A sequence whose range leaves [0, T]
- * counts as bringing none and sets the same bit.
+ * counts as bringing none and sets the same bit; what a token that lies in two ranges
+ * gets is unspecified.
  * `next` gives the arrays to write: the cache itself and the same pool (the step in
  * place), or others of the same sizes, so that the next step can be planned while
  * this one's attention still reads the old state; then table, counts and stack are

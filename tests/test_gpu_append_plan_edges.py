@@ -1,5 +1,6 @@
 """The append plan where its two forms meet: batches whose slot map one cluster writes and those
-for which a second kernel follows give the same answers."""
+for which a second kernel follows give the same answers; what that kernel does with dense caches,
+bad ranges and thousands of sequences; what is refused and what a chunk sees then."""
 import numpy as np
 import pytest
 import torch
@@ -135,3 +136,81 @@ def test_chunk_over_a_refused_unit(kvc):
             check_rows(o[w, h], lse[h, w], attend_rows(q[w, h], K, V, last), f"b={b} h={h}")
             if (b, h // 2) != (1, 1):        # these hold the chunk
                 assert torch.equal(K[-m[b]:], x[210:245, Hq + h // 2][w])
+
+
+def test_plan_dense_of_many_tokens(kvc):
+    """A dense cache in a batch large enough for the second kernel, some units refused."""
+    rng = np.random.default_rng(11)
+    B, Hkv, C = 6, 9, 500
+    cache = kvc.SlotCache.empty(B, Hkv, C, 64)
+    cache.n.copy_(torch.from_numpy(rng.integers(0, C + 1, (B, Hkv)).astype(np.int32)))
+    _old_positions(cache)
+    m = np.array([150, 0, 200, 1, 130, 64])
+    T = int(m.sum()) + 7
+    want = _expect(cache, None, m, T, False)
+    pos0 = cache.pos.cpu().clone()
+    slots = torch.full((T, Hkv), 12345, dtype=torch.int32, device="cuda")
+    kvc.kvc_append_plan(cache, _cu(m), slots)
+    torch.cuda.synchronize()
+    assert T > 512 and want["refused"] and kvc.kvc_read_device_status() == kvc.KVC_DEV_CAPACITY
+    _check(want, cache, None, slots, pos0)
+    assert device_status_clean(kvc)
+
+
+@pytest.mark.parametrize("cu,m,order", [
+    ([400, 700, 0, 400], [300, 0, 400], [(0, 400), (2, 0)]),    # backwards, then over again
+    ([0, 300, 700, 2000], [300, 400, 0], [(0, 0), (1, 300)]),   # the last one leaves the batch
+    ([-5, 300, 700, 720], [0, 400, 20], [(1, 300), (2, 700)]),  # the first one starts outside
+])
+@pytest.mark.parametrize("paged", [True, False])
+def test_plan_of_many_tokens_with_bad_ranges(kvc, cu, m, order, paged):
+    """A sequence whose range leaves the batch brings nothing; the others' tokens are where
+    their ranges lie, in any order, and those of no sequence have no row."""
+    rng = np.random.default_rng(sum(m))
+    B, Hkv, C, T = 3, 8, 1024, 720
+    n = rng.integers(0, 400, (B, Hkv))
+    if paged:
+        cache, pool = _state(kvc, rng, B, Hkv, C, n, np.zeros((B, Hkv), int), 300)
+    else:
+        cache, pool = kvc.SlotCache.empty(B, Hkv, C, 64), None
+        cache.n.copy_(torch.from_numpy(n.astype(np.int32)))
+    _old_positions(cache)
+    want = _expect(cache, pool, m, sum(m), False)
+    assert not want["refused"]
+    rows, t = [[-1] * Hkv for _ in range(T)], 0
+    for b, start in sorted(order):
+        rows[start:start + m[b]] = want["slots"][t:t + m[b]]
+        t += m[b]
+    want["slots"] = rows
+    pos0 = cache.pos.cpu().clone()
+    slots = torch.full((T, Hkv), 12345, dtype=torch.int32, device="cuda")
+    kvc.kvc_append_plan(cache, torch.tensor(cu, dtype=torch.int32, device="cuda"), slots, pool=pool)
+    torch.cuda.synchronize()
+    assert kvc.kvc_read_device_status() == kvc.KVC_DEV_CAPACITY
+    _check(want, cache, pool, slots, pos0)
+    assert device_status_clean(kvc)
+
+
+@pytest.mark.parametrize("backwards", [False, True])
+def test_plan_of_thousands_of_sequences_and_many_tokens(kvc, backwards):
+    """More sequences than the second kernel keeps the starts of."""
+    rng = np.random.default_rng(13)
+    B, Hkv, C = 2500, 2, 128
+    n = rng.integers(0, C - 3, (B, Hkv))
+    cache, pool = _state(kvc, rng, B, Hkv, C, n, np.zeros((B, Hkv), int), B * Hkv)
+    _old_positions(cache)
+    m = rng.integers(0, 4, B)
+    cu = np.concatenate([[0], np.cumsum(m)])
+    T = int(cu[-1]) + 2
+    if backwards:                # the last sequence brings nothing: its end lies before its start
+        cu[-1] = cu[-2] - 3
+        m[-1] = 0
+    want = _expect(cache, pool, m, T, False)
+    assert not want["refused"]
+    pos0 = cache.pos.cpu().clone()
+    slots = torch.full((T, Hkv), 12345, dtype=torch.int32, device="cuda")
+    kvc.kvc_append_plan(cache, torch.from_numpy(cu.astype(np.int32)).cuda(), slots, pool=pool)
+    torch.cuda.synchronize()
+    assert kvc.kvc_read_device_status() == (kvc.KVC_DEV_CAPACITY if backwards else 0)
+    _check(want, cache, pool, slots, pos0)
+    assert device_status_clean(kvc)

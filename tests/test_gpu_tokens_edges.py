@@ -1,5 +1,6 @@
 """Prompt and chunk attention where they can go wrong at length: value rows that are not finite
-far from the rows that are computed again, and many keys of little weight beside a strong one."""
+far from the rows that are computed again, and many keys of little weight beside a strong one; layouts: padded batches in the two-tile form,
+projections whose tokens lie further apart than their heads, results that are a column range."""
 import numpy as np
 import pytest
 import torch
@@ -168,3 +169,92 @@ def test_chunk_workspace_of_several_sizes(kvc):
                                   nn - m + torch.arange(m))
                 check_rows(o[w, h], None, ref, f"T={T} b={b} h={h}")
     assert device_status_clean(kvc)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,L,lens", [(8, 1, 128, 1500, [1500, 3, 700, 1499]),
+                                             (3, 3, 128, 1100, [1025, 0, 1100]),
+                                             (14, 2, 128, 1300, None),
+                                             (4, 2, 64, 1200, [1200, 1001])])
+@pytest.mark.parametrize("token_major", [False, True])
+def test_padded_prompts_of_more_than_a_thousand_tokens(kvc, Hq, Hkv, D, L, lens, token_major):
+    """Two tiles per item over a padded batch.  token_major: q, k, v are [B, L, H, D] column ranges
+    of one projection, transposed, and o is a column range of a wider result, so that a token's
+    stride is larger than a head's; what lies beside them stays as it was."""
+    B = 3 if lens is None else len(lens)
+    real = [L] * B if lens is None else lens
+    gen = _gen(L + Hq)
+    if token_major:
+        wide = _randn(gen, B, L, Hq + 2 * Hkv + 1, D)
+        q, k, v = (wide[:, :, a:b].transpose(1, 2) for a, b in
+                   ((0, Hq), (Hq, Hq + Hkv), (Hq + Hkv, Hq + 2 * Hkv)))
+        room = torch.full((B, L, Hq + 3, D), 7.0, dtype=torch.float16, device="cuda")
+        o = room[:, :, 1:1 + Hq].transpose(1, 2)
+    else:
+        q = _randn(gen, B, Hq, L, D)
+        k, v = _randn(gen, B, Hkv, L + 30, D), _randn(gen, B, Hkv, L + 30, D)
+        o = torch.full_like(q, 7.0)
+    for b, n in enumerate(real):
+        q[b, :, n:] = k[b, :, n:] = v[b, :, n:] = float("nan")
+    lse = torch.full((B, Hq, L), 7.0, device="cuda")
+    dl = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    kvc.kvc_prompt_attend(q, k, v, o, lens=dl, lse=lse)
+    assert device_status_clean(kvc)
+    for b, n in enumerate(real):
+        for h in range(Hq):
+            g = h // (Hq // Hkv)
+            ref = attend_rows(q[b, h, :n], k[b, g, :n], v[b, g, :n], torch.arange(n))
+            check_rows(o[b, h, :n], lse[b, h, :n], ref, f"b={b} h={h}")
+        assert (o[b, :, n:] == 7.0).all() and (lse[b, :, n:] == 7.0).all()
+    if token_major:
+        assert (room[:, :, 0] == 7.0).all() and (room[:, :, 1 + Hq:] == 7.0).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,lens", [(8, 2, 128, [200, 17, 1, 63]), (5, 1, 64, [90, 333]),
+                                           (8, 1, 128, [1400, 1100])])
+def test_packed_result_in_a_column_range(kvc, Hq, Hkv, D, lens):
+    """o is a column range of a wider buffer, with the heads' stride larger than D."""
+    T = sum(lens)
+    gen = _gen(T)
+    qkv = _randn(gen, T, Hq + 2 * Hkv, D)
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    room = torch.full((T + 2, Hq + 1, D + 8), 7.0, dtype=torch.float16, device="cuda")
+    o = room[1:T + 1, 1:, :D]
+    kvc.kvc_prompt_attend(q, k, v, o, cu_seqlens=_cu(lens))
+    assert device_status_clean(kvc)
+    t = 0
+    for n in lens:
+        for h in range(Hq):
+            g = h // (Hq // Hkv)
+            ref = attend_rows(q[t:t + n, h], k[t:t + n, g], v[t:t + n, g], torch.arange(n))
+            check_rows(o[t:t + n, h], None, ref, f"t={t} h={h}")
+        t += n
+    room[1:T + 1, 1:, :D] = 7.0
+    assert (room == 7.0).all()
+
+
+@pytest.mark.parametrize("D,splits", [(128, 1), (128, 4), (64, 1), (64, 5)])
+@pytest.mark.parametrize("m", [[3, 40], [300, 450]])
+def test_chunk_with_a_given_scale_and_strided_rows(kvc, D, splits, m):
+    """softmax_scale, q a column range and o one of a wider buffer."""
+    Hq, Hkv, C, n = 8, 2, 1024, [[900, 1024], [450, 777]]
+    gen = _gen(D + splits + m[0])
+    cache = kvc.SlotCache.empty(2, Hkv, C, D)
+    cache.K.copy_(_randn(gen, 2, Hkv, C, D) * 2)
+    cache.V.copy_(_randn(gen, 2, Hkv, C, D))
+    cache.n.copy_(torch.tensor(n, dtype=torch.int32))
+    T = sum(m)
+    q = _randn(gen, T, Hq + 3, D)[:, 2:2 + Hq]
+    room = torch.full((T, Hq + 2, D + 16), 7.0, dtype=torch.float16, device="cuda")
+    o, lse = room[:, 1:1 + Hq, 8:8 + D], torch.full((Hq, T), 7.0, device="cuda")
+    ws = torch.empty(max(kvc.kvc_chunk_workspace_size(cache, q, splits) // 4, 4), device="cuda")
+    kvc.kvc_chunk_attend(cache, q, _cu(m), o, lse=lse, workspace=ws, num_splits=splits,
+                         softmax_scale=0.21)
+    assert device_status_clean(kvc)
+    for b, w in ((0, slice(0, m[0])), (1, slice(m[0], T))):
+        for h in range(Hq):
+            nn = n[b][h // 4]
+            ref = attend_rows(q[w, h], cache.K[b, h // 4, :nn], cache.V[b, h // 4, :nn],
+                              nn - m[b] + torch.arange(m[b]), 0.21)
+            check_rows(o[w, h], lse[h, w], ref, f"b={b} h={h}")
+    room[:, 1:1 + Hq, 8:8 + D] = 7.0
+    assert (room == 7.0).all()
