@@ -529,7 +529,8 @@ KVC_API kvc_status kvc_random_evict(const kvc_slot_cache *cache, int prompt_len,
  * packed lse is not of that form, and packed prompts have no such pass.
  * o overlaps neither q, k nor v.
  * A non-finite key or value row affects the rows that attend it and no others.
- * A sequence whose range leaves [0, L] counts as empty and sets KVC_DEV_CAPACITY.
+ * A sequence whose range leaves [0, L], or runs backwards, counts as empty and sets
+ * KVC_DEV_CAPACITY; where the others then overlap, their rows are unspecified.
  * No workspace.  Source: "Rethinking KV Cache Compression" guide, §16 "Prefill、decode、TP 的
  * 性能账" (the prefill computes the prompt's attention in one pass) and "局限与
  * 最终结论" (flash attention never materialises the probabilities).
@@ -572,7 +573,8 @@ KVC_API kvc_status kvc_prompt_attend(const kvc_prompt_args *args, cudaStream_t s
  *            computed apart and merged
  * A row that sees no slot gives o = 0 and lse = -inf.  A unit whose n leaves [0, C]
  * counts as empty and sets KVC_DEV_CAPACITY; so does a sequence whose range leaves
- * [0, T]; slots of a page outside the pool read as zeros and set it too.
+ * [0, T] or runs backwards (where the others then overlap, their rows are unspecified);
+ * slots of a page outside the pool read as zeros and set it too.
  * Rows of the cache behind n may hold anything.
  * No heavy-hitter scores are kept up: the call returns no probabilities and takes no
  * scores, and kvc_h2o_accumulate takes single decode rows or whole padded prompts.  So in
