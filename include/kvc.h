@@ -569,8 +569,10 @@ KVC_API kvc_status kvc_prompt_attend(const kvc_prompt_args *args, cudaStream_t s
  *            tokens may need more than many: a batch that fills the GPU by itself is not
  *            split.  A workspace kept for calls of different T is as large as the
  *            largest of their sizes, not as that of the largest T
- *   num_splits  0: chosen from the sizes; otherwise ranges per unit that are
- *            computed apart and merged
+ *   num_splits  0: chosen from the sizes, with C for the slots that a unit holds;
+ *            otherwise ranges per unit that are computed apart and merged.  Every unit
+ *            gets as many, so a batch with a few sequences far longer than the others
+ *            may be faster with a number given
  * A row that sees no slot gives o = 0 and lse = -inf.  A unit whose n leaves [0, C]
  * counts as empty and sets KVC_DEV_CAPACITY; so does a sequence whose range leaves
  * [0, T] or runs backwards (where the others then overlap, their rows are unspecified);

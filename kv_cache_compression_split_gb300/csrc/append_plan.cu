@@ -8,19 +8,20 @@
 // returned pages go on what is left of the stack, placed by the same sum of back.
 // Integer work of a few bytes per unit and token: latency bound.  One thread-block
 // cluster scans the units, since the sums run over all of them: every CTA its range, the
-// totals through distributed shared memory.  All that is read of the old state is read
-// before the cluster barrier, so the outputs may be the inputs, and a second barrier is
-// needed only where returned pages go on the stack that others still take from.  What
-// has many words is dealt evenly over threads that find their unit by bisecting the sums.
-// 512 sequences of 8 heads, one new token each: 10.6 us, of which an empty batch takes 7
-// (the cluster's start, one round of loads, the barrier) and the copy of the 0.5 MB table
-// and the 0.5 MB stack to other arrays most of the rest; 96 ragged prompts, 33 K tokens:
-// 12.3 us (a kernel on all SMs writes their slot map).
+// totals through distributed shared memory.  The outputs may be the inputs: of the old state
+// only the stack's taken pages and the table's returned entries are read after the cluster
+// barrier, the latter by the thread that then writes them, and a second barrier lies between
+// the taking and the returned pages that go on the same stack.  What has many words is dealt
+// evenly over threads that find their unit by bisecting the sums.
+// 512 sequences of 8 heads, one new token each: 10.4 to 10.7 us in a graph, of which an empty
+// batch takes 7 (the cluster's start, one round of loads, the barrier) and the copy of the
+// 0.5 MB table and the 0.5 MB stack to other arrays, by these eight SMs, most of the rest; 96
+// ragged prompts, 33 K tokens: 12.3 to 12.9 us (a kernel on all SMs writes their slot map).
 //
 // kvc_append_packed: one 16-byte chunk of a K and of a V row per thread and step,
 // written to the row that the slot map names.  HBM bound: 2 D bytes read and
-// written per row, twice.  35 K tokens of 8 heads of 128: 291 MB in 46.5 us, 6.2 TB/s,
-// 0.92 of the measured copy rate.
+// written per row, twice.  35 K tokens of 8 heads of 128: 291 MB in 46.5 us in a graph,
+// 6.2 TB/s, 0.92 of the measured copy rate, and 48.5 us by single calls, 0.88.
 #include "kvc_device.cuh"
 #include "kvc_internal.h"
 
@@ -172,8 +173,8 @@ __global__ void __launch_bounds__(THREADS) k_append_plan(const PlanLaunch p)
     const bool paged = p.table != nullptr;
     asm volatile("griddepcontrol.launch_dependents;");
 
-    // ---- everything of the old state that is read: it may be replaced after the cluster
-    // barrier below
+    // ---- the old counts, lengths and held pages, all of them: they may be replaced after the
+    // cluster barrier below
     const int given = paged ? *p.count : 0, count = min(max(given, 0), p.num_pages);
     if (given != count && gtid == 0)
         flag_error(p.status, DEV_CAPACITY);

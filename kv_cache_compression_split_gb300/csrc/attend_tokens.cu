@@ -44,14 +44,18 @@
 //
 // What bounds it.  Per 128 x 128 block of D = 128 the two products take 1070 clocks of the
 // tensor pipe (a 128 x 128 x 16 product was measured at 64.5 to 67 clocks), the
-// exponentials 520 of the SFU.  The two-tile form spends 1245 clocks a block once it runs:
-// a row's thread needs 1300 for its block (reading 30, maximum 300, exponentials and
+// exponentials 520 of the SFU.  The two-tile form spends 1250 to 1310 clocks a block once it
+// runs: a row's thread needs 1300 for its block (reading 30, maximum 300, exponentials and
 // packing 800, storing 35) while the tensor cores do the other tile's.  8192 tokens of
-// 64 / 8 heads: 650 to 690 us, 1600 to 1690 TFLOP/s, under the power cap (about 1.5 GHz):
-// 0.85 to 0.9 of the measured burst rate, 0.94 to 1.0 of the sustained one.  Shorter prompts
-// pay about 3000 clocks per item between its last product and the next one's.  A batch of few
-// tokens over long caches is HBM bound in the middle (64 KB per SM in 2700 clocks) and spends
-// the rest on the start, the last round and the merge: 131 MB in 30 us.
+// 64 / 8 heads: 654 to 729 us over GPUs and clocks, 1510 to 1680 TFLOP/s, 0.80 to 0.89 of the
+// measured burst rate and 0.89 to 0.99 of the sustained one; back to back under the power cap
+// 724 us at 1.64 GHz.  Shorter prompts pay about 3000 clocks per item between its last product
+// and the next one's: one MMA warp serves both tiles in order, so both end and are stored
+// together.  A batch of few tokens over long caches is HBM bound in the middle (64 KB per SM
+// in 2700 clocks) and spends the rest on the start, the last round and the merge: 131 MB in
+// 30 us in a graph, 33 us by single calls.  Heads of 64 channels: a block's products take half
+// as long and its row threads as long as before, whose chain of loads, maximum, exponentials
+// and stores bounds them: 2 x 8192 tokens of 16 heads 279 us, 985 TFLOP/s.
 //
 // Non-finite values.  A masked score is replaced, not added to, so keys behind a
 // row's range never matter.  A masked value row would enter as 0 * v: rows behind the
@@ -1388,9 +1392,13 @@ cudaError_t attend_tokens_impl(TokensLaunch p, cudaStream_t s)
 // Form and splits of a chunk, by what a call takes in microseconds: a start, then each
 // round of CTAs its key blocks and an item's start and end, then the merge.  The numbers
 // are fitted to a sweep of forms and splits over 24 shapes (1 to 32 sequences, 1 to 600
-// tokens each, 512 to 32768 slots); the choice was within 4% of the best one of the sweep
-// on all of them but one (3 x 40 tokens over 3008 slots: 7%).  The slots that a unit holds
-// are known on the GPU alone: the capacity stands for them.
+// tokens each, 512 to 32768 slots).  Against 12 numbers of splits from 1 to 64 on two GPUs the
+// choice was within 1% of the best on all of them but one (3 x 40 tokens over 3008 slots: 9
+// and 10%).  A block's time does not depend on D: shapes of 64 channels are predicted a
+// quarter too slow, which changed no choice in the sweep.  The slots that a unit holds are
+// known on the GPU alone, so the capacity stands for them and every unit gets as many ranges:
+// 64 sequences of 4 tokens, one over 32000 slots and the others over 300 to 610 of 32768, are
+// not split and take 359 us, 88 us with num_splits = 8.
 TokensPlan plan_tokens(int T, int B, int Hq, int Hkv, int D, int C, int requested)
 {
     const int tpt = TM / (Hq / Hkv), sms = sm_count();
@@ -1431,7 +1439,7 @@ cudaError_t launch_attend_tokens(const TokensLaunch &p, cudaStream_t s)
     // of 128, one against two tiles, us: 16 x 512 tokens 27.4 / 29.2, 8 x 1024 40.1 / 41.6,
     // 8 x 2048 113 / 110, 4 x 4096 200 / 185, 2 x 8192 379 / 349, but 1 x 2048 29.7 / 32.9;
     // 16 / 16 heads: 35.9 / 37.9, 44.1 / 45.6, 118 / 114, 214 / 193, 404 / 364, but 1 x 2048
-    // 25.8 / 29.8.  Heads of 64 channels, whose time goes to the exponentials, were faster with
+    // 25.8 / 29.8.  Heads of 64 channels, whose time goes to the row threads, were faster with
     // one tile throughout (2 x 8192: 276 / 298).  A chunk's form comes with its plan.
     const long seqs = p.cu ? p.B : 1, pair = 2 * (TM / (p.Hq / p.Hkv));
     const bool few = (p.L / pair + seqs) * p.Hkv * (p.cu ? 1 : p.B) <= sm_count();
