@@ -259,7 +259,8 @@ __device__ __forceinline__ bool mbar_sleep_or_abort(uint64_t *bar, uint32_t pari
 // The same two waits for a CTA in which warps may be at work that takes long but ends by
 // itself: they call still_active meanwhile, and a wait gives up when the last call lies past the
 // limit too.  Times are the clock's low words.  Their differences come round every 4.29 s; both
-// are past the limit of 2 s in more than half of that, so in a part of every round at once.
+// are past the limit of 2 s in more than half of that, so in a part of every round at once:
+// such a wait ends within 4.3 s of its own work's or the others' standstill.
 __device__ __forceinline__ uint32_t globaltimer_lo()
 {
     uint32_t t;
