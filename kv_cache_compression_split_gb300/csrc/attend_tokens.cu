@@ -47,8 +47,8 @@
 // exponentials 520 of the SFU.  The two-tile form spends 1250 to 1310 clocks a block once it
 // runs: a row's thread needs 1300 for its block (reading 30, maximum 300, exponentials and
 // packing 800, storing 35) while the tensor cores do the other tile's.  8192 tokens of
-// 64 / 8 heads: 654 to 729 us over GPUs and clocks, 1510 to 1680 TFLOP/s, 0.80 to 0.89 of the
-// measured burst rate and 0.89 to 0.99 of the sustained one; back to back under the power cap
+// 64 / 8 heads: 654 to 737 us over GPUs and clocks, 1490 to 1680 TFLOP/s, 0.79 to 0.89 of the
+// measured burst rate and 0.88 to 0.99 of the sustained one; back to back under the power cap
 // 724 us at 1.64 GHz.  Shorter prompts pay about 3000 clocks per item between its last product
 // and the next one's: one MMA warp serves both tiles in order, so both end and are stored
 // together.  A batch of few tokens over long caches is HBM bound in the middle (64 KB per SM
