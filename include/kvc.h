@@ -15,6 +15,10 @@
  *   - ragged appends: page tables, slot map and lengths of a batch whose
  *     sequences bring different numbers of tokens, and the rows themselves
  *                                             -- kvc_append_plan, kvc_append_packed
+ *   - trees of drafted tokens: their masks and positions, their attention over the slot
+ *     cache, which of them the target accepts, and the cache back on the accepted path
+ *                                             -- kvc_tree_plan, kvc_tree_attend,
+ *                                                kvc_draft_verify, kvc_draft_commit
  *   - StreamingLLM sink + recent window       -- kvc_stream_evict, kvc_stream_append
  *   - per-head uniform random eviction with the prompt locked
  *                                             -- kvc_random_evict
@@ -671,6 +675,142 @@ KVC_API kvc_status kvc_append_packed(const kvc_slot_cache *cache, const uint16_t
                                      const int64_t k_stride[2], const uint16_t *v_new,
                                      const int64_t v_stride[2], int T, const int32_t *slot_map,
                                      cudaStream_t stream);
+
+/*
+ * Trees of drafted tokens.  A step of speculative decoding takes several continuations of a
+ * sequence through the model at once and keeps the one that the model's own probabilities
+ * accept.  Sequence b brings m_b = cu_new[b+1] - cu_new[b] nodes, packed like the new tokens
+ * of kvc_append_plan; its node i is token cu_new[b] + i.  Node 0 is the last token that is
+ * certain and is not in the cache yet; the others are drafts.  parent[i] < i is the node that
+ * node i continues, -1 for a node that continues the cache itself (node 0).  A step is
+ *   kvc_tree_plan -> kvc_append_plan + kvc_append_packed (or kvc_append) ->
+ *   kvc_tree_attend, in every layer -> kvc_draft_verify -> kvc_draft_commit, in every layer
+ * and the next step's node 0 is the token that kvc_draft_verify drew.  A chain of drafts is
+ * the tree with parent[i] = i - 1; its attention is kvc_chunk_attend too.
+ * The pages describe no speculative decoding; the four calls are an extension of this library
+ * beside kvc_chunk_attend.  Their definition: the acceptance rule of speculative sampling (Leviathan,
+ * Kalman, Matias, "Fast Inference from Transformers via Speculative Decoding", ICML 2023),
+ * applied to one sibling after the other on what the refused ones leave.
+ */
+#define KVC_TREE_MAX_NODES 256
+#define KVC_DRAFT_MAX_VOCAB (1 << 24)
+
+/*
+ * kvc_tree_plan -- masks and positions of the nodes.
+ *   parent  [T] int32
+ *   words   64-bit words per mask, 1 .. KVC_TREE_MAX_NODES / 64
+ *   mask    [T, words]: bit j of token t's mask (word j / 64, bit j % 64) is set when node j of
+ *           its sequence is the token's own node or one of its ancestors
+ *   pos     optional [T] int32: the token's position, (seqlen ? seqlen[b] : 0) + the number of
+ *           its ancestors; with the seqlen [B] of the time before the append these are the
+ *           positions of rotary embeddings
+ * A parent that is neither -1 nor a node before the token's own counts as -1 and sets
+ * KVC_DEV_CAPACITY.  A sequence of more than 64 words nodes, and one whose range leaves [0, T]
+ * or runs backwards, sets it too, and its masks and positions are left as they were, like those
+ * of tokens outside every sequence.
+ */
+KVC_API kvc_status kvc_tree_plan(const int32_t *cu_new, int B, const int32_t *parent, int T,
+                                 const int32_t *seqlen, int words, uint64_t *mask, int32_t *pos,
+                                 cudaStream_t stream);
+
+/*
+ * kvc_tree_attend -- kvc_chunk_attend for nodes that see their ancestors only.  The nodes' K/V
+ * rows are in the last m_b of each unit's n slots, node j in slot n - m_b + j.  Node i attends
+ * every slot before these, and of the nodes j <= i those whose bit j is set in its mask (words
+ * 64-bit words, as kvc_tree_plan writes them; any other masks may be given: bits above i are
+ * not looked at, and a node need not see itself).  A row that sees no slot gives o = 0 and
+ * lse = -inf.  A sequence of more than 64 words nodes counts as empty (its rows of o and lse are
+ * left as they were) and sets KVC_DEV_CAPACITY.  Everything else is as in kvc_chunk_attend: the
+ * arguments in `chunk`, the workspace (kvc_tree_workspace_size(args)) and its sharing, what
+ * becomes of bad counts, ranges and pages and of units that an append refused.  Non-finite keys
+ * and values affect the rows that attend them and no others.
+ */
+typedef struct kvc_tree_args {
+    kvc_chunk_args chunk;
+    const uint64_t *mask; /* [T, words] */
+    int words;            /* 1 .. KVC_TREE_MAX_NODES / 64 */
+} kvc_tree_args;
+
+KVC_API size_t kvc_tree_workspace_size(const kvc_tree_args *args);
+KVC_API kvc_status kvc_tree_attend(const kvc_tree_args *args, cudaStream_t stream);
+
+/*
+ * kvc_draft_verify -- which nodes are accepted, and the token behind them.  p [T, V] holds the
+ * target's probabilities of the token behind each node.  The walk starts at node 0.  At node c
+ * it takes c's children in their order; child j with the token x = tokens[j] is accepted when
+ *   u[j] q(x) S < p(x) - a q(x),  with a = 0 and S = 1 at first        (q given)
+ *   u[j] S < p(x),                with S = 1 at first                  (q NULL)
+ * where p(x), q(x) are entries of row c, and then the walk goes on at j.  A child that is
+ * refused changes what is left for the next one:
+ *   q given  siblings were drawn from row c of q [T, V], each by itself: a grows by S, then
+ *            S = sum over the vocabulary of max(p - a q, 0).  That is the residual
+ *            max(r - q, 0) of the normalised r, one sibling after the other.
+ *   q NULL   siblings are given tokens (the draft's most likely ones): the weight of x becomes
+ *            0 and S falls by it.
+ * When no child is left, or max_path nodes are accepted, the next token is drawn from the
+ * weights of that node (max(p - a q, 0), or p without the refused tokens; p itself where
+ * nothing of it is left): the first token at which their running sum exceeds u_next[b] times
+ * their sum.  So the tokens along the path and the next token are distributed as the target's own
+ * samples.  u and u_next are uniform in [0, 1).
+ *   parent      [T] int32, or NULL: every sequence is a chain
+ *   tokens      [T] int32; a token outside [0, V) is refused (with weight 0)
+ *   p, q        rows of V adjacent fp32 entries; p_stride, q_stride elements between rows, at
+ *               least V.  Any 4-byte aligned address.  Entries that are NaN or negative count as
+ *               0, entries above 1 as 1; rows need to sum to 1 within rounding (of a row that
+ *               does not, the token drawn is unspecified, but a token of positive weight)
+ *   u           [T] fp32 (a node that starts the walk needs none), u_next [B] fp32
+ *   path        [B, max_path] int32: the accepted nodes, node 0 first, then -1
+ *   count       [B] int32: how many (0 for a sequence without nodes)
+ *   next_token  [B] int32; -1 for a sequence without nodes, and where p is 0 throughout
+ * Sums are 64-bit fixed-point numbers of 2^-52 over entries held exactly, so that the border
+ * between two tokens is where 64-bit arithmetic has it and the same inputs always give the same
+ * tokens.  A parent that is neither -1 nor an earlier node sets KVC_DEV_CAPACITY and counts as
+ * -1 (its node is then nobody's child); a sequence of more than KVC_TREE_MAX_NODES nodes, or
+ * whose range leaves [0, T] or runs backwards, counts as one without nodes and sets it too.
+ * V is at most KVC_DRAFT_MAX_VOCAB.  One launch, no workspace.
+ */
+typedef struct kvc_draft_args {
+    int B, T, V;
+    const int32_t *cu_new;
+    const int32_t *parent;
+    const int32_t *tokens;
+    const float *p;
+    const float *q;
+    const float *u;
+    const float *u_next;
+    int64_t p_stride, q_stride;
+    int32_t *path;
+    int32_t *count;
+    int32_t *next_token;
+    int max_path;
+} kvc_draft_args;
+
+KVC_API kvc_status kvc_draft_verify(const kvc_draft_args *args, cudaStream_t stream);
+
+/*
+ * kvc_draft_commit -- the slots of the accepted path stay.  In each unit the rows of the nodes
+ * path[b][0 .. count[b]) (increasing node numbers, as kvc_draft_verify gives them) move from
+ * the slots n - m_b + path[b][i] to n - m_b + i, and then n -= m_b - count[b], seqlen -= m_b -
+ * count[b].  The slots' positions stay as the append wrote them: slot n - m_b + i has the
+ * position of the node that lies there now.  Pages that a paged unit no longer fills stay its
+ * own until a kvc_append_plan with release; scores of kvc_h2o_evict are not touched (nodes have
+ * the score 0, kvc_tree_attend adds nothing to it).
+ *   path      [B, max_path] int32, count [B] int32
+ *   slot_map  optional [T, Hkv] of the kvc_append_plan that brought the nodes: a unit whose
+ *             entry of node 0 is -1 was refused, does not hold the nodes and is left as it is.
+ *             Without it such a unit loses its newest slots instead
+ *   T         tokens in all; the bound of the ranges in cu_new
+ *   next      gives the arrays n and seqlen to write: the cache itself, or another one of the
+ *             same B and Hkv (then all counts are written); K and V rows move in place
+ * A sequence whose range leaves [0, T] or runs backwards, whose count leaves [0, min(m_b,
+ * max_path)] or whose path is not an increasing list of its nodes keeps its n and seqlen and
+ * sets KVC_DEV_CAPACITY; so does a unit whose n leaves [m_b, C].  A row on a page outside the
+ * pool is not moved and sets it.
+ */
+KVC_API kvc_status kvc_draft_commit(const kvc_slot_cache *cache, const int32_t *cu_new, int T,
+                                    const int32_t *path, const int32_t *count, int max_path,
+                                    const int32_t *slot_map, const kvc_slot_cache *next,
+                                    cudaStream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 KVC_API const char *kvc_status_string(kvc_status status);

@@ -32,6 +32,8 @@ PAGE_SLOTS = 64            # KVC_PAGE_SLOTS: slots per page of the paged layout
 KIVI_PAGE_GROUPS = 4       # KVC_KIVI_PAGE_GROUPS: 32-token groups per KIVI page
 H2O_ONCHIP_MAX_SLOTS = 1024   # KVC_H2O_ONCHIP_MAX_SLOTS: fused H2O with logits kept on chip
 PLAN_MAX_UNITS = 65536     # KVC_PLAN_MAX_UNITS: units of one kvc_append_plan
+TREE_MAX_NODES = 256       # KVC_TREE_MAX_NODES: nodes of one sequence's tree
+DRAFT_MAX_VOCAB = 1 << 24  # KVC_DRAFT_MAX_VOCAB: tokens of the vocabulary
 KVC_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
 
@@ -92,6 +94,18 @@ class ChunkArgs(C.Structure):
                 ("num_splits", C.c_int), ("softmax_scale", C.c_float)]
 
 
+class TreeArgs(C.Structure):
+    _fields_ = [("chunk", ChunkArgs), ("mask", C.c_void_p), ("words", C.c_int)]
+
+
+class DraftArgs(C.Structure):
+    _fields_ = [("B", C.c_int), ("T", C.c_int), ("V", C.c_int), ("cu_new", C.c_void_p),
+                ("parent", C.c_void_p), ("tokens", C.c_void_p), ("p", C.c_void_p),
+                ("q", C.c_void_p), ("u", C.c_void_p), ("u_next", C.c_void_p),
+                ("p_stride", C.c_int64), ("q_stride", C.c_int64), ("path", C.c_void_p),
+                ("count", C.c_void_p), ("next_token", C.c_void_p), ("max_path", C.c_int)]
+
+
 class PagePoolDesc(C.Structure):
     _fields_ = [("pages", C.c_void_p), ("free_list", C.c_void_p), ("count", C.c_void_p)]
 
@@ -131,6 +145,11 @@ def lib():
                 "kvc_chunk_attend": (st, [P, P]),
                 "kvc_append_plan": (st, [P, P, P, i, i, P, P, P, P]),
                 "kvc_append_packed": (st, [P, P, P, P, P, i, P, P]),
+                "kvc_tree_plan": (st, [P, i, P, i, P, i, P, P, P]),
+                "kvc_tree_workspace_size": (C.c_size_t, [P]),
+                "kvc_tree_attend": (st, [P, P]),
+                "kvc_draft_verify": (st, [P, P]),
+                "kvc_draft_commit": (st, [P, P, i, P, P, i, P, P, P]),
                 "kvc_status_string": (C.c_char_p, [i]),
                 "kvc_read_device_status": (st, [C.POINTER(C.c_int), P]),
             }
@@ -199,7 +218,7 @@ def _state_without_desc(obj):
 
 
 
-_F16, _F32, _I32 = torch.float16, torch.float32, torch.int32
+_F16, _F32, _I32, _I64 = torch.float16, torch.float32, torch.int32, torch.int64
 
 
 class _Refused(Exception):
@@ -259,9 +278,11 @@ def _wrong_device(t, dev):
 
 
 # The argument structs packed field by field in one call (a ctypes assignment per field took
-# longer than the launch); the field order is that of PromptArgs and ChunkArgs.
+# longer than the launch); the field order is that of PromptArgs, ChunkArgs, TreeArgs and DraftArgs.
 _pack_prompt = struct.Struct("@5i4x7P12qf4x").pack
 _pack_chunk = struct.Struct("@2i5P4qPNif").pack
+_pack_tree = struct.Struct("@2i5P4qPNifPi4x").pack
+_pack_draft = struct.Struct("@3i4x7P2q3Pi4x").pack
 _pack_2q = struct.Struct("@2q").pack
 _pack_3p = struct.Struct("@3P").pack
 
@@ -579,6 +600,109 @@ def kvc_append_packed(cache: "SlotCache", k_new, v_new, slot_map, stream=None):
     _check((_lib or lib()).kvc_append_packed(
         C.addressof(d), kp, _pack_2q(k0, k1), vp, _pack_2q(v0, v1), T,
         _typed(slot_map, "slot_map", _I32, (T, H), dev), stream), "kvc_append_packed")
+
+
+def kvc_tree_plan(cu_new, parent, mask, pos=None, seqlen=None, stream=None):
+    """Masks and positions of trees of drafted tokens (see kvc.h): parent [T] int32 by node of
+    the sequence (-1: the first), mask [T, words] int64 (64 nodes per word), pos [T] int32 =
+    seqlen[b] (0 without) + the node's depth."""
+    dev, stream = _device(stream)
+    T, words = mask.shape
+    B = cu_new.numel() - 1
+    up = _typed(parent, "parent", _I32, (T,), dev)
+    _check((_lib or lib()).kvc_tree_plan(
+        _typed(cu_new, "cu_new", _I32, (B + 1,), dev), B, up, T,
+        _typed(seqlen, "seqlen", _I32, (B,), dev), words,
+        _typed(mask, "mask", _I64, (T, words), dev), _typed(pos, "pos", _I32, (T,), dev), stream),
+        "kvc_tree_plan")
+
+
+def kvc_tree_workspace_size(cache: "SlotCache", q, num_splits: int = 0) -> int:
+    """Bytes of workspace for kvc_tree_attend: those of kvc_chunk_workspace_size."""
+    cache.desc()
+    args = _pack_tree(q.shape[1], q.shape[0], C.addressof(cache.__dict__["_desc"]), 0, 0, 0, 0, 0,
+                      0, 0, 0, 0, 0, num_splits, 0.0, 0, 1)
+    return int((_lib or lib()).kvc_tree_workspace_size(args))
+
+
+def kvc_tree_attend(cache: "SlotCache", q, cu_new, mask, o, lse=None, workspace=None,
+                    num_splits: int = 0, softmax_scale: float = 0.0, stream=None):
+    """kvc_chunk_attend for the nodes of trees: of the new tokens each node sees those of its
+    mask [T, words] int64 (kvc_tree_plan writes it), and every older slot (see kvc.h)."""
+    dev, stream = _device(stream)
+    d = cache.desc(dev)
+    shape = q.shape
+    T, Hq, D = shape
+    if D != d.D:
+        raise ValueError(f"kvc_tree_attend: q must be [T, Hq, {d.D}], got {tuple(shape)}")
+    try:
+        qp, (q2, q1, _) = _rows(q, shape, dev)
+        op, (o2, o1, _) = _rows(o, shape, dev)
+    except _Refused:
+        _explain((("q", q, shape), ("o", o, shape)), dev, ("cu_new", cu_new, (d.B + 1,)))
+    ws = size = 0
+    if workspace is not None:
+        ws, size = _ptr(workspace), workspace.nbytes
+    words = mask.shape[-1]
+    args = _pack_tree(Hq, T, C.addressof(d), qp, op,
+                      _typed(cu_new, "cu_new", _I32, (d.B + 1,), dev),
+                      0 if lse is None else _typed(lse, "lse", _F32, (Hq, T), dev), q1, q2, o1, o2,
+                      ws, size, num_splits, softmax_scale,
+                      _typed(mask, "mask", _I64, (T, words), dev), words)
+    _check((_lib or lib()).kvc_tree_attend(args, stream), "kvc_tree_attend")
+
+
+def _prob_rows(t, what, T, V, dev):
+    """Address and stride of fp32 rows [T, V] of adjacent entries."""
+    if t.dtype is not _F32 or t.shape != (T, V):
+        _typed(t, what, _F32, (T, V), dev)
+    if t.get_device() != dev:
+        _wrong_device(t, dev)
+    s0, s1 = t.stride()
+    if s1 != 1 and V > 1:
+        raise ValueError(f"kvc: the last dimension of {what} must be contiguous")
+    return t.data_ptr(), s0 if T > 1 else V
+
+
+def kvc_draft_verify(cu_new, tokens, p, u, u_next, path, count, next_token, parent=None, q=None,
+                     stream=None):
+    """Which drafted nodes the target accepts, and the token behind them (see kvc.h): p [T, V]
+    fp32 the target's probabilities behind each node, q [T, V] the draft's where siblings were
+    drawn from it, tokens [T] and parent [T] int32 (None: chains), u [T] and u_next [B] fp32 in
+    [0, 1).  Writes path [B, P] int32 (accepted nodes, then -1), count [B] and next_token [B]."""
+    dev, stream = _device(stream)
+    T, V = p.shape
+    B, P = path.shape
+    qp = qs = 0
+    if q is not None:
+        qp, qs = _prob_rows(q, "q", T, V, dev)
+    pp, ps = _prob_rows(p, "p", T, V, dev)
+    args = _pack_draft(B, T, V, _typed(cu_new, "cu_new", _I32, (B + 1,), dev),
+                       0 if parent is None else _typed(parent, "parent", _I32, (T,), dev),
+                       _typed(tokens, "tokens", _I32, (T,), dev), pp, qp,
+                       _typed(u, "u", _F32, (T,), dev), _typed(u_next, "u_next", _F32, (B,), dev),
+                       ps, qs, _typed(path, "path", _I32, (B, P), dev),
+                       _typed(count, "count", _I32, (B,), dev),
+                       _typed(next_token, "next_token", _I32, (B,), dev), P)
+    _check((_lib or lib()).kvc_draft_verify(args, stream), "kvc_draft_verify")
+
+
+def kvc_draft_commit(cache: "SlotCache", cu_new, path, count, slot_map=None,
+                     out: "Optional[SlotCache]" = None, stream=None):
+    """The slots of the accepted nodes (path [B, P], count [B] int32, as kvc_draft_verify writes
+    them) stay, those of the sequence's other nodes are given back; n and seqlen fall (those of
+    `out` are written; default: the cache's own).  With the slot_map [T, Hkv] of the append, units
+    that it refused stay as they are."""
+    dev, stream = _device(stream)
+    d = cache.desc(dev)
+    n = out.desc(dev) if out is not None else d
+    B, P = path.shape
+    T = 2**31 - 1 if slot_map is None else slot_map.shape[0]
+    sm = 0 if slot_map is None else _typed(slot_map, "slot_map", _I32, (T, d.Hkv), dev)
+    _check((_lib or lib()).kvc_draft_commit(
+        C.addressof(d), _typed(cu_new, "cu_new", _I32, (d.B + 1,), dev), T,
+        _typed(path, "path", _I32, (d.B, P), dev), _typed(count, "count", _I32, (d.B,), dev), P,
+        sm, C.addressof(n), stream), "kvc_draft_commit")
 
 
 def kvc_read_device_status(stream=None) -> int:

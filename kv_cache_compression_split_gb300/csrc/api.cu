@@ -767,7 +767,9 @@ size_t kvc_chunk_workspace_size(const kvc_chunk_args *a)
     return chunk_bytes(a, chunk_plan(a).splits);
 }
 
-kvc_status kvc_chunk_attend(const kvc_chunk_args *a, cudaStream_t stream)
+// A chunk over the slot cache, or with masks the nodes of trees.
+static kvc_status chunk_attend(const kvc_chunk_args *a, const uint64_t *mask, int words,
+                               cudaStream_t stream)
 {
     const kvc_status st = check_chunk(a);
     if (st != KVC_OK)
@@ -811,8 +813,111 @@ kvc_status kvc_chunk_attend(const kvc_chunk_args *a, cudaStream_t stream)
     p.block_table = c.block_table;
     p.num_pages = c.num_pages;
     p.scale_log2 = (a->softmax_scale > 0.f ? a->softmax_scale : 1.0f / sqrtf((float)c.D)) * LOG2E;
+    p.mask = mask;
+    p.words = words;
     p.status = dev_status_ptr();
     return from_cuda(launch_attend_tokens(p, stream));
+}
+
+kvc_status kvc_chunk_attend(const kvc_chunk_args *a, cudaStream_t stream)
+{
+    return chunk_attend(a, nullptr, 0, stream);
+}
+
+static bool tree_words_ok(int words) { return words >= 1 && words <= KVC_TREE_MAX_NODES / 64; }
+
+size_t kvc_tree_workspace_size(const kvc_tree_args *a)
+{
+    return a ? kvc_chunk_workspace_size(&a->chunk) : 0;
+}
+
+kvc_status kvc_tree_attend(const kvc_tree_args *a, cudaStream_t stream)
+{
+    if (!a || !tree_words_ok(a->words) || a->chunk.T < 0 ||
+        (a->chunk.T > 0 && (!a->mask || reinterpret_cast<uintptr_t>(a->mask) % 8)))
+        return KVC_ERR_INVALID_ARG;
+    return chunk_attend(&a->chunk, a->mask, a->words, stream);
+}
+
+kvc_status kvc_tree_plan(const int32_t *cu_new, int B, const int32_t *parent, int T,
+                         const int32_t *seqlen, int words, uint64_t *mask, int32_t *pos,
+                         cudaStream_t stream)
+{
+    if (B <= 0 || T < 0 || !tree_words_ok(words))
+        return KVC_ERR_INVALID_ARG;
+    if (T == 0)
+        return KVC_OK;
+    if (!cu_new || !parent || !mask || reinterpret_cast<uintptr_t>(mask) % 8)
+        return KVC_ERR_INVALID_ARG;
+    const TreePlanLaunch p{B, T, words, cu_new, parent, seqlen, mask, pos, dev_status_ptr()};
+    return from_cuda(launch_tree_plan(p, stream));
+}
+
+kvc_status kvc_draft_verify(const kvc_draft_args *a, cudaStream_t stream)
+{
+    if (!a || a->B <= 0 || a->T < 0 || a->V <= 0 || a->max_path <= 0 || !a->cu_new || !a->path ||
+        !a->count || !a->next_token)
+        return KVC_ERR_INVALID_ARG;
+    if (a->T > 0 && (!a->tokens || !a->p || !a->u || !a->u_next || reinterpret_cast<uintptr_t>(a->p) % 4 || reinterpret_cast<uintptr_t>(a->q) % 4 ||
+                     a->p_stride < a->V || (a->q && a->q_stride < a->V)))
+        return KVC_ERR_INVALID_ARG;
+    if (a->V > KVC_DRAFT_MAX_VOCAB || a->B > INT_MAX / 16)
+        return KVC_ERR_UNSUPPORTED;
+    VerifyLaunch p{};
+    p.B = a->B;
+    p.T = a->T;
+    p.V = a->V;
+    p.cu = a->cu_new;
+    p.parent = a->parent;
+    p.tokens = a->tokens;
+    p.p = a->p;
+    p.q = a->q;
+    p.u = a->u;
+    p.u_next = a->u_next;
+    p.ps = a->p_stride;
+    p.qs = a->q_stride;
+    p.path = a->path;
+    p.count = a->count;
+    p.next_token = a->next_token;
+    p.max_path = a->max_path;
+    p.status = dev_status_ptr();
+    return from_cuda(launch_draft_verify(p, stream));
+}
+
+kvc_status kvc_draft_commit(const kvc_slot_cache *cache, const int32_t *cu_new, int T,
+                            const int32_t *path, const int32_t *count, int max_path,
+                            const int32_t *slot_map, const kvc_slot_cache *next,
+                            cudaStream_t stream)
+{
+    const kvc_status st = check_slot_cache(cache);
+    if (st != KVC_OK)
+        return st;
+    if (T < 0 || max_path <= 0 || !cu_new || !path || !count || !next || !next->n ||
+        !next->seqlen || next->B != cache->B || next->Hkv != cache->Hkv)
+        return KVC_ERR_INVALID_ARG;
+    if ((long long)cache->B * cache->Hkv > (long long)INT_MAX)
+        return KVC_ERR_UNSUPPORTED;
+    CommitLaunch p{};
+    p.B = cache->B;
+    p.Hkv = cache->Hkv;
+    p.D = cache->D;
+    p.C = cache->C;
+    p.T = T;
+    p.max_path = max_path;
+    p.num_pages = cache->num_pages;
+    p.K = cache->K;
+    p.V = cache->V;
+    p.cu = cu_new;
+    p.path = path;
+    p.count = count;
+    p.slot_map = slot_map;
+    p.n = cache->n;
+    p.seqlen = cache->seqlen;
+    p.table = cache->block_table;
+    p.n_out = next->n;
+    p.seqlen_out = next->seqlen;
+    p.status = dev_status_ptr();
+    return from_cuda(launch_draft_commit(p, stream));
 }
 
 kvc_status kvc_append_plan(const kvc_slot_cache *cache, const kvc_page_pool *pool,

@@ -126,12 +126,13 @@ struct TokMaps {
 };
 
 // First token and length of sequence b; a range that leaves [0, L] counts as an
-// empty sequence and is reported.
+// empty sequence and is reported, and so does a tree of more nodes than its masks have bits.
+template <bool TREE>
 __device__ __forceinline__ void seq_range(const TokensLaunch &p, int b, int &start, int &len)
 {
     start = p.cu ? p.cu[b] : 0;
     len = p.cu ? p.cu[b + 1] - start : p.lens ? p.lens[b] : p.L;
-    if (start < 0 || start > p.L || len < 0 || len > p.L - start) {
+    if (start < 0 || start > p.L || len < 0 || len > p.L - start || (TREE && len > 64 * p.words)) {
         flag_error(p.status, DEV_CAPACITY);
         start = len = 0;
     }
@@ -144,7 +145,7 @@ struct ItemWalk {
     int b0 = 0;
     unsigned base = 0;   // items before it
     // tiles: per item; keys: per block
-    template <bool CHUNK>
+    template <bool CHUNK, bool TREE>
     __device__ bool find(const TokensLaunch &p, int tpt, int tiles, int keys, unsigned idx,
                          TokItem &it)
     {
@@ -158,7 +159,7 @@ struct ItemWalk {
         for (; b0 < p.B; b0 += 32) {
             int s = 0, n = 0;
             if (b0 + lane < p.B)
-                seq_range(p, b0 + lane, s, n);
+                seq_range<TREE>(p, b0 + lane, s, n);
             const unsigned ranges = (unsigned)(n + tiles * tpt - 1) / (unsigned)(tiles * tpt);
             unsigned sum = ranges * Hkv * splits;
             // ranges that overlap may add up to more than the grid: sums stop at the largest
@@ -243,6 +244,32 @@ __device__ __forceinline__ void mask64(float (&x)[64], int lim)
         x[c] = c <= lim ? x[c] : -INFINITY;
 }
 
+// Which of the 64 columns that begin with node `off` of its tree a row sees: all in front of
+// the tree (off may be negative), then its mask's, none behind column lim.
+__device__ __forceinline__ uint64_t tree_columns(const uint64_t *mask, int words, int off, int lim)
+{
+    if (lim < 0)
+        return 0;
+    uint64_t x = ~0ull;
+    if (off > -64) {
+        const int w = off >> 6, s = off & 63;
+        const uint64_t lo = w < 0 ? ~0ull : w < words ? mask[w] : 0;
+        const uint64_t hi = w + 1 < words ? mask[w + 1] : 0;
+        x = s ? lo >> s | hi << (64 - s) : lo;
+    }
+    return lim < 63 ? x & ((2ull << lim) - 1) : x;
+}
+
+__device__ __forceinline__ void mask64(float (&x)[64], uint64_t columns)
+{
+    const uint32_t lo = (uint32_t)columns, hi = (uint32_t)(columns >> 32);
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+        x[c] = lo >> c & 1 ? x[c] : -INFINITY;
+        x[32 + c] = hi >> c & 1 ? x[32 + c] : -INFINITY;
+    }
+}
+
 __device__ __forceinline__ float max64(const float (&x)[64])
 {
     float c0 = fmax3f(x[0], x[1], x[2]), c1 = fmax3f(x[16], x[17], x[18]);
@@ -319,11 +346,13 @@ template <int CH> struct Channels {
 // rows behind it a pass over the values, and only the rows of its own tile are computed again:
 // 200 003 tokens of 8 heads over one of 128 channels take 46 ms, 600 ms with a NaN in the last
 // tile and 480 ms with one in the first.
-template <int D, bool CHUNK>
+// In a tree, a row attends every key before it.shift and then those of its mask: the first are
+// looked through for all rows together, the others, few, for each row by itself.
+template <int D, bool CHUNK, bool TREE>
 __device__ __noinline__ void rows_again(const TokensLaunch &p, const TokItem &it, unsigned rows,
-                                        const uint16_t *q, int first, int end, int last, float ref,
-                                        float scale, uint16_t *o, float4 *part, long stride,
-                                        volatile uint32_t *active)
+                                        const uint16_t *q, int first, int end, int last,
+                                        const uint64_t *mask, float ref, float scale, uint16_t *o,
+                                        float4 *part, long stride, volatile uint32_t *active)
 {
     constexpr int CH = D / 32, U = 8, R = 2;
     constexpr unsigned ALL = 0xffffffffu;
@@ -341,14 +370,15 @@ __device__ __noinline__ void rows_again(const TokensLaunch &p, const TokItem &it
         nan_at[c] = pos_at[c] = neg_at[c] = NEVER;
         any_at[c] = -1;
     }
+    const int tree = TREE ? min(end, max(first, it.shift)) : end;   // the item's first node
 #pragma unroll 1
-    for (int j = first; j < end; j += 2 * U) {
+    for (int j = first; j < tree; j += 2 * U) {
         still_active(active);
         Vec x[2 * U];
         uint32_t odd = 0;
 #pragma unroll
         for (int u = 0; u < 2 * U; ++u) {
-            const uint16_t *v = j + u < end ? key_row<CHUNK>(p, p.v, p.vs, it, j + u) : nullptr;
+            const uint16_t *v = j + u < tree ? key_row<CHUNK>(p, p.v, p.vs, it, j + u) : nullptr;
             x[u] = Vec{};
             if (v)
                 x[u].load(v + c0);
@@ -371,8 +401,40 @@ __device__ __noinline__ void rows_again(const TokensLaunch &p, const TokItem &it
                     neg_at[c] = min(neg_at[c], nan || !neg ? NEVER : j + u);
                 }
     }
-    auto attended = [&](int c, int lim) {
-        return nan_at[c] <= lim || pos_at[c] <= lim || neg_at[c] <= lim;
+    auto sees = [&](int j, int lim, const uint64_t *row_mask) {
+        if (!TREE || j < it.shift)
+            return j <= lim;
+        return j <= lim && (row_mask[(j - it.shift) >> 6] >> (j - it.shift & 63) & 1);
+    };
+    // Per channel of this lane what the row of lane `src` meets: NaN, +inf and -inf that it
+    // attends, and any of them that it does not.
+    constexpr uint32_t HAS_NAN = 1, HAS_POS = 2, HAS_NEG = 4, ATTENDED = 7, BEHIND = 8;
+    auto meets = [&](int src, uint32_t (&st)[CH]) {
+        const int lim = __shfl_sync(ALL, last, src);
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            st[c] = (nan_at[c] <= lim ? HAS_NAN : 0) | (pos_at[c] <= lim ? HAS_POS : 0) |
+                    (neg_at[c] <= lim ? HAS_NEG : 0) | (any_at[c] > lim ? BEHIND : 0);
+        if constexpr (TREE) {
+            const uint64_t *row_mask = from(mask, src);
+            still_active(active);
+#pragma unroll 1
+            for (int j = tree; j < end; ++j) {
+                const uint16_t *v = key_row<CHUNK>(p, p.v, p.vs, it, j);
+                Vec x{};
+                if (v)
+                    x.load(v + c0);
+                if (!x.odd())
+                    continue;
+                const bool in = sees(j, lim, row_mask);
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const uint32_t h = x.bits(c);
+                    if ((h & 0x7c00u) == 0x7c00u)
+                        st[c] |= !in ? BEHIND : h & 0x3ffu ? HAS_NAN : h & 0x8000u ? HAS_NEG : HAS_POS;
+                }
+            }
+        }
     };
     auto store = [&](uint16_t *to, float4 *to4, int c, float x) {
         if (to4)
@@ -383,16 +445,18 @@ __device__ __noinline__ void rows_again(const TokensLaunch &p, const TokItem &it
     unsigned again = 0;
 #pragma unroll 1
     for (unsigned left = rows; left; left &= left - 1) {
-        const int src = __ffs(left) - 1, lim = __shfl_sync(ALL, last, src);
+        const int src = __ffs(left) - 1;
         uint16_t *to = from(o, src);
         float4 *to4 = from(part, src);
+        uint32_t st[CH];
+        meets(src, st);
         bool behind = false;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const bool neg = neg_at[c] <= lim, pos = pos_at[c] <= lim;
-            const bool nan = nan_at[c] <= lim || (neg && pos);
-            behind |= !attended(c, lim) && any_at[c] > lim;
-            if (attended(c, lim))
+            const bool neg = st[c] & HAS_NEG, pos = st[c] & HAS_POS;
+            const bool nan = (st[c] & HAS_NAN) || (neg && pos);
+            behind |= !(st[c] & ATTENDED) && (st[c] & BEHIND);
+            if (st[c] & ATTENDED)
                 store(to, to4, c, nan ? NAN : pos ? INFINITY : -INFINITY);
         }
         if (__any_sync(ALL, behind))
@@ -402,6 +466,7 @@ __device__ __noinline__ void rows_again(const TokensLaunch &p, const TokItem &it
     while (again) {
         int src[R], lim[R], most = -1;   // rows that there are not: the last one once more
         const uint16_t *qr[R];
+        const uint64_t *row_mask[R];
         float m[R], acc[R][CH];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -410,6 +475,7 @@ __device__ __noinline__ void rows_again(const TokensLaunch &p, const TokItem &it
             lim[r] = __shfl_sync(ALL, last, src[r]);
             m[r] = __shfl_sync(ALL, ref, src[r]);
             qr[r] = from(q, src[r]);
+            row_mask[r] = TREE ? from(mask, src[r]) : nullptr;
             most = max(most, lim[r]);
 #pragma unroll
             for (int c = 0; c < CH; ++c)
@@ -442,7 +508,7 @@ __device__ __noinline__ void rows_again(const TokensLaunch &p, const TokItem &it
                 }
 #pragma unroll
                 for (int r = 0; r < R; ++r)
-                    w[r] = j <= lim[r] ? ex2(w[r] * p.scale_log2 - m[r]) : 0.f;
+                    w[r] = sees(j, lim[r], row_mask[r]) ? ex2(w[r] * p.scale_log2 - m[r]) : 0.f;
             }
 #pragma unroll 1
             for (int i = 0; i < 32; i += U) {
@@ -474,16 +540,18 @@ __device__ __noinline__ void rows_again(const TokensLaunch &p, const TokItem &it
             const float f = __shfl_sync(ALL, scale, src[r]);
             uint16_t *to = from(o, src[r]);
             float4 *to4 = from(part, src[r]);
+            uint32_t st[CH];
+            meets(src[r], st);
 #pragma unroll
             for (int c = 0; c < CH; ++c)
-                if (!attended(c, lim[r]))
+                if (!(st[c] & ATTENDED))
                     store(to, to4, c, acc[r][c] * f);
         }
     }
     still_active(active);
 }
 
-template <int D, int TILES, bool CHUNK>
+template <int D, int TILES, bool CHUNK, bool TREE>
 __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS)
     k_attend_tokens(const __grid_constant__ TokMaps maps, const __grid_constant__ TokensLaunch p)
 {
@@ -595,7 +663,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                     clc_request(clc, clc_full);
                     asked = n_clc;
                 }
-                if (!walk.find<CHUNK>(p, tpt, TILES, TK, idx, it))
+                if (!walk.find<CHUNK, TREE>(p, tpt, TILES, TK, idx, it))
                     it.j0 = it.j1 = it.two = 0;   // the grid is an upper bound
             }
             if (idx < 0 || it.b >= 0) {
@@ -930,6 +998,12 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
             const bool idle = w_tok >= rg.ntok;                   // no row of the warp is real
             const bool full = 32 % g == 0 && w_tok + 32 / g <= rg.ntok;
             const int first_last = it.shift + rg.tok + w_tok;
+            // a row that is not real looks at no mask
+            const uint64_t *mask = nullptr;
+            if (TREE && real) {
+                mask = p.mask + (size_t)(it.start + rg.tok + r_tok) * p.words;
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(mask));
+            }
             float m = -INFINITY, l = 0.f;
             for (int i = 0; i < rg.count; ++i) {
                 const int k0 = (rg.j + i * rg.step) * TK;
@@ -949,15 +1023,24 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 tc_fence_after();
                 float lo[64], hi[TILES == 2 ? 64 : 1];
                 const int lim = last - k0;
-                const bool cut = k0 + TK - 1 > first_last;   // ends behind some row's range
+                // ends behind some row's range, or behind some row's first node
+                const bool cut = TREE ? k0 + TK > it.shift : k0 + TK - 1 > first_last;
                 tmem_ld64(s_col, lo);
-                if (cut)
-                    mask64(lo, lim);
+                if (cut) {
+                    if constexpr (TREE)
+                        mask64(lo, tree_columns(mask, p.words, k0 - it.shift, lim));
+                    else
+                        mask64(lo, lim);
+                }
                 float top = max64(lo);
                 if constexpr (TILES == 2) {
                     tmem_ld64(s_col + 64, hi);
-                    if (cut)
-                        mask64(hi, lim - 64);
+                    if (cut) {
+                        if constexpr (TREE)
+                            mask64(hi, tree_columns(mask, p.words, k0 + 64 - it.shift, lim - 64));
+                        else
+                            mask64(hi, lim - 64);
+                    }
                     top = fmaxf(top, max64(hi));
                 }
                 const float mx = scale * top;
@@ -1202,9 +1285,10 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                                     tok * p.qs[2];
                 const int end = max(0, it.shift + it.tok0 + it.ntok);   // keys of the item
                 const TokItem item = it;   // it stays in registers
-                rows_again<D, CHUNK>(p, item, __ballot_sync(0xffffffffu, again), q, it.j0 * TK,
-                                     min(end, it.j1 * TK), last, m == -INFINITY ? 0.f : m, inv,
-                                     o_row(), part ? part_o() : nullptr, rows, active);
+                rows_again<D, CHUNK, TREE>(p, item, __ballot_sync(0xffffffffu, again), q,
+                                           it.j0 * TK, min(end, it.j1 * TK), last, mask,
+                                           m == -INFINITY ? 0.f : m, inv, o_row(),
+                                           part ? part_o() : nullptr, rows, active);
             }
             tc_fence_before();
         }
@@ -1252,14 +1336,16 @@ __global__ void __launch_bounds__(128) k_combine_tokens(const TokensLaunch p, co
     bool real = false;
     if (lo < p.B && row < rows) {
         const int start = p.cu[lo], end = p.cu[lo + 1];
-        real = start >= 0 && start <= tok && end <= p.L;   // as the attention took it
+        // as the attention took it
+        real = start >= 0 && start <= tok && end <= p.L && (!p.words || end - start <= 64 * p.words);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!real && row < rows && *p.broken)
 #pragma unroll 1
         for (int b = 0; b < p.B && !real; ++b) {
             const int start = p.cu[b], end = p.cu[b + 1];
-            real = start >= 0 && start <= tok && tok < end && end <= p.L;
+            real = start >= 0 && start <= tok && tok < end && end <= p.L &&
+                   (!p.words || end - start <= 64 * p.words);
         }
     const long step = (long)p.Hkv * rows;   // entries of a split
     const float2 *ml = p.part_ml + split0 * step + (long)blockIdx.y * rows + row;
@@ -1324,7 +1410,7 @@ __global__ void __launch_bounds__(128) k_combine_tokens(const TokensLaunch p, co
         p.lse[head * p.ls[1] + tok] = l > 0.f ? (m + __log2f(l)) * LN2 : l == 0.f ? -INFINITY : l;
 }
 
-template <int D, int TILES, bool CHUNK>
+template <int D, int TILES, bool CHUNK, bool TREE = false>
 cudaError_t attend_tokens_impl(TokensLaunch p, cudaStream_t s)
 {
     using Cfg = TokCfg<D, TILES>;
@@ -1353,7 +1439,7 @@ cudaError_t attend_tokens_impl(TokensLaunch p, cudaStream_t s)
     if (!ok)
         return cudaErrorInvalidValue;
     cudaError_t e =
-        set_smem_once(reinterpret_cast<const void *>(k_attend_tokens<D, TILES, CHUNK>), Cfg::SMEM);
+        set_smem_once(reinterpret_cast<const void *>(k_attend_tokens<D, TILES, CHUNK, TREE>), Cfg::SMEM);
     if (e != cudaSuccess)
         return e;
     // packed: every sequence ends in at most one partial range
@@ -1363,7 +1449,7 @@ cudaError_t attend_tokens_impl(TokensLaunch p, cudaStream_t s)
     const long items = ranges * p.Hkv * p.splits;
     if (items > 0x7fffffffL)
         return cudaErrorInvalidValue;
-    k_attend_tokens<D, TILES, CHUNK><<<(unsigned)items, Cfg::NTHR, Cfg::SMEM, s>>>(maps, p);
+    k_attend_tokens<D, TILES, CHUNK, TREE><<<(unsigned)items, Cfg::NTHR, Cfg::SMEM, s>>>(maps, p);
     e = cudaGetLastError();
     if (!CHUNK || e != cudaSuccess || p.splits == 1)
         return e;
@@ -1444,6 +1530,10 @@ cudaError_t launch_attend_tokens(const TokensLaunch &p, cudaStream_t s)
     const long seqs = p.cu ? p.B : 1, pair = 2 * (TM / (p.Hq / p.Hkv));
     const bool few = (p.L / pair + seqs) * p.Hkv * (p.cu ? 1 : p.B) <= sm_count();
     const bool one = p.n ? p.tiles == 1 : p.L <= 1024 * seqs || few;
+    if (p.mask)
+        return p.D == 64 ? attend_tokens_impl<64, 1, true, true>(p, s)
+               : one     ? attend_tokens_impl<128, 1, true, true>(p, s)
+                         : attend_tokens_impl<128, 2, true, true>(p, s);
     if (p.n)
         return p.D == 64 ? attend_tokens_impl<64, 1, true>(p, s)
                : one     ? attend_tokens_impl<128, 1, true>(p, s)

@@ -132,6 +132,8 @@ struct TokensLaunch {
     float *part_o;             // [splits, Hkv, D / 4, L * g, 4]: sums of the values, fp32
     float2 *part_ml;           // [splits, Hkv, L * g]: reference and sum
     int *broken;               // whether some sequence's range is bad, for the merge
+    const uint64_t *mask;      // tree: [L, words] which nodes a node sees (nullptr: no tree)
+    int words;
     float scale_log2;
     int *status;
 };
@@ -153,6 +155,37 @@ struct PlanLaunch {
     int *status;
 };
 cudaError_t launch_append_plan(const PlanLaunch &p, cudaStream_t s);
+
+// Trees of drafted tokens: masks and positions, the walk over the accepted nodes, and the
+// cache back on their path.
+struct TreePlanLaunch {
+    int B, T, words;
+    const int32_t *cu, *parent, *seqlen;
+    uint64_t *mask;
+    int32_t *pos;
+    int *status;
+};
+cudaError_t launch_tree_plan(const TreePlanLaunch &p, cudaStream_t s);
+
+struct VerifyLaunch {
+    int B, T, V;
+    const int32_t *cu, *parent, *tokens;
+    const float *p, *q, *u, *u_next;
+    long ps, qs;
+    int32_t *path, *count, *next_token;
+    int max_path;
+    int *status;
+};
+cudaError_t launch_draft_verify(const VerifyLaunch &p, cudaStream_t s);
+
+struct CommitLaunch {
+    int B, Hkv, D, C, T, max_path, num_pages;
+    uint16_t *K, *V;
+    const int32_t *cu, *path, *count, *slot_map, *n, *seqlen, *table;
+    int32_t *n_out, *seqlen_out;
+    int *status;
+};
+cudaError_t launch_draft_commit(const CommitLaunch &p, cudaStream_t s);
 
 // New rows to the slots of a slot map (rows of the cache's K / V arrays, -1: skipped).
 struct PackedLaunch {
