@@ -83,29 +83,40 @@ int sm_count()
 }
 
 namespace {
+enum KernelFact { SMEM_SET, RESIDENT, LARGE_CLUSTERS };
 struct KernelDeviceEntry {
     const void *func;
     int dev;
-    int value;   // resident CTAs (resident_ctas) or 1 (set_smem_once)
-    bool occupancy;
+    int value;   // resident CTAs (resident_ctas), else 1
+    KernelFact fact;
 };
 std::vector<KernelDeviceEntry> g_kernel_entries;   // guarded by g_mu
 } // namespace
 
-cudaError_t set_smem_once(const void *func, int bytes)
+static cudaError_t set_attribute_once(const void *func, KernelFact fact, cudaFuncAttribute attr,
+                                      int value)
 {
     const int dev = current_device();
     if (dev < 0)
         return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lk(g_mu);
     for (const KernelDeviceEntry &e : g_kernel_entries)
-        if (e.func == func && e.dev == dev && !e.occupancy)
+        if (e.func == func && e.dev == dev && e.fact == fact)
             return cudaSuccess;
-    const cudaError_t err =
-        cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t err = cudaFuncSetAttribute(func, attr, value);
     if (err == cudaSuccess)
-        g_kernel_entries.push_back({func, dev, 1, false});
+        g_kernel_entries.push_back({func, dev, 1, fact});
     return err;
+}
+
+cudaError_t set_smem_once(const void *func, int bytes)
+{
+    return set_attribute_once(func, SMEM_SET, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+cudaError_t allow_large_clusters_once(const void *func)
+{
+    return set_attribute_once(func, LARGE_CLUSTERS, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
 int resident_ctas(const void *func, int threads, int smem)
@@ -116,13 +127,13 @@ int resident_ctas(const void *func, int threads, int smem)
     const int sms = sm_count();
     std::lock_guard<std::mutex> lk(g_mu);
     for (const KernelDeviceEntry &e : g_kernel_entries)
-        if (e.func == func && e.dev == dev && e.occupancy)
+        if (e.func == func && e.dev == dev && e.fact == RESIDENT)
             return e.value;
     int per_sm = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, func, threads, smem) != cudaSuccess)
         per_sm = 1;
     const int v = (per_sm > 0 ? per_sm : 1) * sms;
-    g_kernel_entries.push_back({func, dev, v, true});
+    g_kernel_entries.push_back({func, dev, v, RESIDENT});
     return v;
 }
 

@@ -75,57 +75,61 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tree_plan(const TreePlanLaunch
 //
 // Sums.  A running sum of V probabilities decides between neighbours that are 2^-24 apart and
 // less, and there are V borders: with 32-bit sums (off by 10^-8) one token in a few hundred would
-// be another one than 64-bit arithmetic draws.  So a weight is taken apart exactly: with
-// t = w + 1 the bits of t count units of 2^-23, what is left counts units of 2^-46 in the same
-// way, and what is left of that is below 2^-47 and summed in 32 bits.  A thread's three
-// sums become one 64-bit number of units 2^-52, and these add up in any order to the same.
+// be another one than 64-bit arithmetic draws.  64-bit floating point runs at two operations per
+// clock and SM here, so a thread adds in pairs of 32-bit numbers: each addition's exact rounding
+// error (six additions, without a branch) goes into a second sum.  What is lost is 2^-48 of a
+// thread's sum.  The pair becomes one 64-bit number of units 2^-52, and from there on all sums are
+// integers, which add up in any order to the same.  The mass of the residual max(p - a q, 0) is
+// sum p - a sum q over the tokens with p > a q: two such sums, a multiplied in once.  A token
+// that the rounding of a moves across that border has a weight of 2^-24 of its probability.
 constexpr int VER_THREADS = 256, VER_WARPS = VER_THREADS / 32;
-constexpr int VER_UNROLL = 4;                 // strips of 32 vectors in flight per warp
+constexpr int VER_UNROLL = 4;   // strips of 32 vectors in flight per warp
+constexpr int MAX_CLUSTER = 16;
 constexpr uint64_t ONE = 1ull << 52;          // a weight of 1 in fixed point
+constexpr uint64_t A_MOST = 1024 * ONE;       // no distributions get there
 
-__device__ __forceinline__ float clean(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
+// To [0, 1]; NaN becomes 0.
+__device__ __forceinline__ float clean(float x) { return __saturatef(x); }
 
-// Weight p - a q of a token, where positive, as a sum of two floats; a is a sum of two, too.
-struct Weight {
-    float w, rest;
-    __device__ Weight(float p, float q, float ah, float al)
-    {
-        const float h = __fmul_rn(ah, q), l = __fmaf_rn(ah, q, -h);
-        const float d = __fsub_rn(p, h), b = __fsub_rn(d, p);
-        const float e = __fsub_rn(__fsub_rn(p, __fsub_rn(d, b)), __fadd_rn(h, b));
-        const float lo = __fmaf_rn(-al, q, __fsub_rn(e, l));
-        const float s = __fadd_rn(d, lo);
-        w = s > 0.f ? s : 0.f;
-        rest = s > 0.f ? __fsub_rn(lo, __fsub_rn(s, d)) : 0.f;
-    }
-    __device__ explicit Weight(float p) : w(p), rest(0.f) {}
-};
-
-struct Sum {
-    uint32_t hi = 0, lo = 0;
-    float rest = 0.f;
-    __device__ void add(const Weight &x)
-    {
-        constexpr float M = 1.5f / (1 << 23);
-        const float t = __fadd_rn(x.w, 1.f);
-        hi += __float_as_uint(t) - __float_as_uint(1.f);
-        const float l = __fadd_rn(__fsub_rn(x.w, __fsub_rn(t, 1.f)), x.rest);
-        const float t2 = __fadd_rn(l, M);
-        lo += __float_as_uint(t2) - __float_as_uint(M);
-        rest = __fadd_rn(rest, __fsub_rn(l, __fsub_rn(t2, M)));
-    }
-    // not negative but for a rounding of weights near 0
-    __device__ uint64_t fixed() const
-    {
-        const long long x = ((long long)hi << 29) + ((long long)(int32_t)lo << 6) +
-                            __float2ll_rn(rest * 4503599627370496.f);
-        return x > 0 ? (uint64_t)x : 0;
-    }
-};
-
-__device__ __forceinline__ uint64_t shfl_xor64(uint64_t x, int m)
+__device__ __forceinline__ uint64_t to_fixed(float x)
 {
-    return __shfl_xor_sync(ALL, (unsigned long long)x, m);
+    return (uint64_t)__float2ll_rn(x * 4503599627370496.f);   // exact down to 2^-28, then rounded
+}
+
+// a times x, both of 2^-52, x at most 2
+__device__ __forceinline__ uint64_t mul_fixed(uint64_t a, uint64_t x)
+{
+    return __umul64hi(a, x) << 12 | (a * x) >> 52;
+}
+
+__device__ __forceinline__ uint64_t less_fixed(uint64_t x, uint64_t y) { return x > y ? x - y : 0; }
+
+// Sum of pairs of numbers with the rounding errors of its additions.
+struct Sum2 {
+    float2 sum = make_float2(0.f, 0.f), err = make_float2(0.f, 0.f);
+    __device__ __forceinline__ void add(float2 x)
+    {
+        const float2 s = fadd2(sum, x), b = fsub2(s, sum);
+        err = fadd2(err, fadd2(fsub2(sum, fsub2(s, b)), fsub2(x, b)));
+        sum = s;
+    }
+    // both halves, at most 2
+    __device__ __forceinline__ uint64_t fixed() const
+    {
+        const float s = __fadd_rn(sum.x, sum.y), b = __fsub_rn(s, sum.x);
+        const float r = __fadd_rn(__fsub_rn(sum.x, __fsub_rn(s, b)), __fsub_rn(sum.y, b));
+        const long long v = (long long)to_fixed(fminf(s, 2.f)) +
+                            (long long)to_fixed(__fadd_rn(r, __fadd_rn(err.x, err.y)));
+        return v < 0 ? 0 : min((uint64_t)v, 2 * ONE);
+    }
+};
+
+__device__ __forceinline__ uint64_t warp_sum64(uint64_t x)
+{
+#pragma unroll
+    for (int m = 16; m; m >>= 1)
+        x += __shfl_xor_sync(ALL, (unsigned long long)x, m);
+    return x;
 }
 
 // A row of the vocabulary in vectors of four entries that begin on 16-byte boundaries: vector
@@ -137,12 +141,10 @@ struct Row {
     {
         off = (int)(reinterpret_cast<uintptr_t>(row) >> 2 & 3);
     }
-    __device__ int vectors() const { return (V + off + 3) / 4; }
-    // entries i0 .. i0 + 3; this row's own vectors are loaded whole
+    __device__ int vectors() const { return (int)(((unsigned)V + off + 3) / 4); }
+    // entries i0 .. i0 + 3, those outside 0
     __device__ float4 load(int i0) const
     {
-        if (i0 >= 0 && i0 + 3 < V && ((i0 + off) & 3) == 0)
-            return *reinterpret_cast<const float4 *>(at + i0);
         float4 x;
         x.x = i0 >= 0 && i0 < V ? at[i0] : 0.f;
         x.y = i0 + 1 >= 0 && i0 + 1 < V ? at[i0 + 1] : 0.f;
@@ -156,43 +158,45 @@ struct VerShared {
     int parent[MAX_NODES], token[MAX_NODES];
     float u[MAX_NODES], p[MAX_NODES], q[MAX_NODES];
     int path[MAX_NODES], gone[MAX_NODES];
-    uint64_t warp[VER_WARPS];
-    uint64_t total[2];       // this CTA's, read by the cluster; two, used in turn
-    int cur, count, n_gone, ask;
-    float ah, al;
+    uint64_t warp[2][VER_WARPS];
+    uint64_t total[2][MAX_CLUSTER];   // the cluster's CTAs', written by them; two, used in turn
+    float u_next;
+    // the walk: at node cur, whose children up to node last have been refused
+    uint64_t a;
+    long long left;
+    int cur, last, count, n_gone, ask;
 };
 
-__device__ __forceinline__ uint64_t ld_cluster_u64(const uint64_t *local, uint32_t rank)
+// To the shared memory of CTA `rank` of this cluster, at the offset that `local` has in this CTA's.
+__device__ __forceinline__ void st_cluster_u64(uint64_t *local, uint32_t rank, uint64_t v)
 {
     uint32_t ra;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(local)), "r"(rank));
-    uint64_t v;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(ra) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(ra), "l"(v) : "memory");
 }
 
-// The weights of a row, dealt to the cluster's warps in contiguous ranges of vectors.
+// The weights of a row: max(p - a q, 0), or with a = 0 those of p without some tokens.  Of a
+// range of vectors [v0, v1), by a warp.
 struct Weights {
     Row p, q;
-    bool residual;           // p - a q; else p
-    float ah, al;
+    uint64_t a;
+    float ah;                // a in 32 bits
     const int *gone;         // tokens whose weight is 0
     int n_gone;
-    int v0, v1;              // this warp's vectors
 
-    __device__ __forceinline__ void load(int v, float4 &x, float4 &y) const
+    // whether some token of the range is gone
+    __device__ __forceinline__ bool patched(int v0, int v1) const
     {
-        const int i0 = 4 * v - p.off;
-        x = y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (v < v1) {
-            x = p.load(i0);
-            if (residual)
-                y = q.load(i0);
+        bool some = false;
+        for (int k = threadIdx.x & 31; k < n_gone; k += 32) {
+            const int v = (gone[k] + p.off) >> 2;
+            some |= v >= v0 && v < v1;
         }
+        return __any_sync(ALL, some);
     }
-    __device__ __forceinline__ float4 kept(int v, float4 x) const
+    __device__ __forceinline__ void keep(float4 &x, int i0) const
     {
-        const int i0 = 4 * v - p.off;
+#pragma unroll 1
         for (int k = 0; k < n_gone; ++k) {
             const int i = gone[k] - i0;
             x.x = i == 0 ? 0.f : x.x;
@@ -200,61 +204,133 @@ struct Weights {
             x.z = i == 2 ? 0.f : x.z;
             x.w = i == 3 ? 0.f : x.w;
         }
-        return x;
     }
-    __device__ __forceinline__ Weight weight(float x, float y) const
+    // 1 where the weight is positive
+    __device__ __forceinline__ float2 positive(float2 x, float2 y) const
     {
-        return residual ? Weight(clean(x), clean(y), ah, al) : Weight(clean(x));
+        const float2 d = ffma2(make_float2(-ah, -ah), y, x);
+        return make_float2(d.x > 0.f ? 1.f : 0.f, d.y > 0.f ? 1.f : 0.f);
     }
-    // Sum of this warp's weights (at most 2, which no distribution reaches).
-    __device__ uint64_t sum() const
+    // p and q of the tokens that count
+    __device__ __forceinline__ void split(float4 x, float4 y, float2 (&ps)[2], float2 (&qs)[2]) const
     {
+        const float2 x0 = make_float2(clean(x.x), clean(x.y)), x1 = make_float2(clean(x.z), clean(x.w));
+        const float2 y0 = make_float2(clean(y.x), clean(y.y)), y1 = make_float2(clean(y.z), clean(y.w));
+        const float2 m0 = positive(x0, y0), m1 = positive(x1, y1);
+        ps[0] = fmul2(x0, m0);
+        ps[1] = fmul2(x1, m1);
+        qs[0] = fmul2(y0, m0);
+        qs[1] = fmul2(y1, m1);
+    }
+    // Vector v of any place and alignment.
+    __device__ __forceinline__ void any_vector(int v, float2 (&ps)[2], float2 (&qs)[2]) const
+    {
+        const int i0 = 4 * v - p.off;
+        float4 x = p.load(i0), y = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (a)
+            y = q.load(i0);
+        keep(x, i0);
+        split(x, y, ps, qs);
+    }
+    // Sum of the range's weights: whole vectors VER_UNROLL strips of 32 at a time, the others (the
+    // row's ends, the range's last strips, a q of another alignment than p's) one by one.
+    __device__ __forceinline__ uint64_t sum(int v0, int v1) const
+    {
+        constexpr int U = VER_UNROLL;
         const int lane = threadIdx.x & 31;
-        uint64_t all = 0;
-        for (int v = v0 + lane; v - lane < v1; v += 32 * VER_UNROLL) {
-            float4 x[VER_UNROLL], y[VER_UNROLL];
-#pragma unroll
-            for (int u = 0; u < VER_UNROLL; ++u)
-                load(v + 32 * u, x[u], y[u]);
-            Sum s;
-#pragma unroll
-            for (int u = 0; u < VER_UNROLL; ++u) {
-                if (n_gone)
-                    x[u] = kept(v + 32 * u, x[u]);
-                s.add(weight(x[u].x, y[u].x));
-                s.add(weight(x[u].y, y[u].y));
-                s.add(weight(x[u].z, y[u].z));
-                s.add(weight(x[u].w, y[u].w));
+        Sum2 sp, sq;
+        int v = v0;
+        float2 ps[2], qs[2];
+        if (v < v1 && v == 0 && p.off) {         // the row's first vector is not whole
+            if (lane < v1) {
+                any_vector(lane, ps, qs);
+                sp.add(ps[0]);
+                sp.add(ps[1]);
+                sq.add(qs[0]);
+                sq.add(qs[1]);
             }
-            all = min(all + s.fixed(), 2 * ONE);
+            v = min(32, v1);
         }
+        const int whole = min(v1, (p.V + p.off) / 4);
+        if (a && p.off == q.off) {
+            const float4 *xs = reinterpret_cast<const float4 *>(p.at - p.off) + lane;
+            const float4 *ys = reinterpret_cast<const float4 *>(q.at - q.off) + lane;
+#pragma unroll 1
+            for (; v + 32 * U <= whole; v += 32 * U) {
+                float4 x[U], y[U];
 #pragma unroll
-        for (int m = 16; m; m >>= 1)
-            all += shfl_xor64(all, m);
-        return min(all, 2 * ONE);
+                for (int u = 0; u < U; ++u) {
+                    x[u] = xs[v + 32 * u];
+                    y[u] = ys[v + 32 * u];
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    split(x[u], y[u], ps, qs);
+                    sp.add(ps[0]);
+                    sq.add(qs[0]);
+                    sp.add(ps[1]);
+                    sq.add(qs[1]);
+                }
+            }
+        } else if (!a) {
+            const bool patch = n_gone > 0 && patched(v0, v1);
+            const float4 *xs = reinterpret_cast<const float4 *>(p.at - p.off) + lane;
+#pragma unroll 1
+            for (; v + 32 * U <= whole; v += 32 * U) {
+                float4 x[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    x[u] = xs[v + 32 * u];
+                if (patch)
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        keep(x[u], 4 * (v + 32 * u + lane) - p.off);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    sp.add(make_float2(clean(x[u].x), clean(x[u].y)));
+                    sp.add(make_float2(clean(x[u].z), clean(x[u].w)));
+                }
+            }
+        }
+#pragma unroll 1
+        for (v += lane; v < v1; v += 32) {
+            any_vector(v, ps, qs);
+            sp.add(ps[0]);
+            sp.add(ps[1]);
+            sq.add(qs[0]);
+            sq.add(qs[1]);
+        }
+        const uint64_t total = min(warp_sum64(sp.fixed()), 2 * ONE);
+        if (!a)
+            return total;
+        return less_fixed(total, mul_fixed(a, min(warp_sum64(sq.fixed()), 2 * ONE)));
     }
-    // First token of this warp's range at which the running sum (which is `below` before it)
-    // exceeds `line`; the range's last token with a weight if roundings hide it.
-    __device__ int find(uint64_t below, uint64_t line) const
+    // First token of the range at which the running sum (which is `below` before it) exceeds
+    // `line`; the range's last token with a weight if roundings hide it.
+    __device__ __forceinline__ int find(int v0, int v1, uint64_t below, uint64_t line) const
     {
         const int lane = threadIdx.x & 31;
         int last = -1;
-        for (int v = v0 + lane; v - lane < v1; v += 32) {
-            float4 x, y;
-            load(v, x, y);
-            x = kept(v, x);
-            const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-            uint64_t f[4], own = 0;
+#pragma unroll 1
+        for (int v = v0; v < v1; v += 32) {
+            const int i0 = 4 * (v + lane) - p.off;
+            float2 ps[2], qs[2];
+            if (v + lane < v1)
+                any_vector(v + lane, ps, qs);
+            else
+                ps[0] = ps[1] = qs[0] = qs[1] = make_float2(0.f, 0.f);
+            const float x[4] = {ps[0].x, ps[0].y, ps[1].x, ps[1].y};
+            const float y[4] = {qs[0].x, qs[0].y, qs[1].x, qs[1].y};
+            uint64_t w[4], upto = 0;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const Weight w = weight(xs[c], ys[c]);
-                Sum s;
-                s.add(w);
-                f[c] = s.fixed();
-                own += f[c];
-                last = w.w > 0.f ? 4 * v - p.off + c : last;
+                w[c] = to_fixed(x[c]);
+                if (a)
+                    w[c] = less_fixed(w[c], mul_fixed(a, to_fixed(y[c])));
+                upto += w[c];
+                last = x[c] > 0.f ? i0 + c : last;
             }
-            uint64_t upto = own;
+            const uint64_t mine = upto;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const uint64_t o = __shfl_up_sync(ALL, (unsigned long long)upto, off);
@@ -262,17 +338,14 @@ struct Weights {
             }
             const unsigned over = __ballot_sync(ALL, below + upto > line);
             if (over) {
-                uint64_t at = below + upto - own;
-                int token = -1;
+                uint64_t run = below + upto - mine;
+                int c = 0;
 #pragma unroll
-                for (int c = 3; c >= 0; --c) {
-                    uint64_t to = at;
-#pragma unroll
-                    for (int k = 0; k <= c; ++k)
-                        to += f[k];
-                    token = to > line ? 4 * v - p.off + c : token;
+                for (int i = 0; i < 3; ++i) {
+                    run += w[i];
+                    c += run <= line;
                 }
-                return __shfl_sync(ALL, token, __ffs(over) - 1);
+                return __shfl_sync(ALL, i0 + c, __ffs(over) - 1);
             }
             below += __shfl_sync(ALL, (unsigned long long)upto, 31);
         }
@@ -283,7 +356,17 @@ struct Weights {
     }
 };
 
-__global__ void __launch_bounds__(VER_THREADS) k_draft_verify(const VerifyLaunch p, const int size)
+// Vectors of part `i` of `parts` of [v0, v1): whole strips of 32.  Returns the length of the first
+// part, which no other one exceeds.
+__device__ __forceinline__ int part_of(int &v0, int &v1, int i, int parts)
+{
+    const int per = ((v1 - v0 + parts - 1) / parts + 31) / 32 * 32;
+    v0 = (int)min((long)v1, v0 + (long)i * per);
+    v1 = min(v1, v0 + per);
+    return per;
+}
+
+__global__ void __launch_bounds__(VER_THREADS, 4) k_draft_verify(const VerifyLaunch p, const int size)
 {
     __shared__ VerShared s;
     const int b = blockIdx.x / size, rank = blockIdx.x - b * size;
@@ -291,6 +374,8 @@ __global__ void __launch_bounds__(VER_THREADS) k_draft_verify(const VerifyLaunch
     const bool drawn = p.q != nullptr;
     int start, len;
     node_range(p.cu, b, p.T, MAX_NODES, p.status, start, len);
+    if (threadIdx.x == 0 && len > 0)
+        s.u_next = p.u_next[b];
     for (int i = threadIdx.x; i < len; i += VER_THREADS) {
         int up = p.parent ? p.parent[start + i] : i - 1;
         const int x = p.tokens[start + i];
@@ -305,59 +390,32 @@ __global__ void __launch_bounds__(VER_THREADS) k_draft_verify(const VerifyLaunch
         s.p[i] = in ? clean(p.p[(start + up) * p.ps + x]) : 0.f;
         s.q[i] = in && drawn ? clean(p.q[(start + up) * p.qs + x]) : 0.f;
     }
-    __syncthreads();
-
-    int phase = 0;           // which of the two totals is in use
-    uint64_t below = 0;      // sum of the weights in front of this warp's range
-    Weights w{Row(nullptr, 0), Row(nullptr, 0), false, 0.f, 0.f, s.gone, 0, 0, 0};
-    // Sum over the row of node c; in every thread of the cluster.
-    auto row_sum = [&](int c, bool residual, float ah, float al, int n_gone) -> uint64_t {
-        w.p = Row(p.p + (start + c) * p.ps, p.V);
-        w.q = Row(residual ? p.q + (start + c) * p.qs : nullptr, p.V);
-        w.residual = residual;
-        w.ah = ah;
-        w.al = al;
-        w.n_gone = n_gone;
-        const int vectors = w.p.vectors();
-        const int per = ((vectors + size * VER_WARPS - 1) / (size * VER_WARPS) + 31) / 32 * 32;
-        w.v0 = min(vectors, (rank * VER_WARPS + warp) * per);
-        w.v1 = min(vectors, w.v0 + per);
-        const uint64_t mine = w.sum();
-        if (lane == 0)
-            s.warp[warp] = mine;
+    if (size > 1)
+        cluster_sync_all();      // every CTA of the cluster runs: its shared memory may be written
+    else
         __syncthreads();
-        uint64_t total = 0;
-        below = 0;
-#pragma unroll
-        for (int i = 0; i < VER_WARPS; ++i) {
-            const uint64_t x = s.warp[i];
-            below += i < warp ? x : 0;
-            total += x;
-        }
-        if (size > 1) {
-            s.total[phase] = total;
-            cluster_sync_all();
-            total = 0;
-            for (int i = 0; i < size; ++i) {
-                const uint64_t x = ld_cluster_u64(&s.total[phase], i);
-                below += i < rank ? x : 0;
-                total += x;
-            }
-            phase ^= 1;
-        }
-        __syncthreads();     // s.warp is free again
-        return total;
-    };
 
-    // The walk, by warp 0: what lies behind (cur, j) is the same in all its lanes.
-    int cur = 0, j = 0, count = len > 0 ? 1 : 0, n_gone = 0;
-    double a = 0.0, left = 1.0;
-    bool have = true;        // `left` is that of a
-    if (threadIdx.x == 0)
-        s.path[0] = 0;
+    // The walk is warp 0's; its state waits in shared memory during the passes over a row: for the
+    // residual's mass, then for the next token.
+    if (threadIdx.x == 0) {
+        s.path[0] = s.cur = s.last = s.n_gone = 0;
+        s.count = len > 0 ? 1 : 0;
+        s.a = 0;
+        s.left = ONE;
+    }
+    Weights w{Row(nullptr, 0), Row(nullptr, 0), 0, 0.f, s.gone, 0};
+    int phase = 0;               // which of the two totals is in use
+    uint64_t at = 0, line = 0;   // sum in front of this CTA's, the owner's, the finder's range; the draw
+    int owner = -1;              // the CTA's warp in whose range the next token lies
+    int v0, v1;                  // this warp's range of vectors
+    bool finder = false, none = true, plain = false;
     for (;;) {
-        if (warp == 0) {
-            bool ask = false;
+        if (warp == 0 && owner < 0 && !plain) {
+            __syncwarp();
+            int cur = s.cur, j = s.last, count = s.count, n_gone = s.n_gone;
+            uint64_t a = s.a;            // of 2^-52, like `left`, the mass S; of given tokens 0
+            long long left = s.left;
+            bool ask = false, have = true;   // `left` is that of a
             while (count > 0 && count < p.max_path) {
                 int child = -1;
                 for (int i = j + 1; i < len && child < 0; i += 32) {
@@ -367,38 +425,47 @@ __global__ void __launch_bounds__(VER_THREADS) k_draft_verify(const VerifyLaunch
                 if (child < 0)
                     break;
                 if (!have) {
-                    ask = true;      // the residual's mass, from everybody
+                    ask = true;          // the residual's mass, from everybody
                     break;
                 }
+                // accepted iff u q S < p - a q; of given tokens q is 1 and a 0
                 const int x = s.token[child];
-                const double u = s.u[child], qx = s.q[child];
-                double wx = s.p[child];
-                bool take;
-                if (drawn) {
-                    wx -= a * qx;
-                    take = wx > 0.0 && u * qx * left < wx;
-                } else {
+                const float u = s.u[child], qx = drawn ? s.q[child] : 1.f;
+                float px = s.p[child];
+                if (n_gone > 0) {
                     bool again = false;
                     for (int k = lane; k < n_gone; k += 32)
                         again |= s.gone[k] == x;
-                    if (__any_sync(ALL, again))
-                        wx = 0.0;
-                    take = wx > 0.0 && u * left < wx;
+                    px = __any_sync(ALL, again) ? 0.f : px;
                 }
+                bool take;
+                if (a == 0 && left == (long long)ONE) {
+                    take = __fmaf_rn(u, qx, -px) < 0.f;      // one rounding: the sign is exact
+                } else {
+                    // 32 bits where they are enough: 64-bit products take hundreds of clocks here
+                    const float af = (float)a * (1.f / ONE), rhs = __fmaf_rn(-af, qx, px);
+                    const float lhs = u * qx * ((float)left * (1.f / ONE));
+                    take = lhs < rhs;
+                    if (fabsf(lhs - rhs) <= (fabsf(lhs) + px + af * qx) * (1.f / (1 << 21))) {
+                        const double wx = (double)px - (double)a * (1.0 / (double)ONE) * (double)qx;
+                        take = wx > 0.0 && (double)u * (double)qx * ((double)left * (1.0 / (double)ONE)) < wx;
+                    }
+                }
+                take = take && px > 0.f;
                 j = child;
                 if (take) {
                     cur = child;
-                    a = 0.0;
-                    left = 1.0;
+                    a = 0;
+                    left = ONE;
                     n_gone = 0;
                     if (lane == 0)
                         s.path[count] = child;
                     ++count;
                 } else if (drawn) {
-                    a += left;
+                    a = min(a + (uint64_t)left, A_MOST);
                     have = false;
                 } else {
-                    left -= wx;
+                    left -= (long long)to_fixed(px);
                     if (lane == 0)
                         s.gone[n_gone] = x;
                     ++n_gone;
@@ -408,48 +475,116 @@ __global__ void __launch_bounds__(VER_THREADS) k_draft_verify(const VerifyLaunch
             if (lane == 0) {
                 s.ask = ask;
                 s.cur = cur;
+                s.last = j;
                 s.count = count;
                 s.n_gone = n_gone;
-                s.ah = (float)a;
-                s.al = (float)(a - (double)(float)a);
+                s.a = a;
             }
         }
         __syncthreads();
-        if (!s.ask)
+        if (len == 0)
             break;
-        const uint64_t sum = row_sum(s.cur, true, s.ah, s.al, 0);
-        left = (double)sum * (1.0 / (double)ONE);
-        have = true;
+        // Sum of the weights of node cur's row, in every thread of the cluster; or, when the next
+        // token's place is known to lie in warp `owner`'s range, of the parts of that range.
+        w.a = plain ? 0 : s.a;
+        w.ah = (float)w.a * (1.f / ONE);
+        w.n_gone = plain ? 0 : s.n_gone;
+        w.p = Row(p.p + (start + s.cur) * p.ps, p.V);
+        w.q = Row(w.a ? p.q + (start + s.cur) * p.qs : nullptr, p.V);
+        v0 = 0;
+        v1 = w.p.vectors();
+        const int per = part_of(v0, v1, rank * VER_WARPS + (owner < 0 ? warp : owner), size * VER_WARPS);
+        if (owner >= 0)
+            part_of(v0, v1, warp, VER_WARPS);
+        const uint64_t mine = w.sum(v0, v1);
+        if (lane == 0)
+            s.warp[owner >= 0][warp] = mine;
+        __syncthreads();
+        if (owner >= 0) {
+            int part = -1;
+            uint64_t from = at;
+#pragma unroll
+            for (int i = 0; i < VER_WARPS; ++i) {
+                const uint64_t x = s.warp[1][i];
+                if (part < 0) {
+                    if (line - from < x)
+                        part = i;
+                    else
+                        from += x;
+                }
+            }
+            if (part >= 0) {
+                at = from;
+            } else {             // roundings of the parts hide it: the whole range
+                v0 = 0;
+                v1 = w.p.vectors();
+                part_of(v0, v1, rank * VER_WARPS + owner, size * VER_WARPS);
+            }
+            finder = warp == max(part, 0);
+            break;
+        }
+        uint64_t total = 0;
+#pragma unroll
+        for (int i = 0; i < VER_WARPS; ++i)
+            total += s.warp[0][i];
+        at = 0;
+        if (size > 1) {
+            if (threadIdx.x < size)
+                st_cluster_u64(&s.total[phase][rank], threadIdx.x, total);
+            cluster_sync_all();
+            total = 0;
+#pragma unroll 4
+            for (int i = 0; i < size; ++i) {
+                const uint64_t x = s.total[phase][i];
+                at += i < rank ? x : 0;
+                total += x;
+            }
+            phase ^= 1;
+        }
+        if (s.ask) {
+            if (threadIdx.x == 0)
+                s.left = (long long)total;
+        } else if (total > 0) {
+            none = false;
+            const float u = fminf(fmaxf(s.u_next, 0.f), 0x1.fffffep-1f);
+            line = __umul64hi(__float2ull_rz(u * 18446744073709551616.f), total);
+            if (line < at)
+                break;
+#pragma unroll
+            for (int i = 0; i < VER_WARPS; ++i) {
+                const uint64_t x = s.warp[0][i];
+                if (owner < 0) {
+                    if (line - at < x)
+                        owner = i;
+                    else
+                        at += x;
+                }
+            }
+            finder = warp == owner;
+            if (owner < 0 || per <= 32 * VER_UNROLL)   // another CTA's, or short: no parts
+                break;
+        } else {
+            if (!w.a && !w.n_gone)
+                break;
+            plain = true;        // nothing of p is left: p itself
+        }
+        __syncthreads();         // what warp 0 wrote, and the warps' sums, have been read
     }
 
-    // The next token, and the path.
-    uint64_t total = 0;
-    if (len > 0) {
-        const bool residual = s.ah > 0.f;
-        total = row_sum(s.cur, residual, s.ah, s.al, s.n_gone);
-        if (total == 0 && (residual || s.n_gone))
-            total = row_sum(s.cur, false, 0.f, 0.f, 0);
-    }
-    if (total > 0) {
-        const float u = fminf(fmaxf(p.u_next[b], 0.f), 0x1.fffffep-1f);
-        const uint64_t line = __umul64hi(__float2ull_rz(u * 18446744073709551616.f), total);
-        if (line >= below && line - below < s.warp[warp]) {
-            const int token = w.find(below, line);
-            if (lane == 0)
-                p.next_token[b] = token;
-        }
+    if (finder) {
+        const int token = w.find(v0, v1, at, line);
+        if (lane == 0)
+            p.next_token[b] = token;
     }
     if (rank == 0) {
         if (threadIdx.x == 0) {
             p.count[b] = s.count;
-            if (total == 0)
+            if (none)
                 p.next_token[b] = -1;
         }
         for (int i = threadIdx.x; i < p.max_path; i += VER_THREADS)
             p.path[(size_t)b * p.max_path + i] = i < s.count ? s.path[i] : -1;
     }
-    if (size > 1)
-        cluster_sync_all();  // a CTA's totals are read by the others
 }
 
 // ------------------------------------------------------------------ the accepted path's rows
@@ -524,9 +659,30 @@ cudaError_t launch_tree_plan(const TreePlanLaunch &p, cudaStream_t s)
     return cudaGetLastError();
 }
 
+// CTAs per sequence.  A pass over a row costs a cluster barrier and what a CTA reads, and many
+// sequences fill the card by themselves: the more there are, the longer a CTA's part has to be.
+// Measured in a graph, us, with 1 / 2 / 4 / 8 / 16 CTAs (drawn trees of up to 6 nodes): one sequence
+// of 32000 tokens 9.6 / 8.9 / 7.8 / 7.7 / 6.9, of 128000 20.8 / 15.3 / 10.8 / 9.0 / 8.2; 64 sequences
+// of 32000 22.5 / 18.3 / 15.6 / 15.9 / 24.1, of 128000 72 / 47 / 30 / 24 / 30; 512 of 32000
+// 40 / 41 / 48 / 69 / 153, of 128000 94 / 81 / 73 / 84 / 139; 1000 tokens take one CTA at any number.
+int verify_ctas(int B, int V)
+{
+    const int part = 1900 + 64 * (B < 256 ? B : 256), most = B >= 128 ? 4 : B > 32 ? 8 : MAX_CLUSTER;
+    int size = 1;
+    while (2 * size <= most && V / part >= 2 * size)
+        size *= 2;
+    return size;
+}
+
 cudaError_t launch_draft_verify(const VerifyLaunch &p, cudaStream_t s)
 {
-    const int size = 1;
+    const int size = verify_ctas(p.B, p.V);
+    const void *kernel = reinterpret_cast<const void *>(k_draft_verify);
+    if (size > 8) {
+        const cudaError_t e = allow_large_clusters_once(kernel);
+        if (e != cudaSuccess)
+            return e;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)p.B * size);
     cfg.blockDim = dim3(VER_THREADS);

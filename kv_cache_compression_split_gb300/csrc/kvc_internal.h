@@ -24,6 +24,9 @@ int sm_count();
 // device, once per (kernel, device); thread safe.  Returns the attribute call's error.
 cudaError_t set_smem_once(const void *func, int bytes);
 
+// Let kernel `func` run in clusters of more than 8 CTAs on the current device, likewise once.
+cudaError_t allow_large_clusters_once(const void *func);
+
 // CTAs of `func` (threads per CTA, dynamic shared memory) resident on all SMs of the
 // current device together (at least one per SM), cached per (kernel, device).
 int resident_ctas(const void *func, int threads, int smem);
