@@ -21,7 +21,12 @@
 //
 // Pipeline.  The grid has a CTA per item; one that runs takes over the items of CTAs that
 // have not started (cluster launch control), so work is balanced without a counter in
-// memory and the pipeline does not drain between items.  A producer warp (TMA: query
+// memory and the pipeline does not drain between items.  A warp asks for the next item and looks
+// it up: its sequence, its unit's slots, its part of the page table.  It does so when the
+// producer has LEAD blocks of the item before left to load.  Asked for at that item's start, an
+// item is held back by a CTA that may be busy for long: 16 trees over 1000 to 8192 slots 232 us
+// then, 212 with 2 to 6 blocks left, 4 chunks of 257 to 512 tokens over such caches 178 and 155,
+// 4 prompts of 2048 tokens of 32 heads 120 and 115.  A producer warp (TMA: query
 // tiles, and K and V blocks through a ring), an MMA warp, and a warpgroup per tile in
 // which a thread owns a row.  S = Q K^T (128 x 128, fp32) lands in TMEM; the row's
 // thread reads it, keeps the running reference m and sum l in registers, and writes
@@ -79,7 +84,7 @@ constexpr float LN2 = 0.6931471805599453f;
 constexpr float BELOW = 7.f, GROWTH = 8.f;
 
 template <int D, int TILES> struct TokCfg {
-    static constexpr int W_TMA = 4 * TILES, W_MMA = W_TMA + 1;   // two more warps are idle
+    static constexpr int W_TMA = 4 * TILES, W_MMA = W_TMA + 1, W_NEXT = W_TMA + 2;   // one more is idle
     static constexpr int NTHR = 128 * (TILES + 1);
     static constexpr int CTAS = 3 - TILES;                 // per SM
     // keys of a block, and score buffers in TMEM: one per tile, or two for the only tile, so
@@ -89,6 +94,7 @@ template <int D, int TILES> struct TokCfg {
     static constexpr int QBOX_BYTES = TM * 128, QTILE_BYTES = NBOX * QBOX_BYTES;
     static constexpr int BOX_BYTES = TK * 128, TILE_BYTES = NBOX * BOX_BYTES;
     static constexpr int NS = D == 128 ? 4 : 8;   // ring stages (one K or V block each)
+    static constexpr int LEAD = 4;   // blocks of an item that are still to be loaded when the next is asked for
     // output area of a row warp: buffers of 32 rows of 64 bytes
     static constexpr int OUT_BUF = 32 * 64, OUT_BUFS = TILES;
     static constexpr int OUT_BYTES = OUT_BUFS * OUT_BUF;
@@ -116,6 +122,7 @@ struct TokItem {
     int tok0, ntok;      // tokens of the sequence
     int start;           // the sequence's first token in the tensors
     int shift;           // token i sees the keys j <= i + shift
+    int keys;            // of the sequence or unit
     int j0, j1;          // key blocks
     int split;
     int two;             // one tile of rows, its blocks dealt to both warpgroups
@@ -141,9 +148,17 @@ __device__ __forceinline__ void seq_range(const TokensLaunch &p, int b, int &sta
 // Walks the items in order: sequences, token ranges from the last (longest) to the
 // first, KV heads, splits.  Every lane of the warp calls it.  It goes on from the
 // sequences of the last call, since the work is handed out in order.
+// Over a cache the sequences' slots may differ by far, and an item that is long and starts late
+// runs while other SMs have nothing left.  So up to 32 sequences, one per lane, whose items do
+// not all run at once are walked in four rounds, those of most slots first (by the first
+// head's): 16 trees over 1000 to 8192 slots of 32 heads 217 us as they come, 215 in this order, 4
+// chunks of 257 to 512 tokens over 2000 to 8192 slots 178 and 155.  Of more sequences the items
+// are many against the CTAs that run.
 struct ItemWalk {
-    int b0 = 0;
+    static constexpr int ROUNDS = 4;
+    int b0 = 0, round = 0;
     unsigned base = 0;   // items before it
+    int s = 0, n = 0, own_round = -1;
     // tiles: per item; keys: per block
     template <bool CHUNK, bool TREE>
     __device__ bool find(const TokensLaunch &p, int tpt, int tiles, int keys, unsigned idx,
@@ -151,15 +166,38 @@ struct ItemWalk {
     {
         const int lane = threadIdx.x & 31;
         const unsigned splits = CHUNK ? p.splits : 1, Hkv = p.Hkv;
+        const bool ordered = CHUNK && p.ordered;
         if (idx < base) {
-            b0 = 0;
+            b0 = round = 0;
             base = 0;
         }
+        if (ordered && own_round < 0) {
+            own_round = ROUNDS;
+            if (lane < p.B) {
+                const unsigned slots = (unsigned)p.n[lane * p.Hkv];
+                seq_range<TREE>(p, lane, s, n);
+                own_round = ROUNDS - 1 - min(slots / (p.C / ROUNDS + 1u), ROUNDS - 1u);
+            }
+        }
+        const int all = n;
 #pragma unroll 1
-        for (; b0 < p.B; b0 += 32) {
-            int s = 0, n = 0;
-            if (b0 + lane < p.B)
-                seq_range<TREE>(p, b0 + lane, s, n);
+        for (;; b0 += 32) {
+            if (b0 >= p.B) {
+                if (!ordered || ++round >= ROUNDS)
+                    break;
+                b0 = 0;
+            }
+            int s = this->s, n = all;
+            if (ordered) {
+                if (own_round != round)
+                    n = 0;
+                if (!__any_sync(0xffffffffu, n > 0))
+                    continue;
+            } else {
+                s = n = 0;
+                if (b0 + lane < p.B)
+                    seq_range<TREE>(p, b0 + lane, s, n);
+            }
             const unsigned ranges = (unsigned)(n + tiles * tpt - 1) / (unsigned)(tiles * tpt);
             unsigned sum = ranges * Hkv * splits;
             // ranges that overlap may add up to more than the grid: sums stop at the largest
@@ -197,6 +235,7 @@ struct ItemWalk {
                     n_keys = 0;
                 }
             }
+            it.keys = n_keys;
             it.shift = n_keys - len;
             const int end = max(0, it.shift + it.tok0 + it.ntok);
             const int blocks = (end + keys - 1) / keys;
@@ -570,7 +609,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
     uint64_t *it_full = o_full + 2, *it_empty = it_full + NI;
     uint64_t *mrg_full = it_empty + NI, *mrg_empty = mrg_full + 4;
     uint64_t *mma_done = mrg_empty + 4;
-    uint64_t *clc_full = mma_done + 1;
+    uint64_t *clc_full = mma_done + 1, *next = clc_full + 1;
     uint4 *clc = reinterpret_cast<uint4 *>(bars + 64);       // a 16-byte answer
     TokItem *s_item = reinterpret_cast<TokItem *>(clc + 1);
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(s_item + NI);
@@ -599,7 +638,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
         }
         for (int i = 0; i < NI; ++i) {
             mbar_init(&it_full[i], 1);
-            mbar_init(&it_empty[i], 1 + 4 * TILES);   // the MMA warp and the row warps
+            mbar_init(&it_empty[i], 2 + 4 * TILES);   // the TMA, the MMA and the row warps
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&mrg_full[i], 1);
@@ -607,16 +646,20 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
         }
         mbar_init(mma_done, 1);
         mbar_init(clc_full, 1);
+        mbar_init(next, 1);
         fence_mbar_init();
     }
     if (warp == W_MMA) {
         tmem_alloc(s_tmem, Cfg::TMEM_COLS);
         tmem_relinquish();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *s_tmem;
+    // What the set-up above wrote is there behind this, which every warp calls once.
+    auto set_up = [&] {
+        tc_fence_before();
+        asm volatile("bar.sync 1, %0;" ::"n"(Cfg::NTHR) : "memory");
+        tc_fence_after();
+        return *s_tmem;
+    };
 
     // The others' waits run out only when no warp has been computing rows again for as long.
     auto spin = [&](uint64_t *bar, uint32_t parity) {
@@ -640,32 +683,24 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
 
     if (warp >= W_TMA) {
     regs_dec<Cfg::REGS_IO>();
-    if (warp == W_TMA) {
-        // ------------------------------------------------ producer
-        if (lane == 0) {
-            prefetch_tmap(&maps.q);
-            prefetch_tmap(&maps.k);
-            prefetch_tmap(&maps.v);
-            prefetch_tmap(&maps.o);
-        }
+    if (warp == Cfg::W_NEXT) {
+        // ------------------------------------------------ the feed: which item comes next
+        // An item is asked for when the one before has LEAD blocks left to load, so that its own loads
+        // follow without the latency of sequence range, slot count and page table; and not
+        // before, so that no CTA holds an item back while others have none.
         ItemWalk walk;
         int idx = blockIdx.x;
-        int n_it = 0, n_q = 0;   // ring slots and query loads
-        bool ok = true;
+        bool ok = true, first = true;
         int n_clc = 0;
         int asked = -1;   // the launch-control request whose answer is still to come
-        for (int k = 0; ok; ++n_clc) {
+        for (int k = 0; ok;) {
             TokItem it;
             it.b = -1;
-            if (idx >= 0) {
-                // the next item while this one runs: take over a CTA that has not started
-                if (lane == 0) {
-                    clc_request(clc, clc_full);
-                    asked = n_clc;
-                }
-                if (!walk.find<CHUNK, TREE>(p, tpt, TILES, TK, idx, it))
-                    it.j0 = it.j1 = it.two = 0;   // the grid is an upper bound
-            }
+            if (idx >= 0 && !walk.find<CHUNK, TREE>(p, tpt, TILES, TK, idx, it))
+                it.j0 = it.j1 = it.two = 0;   // the grid is an upper bound
+            if (first)   // the first item was looked up while the others set up
+                set_up();
+            first = false;
             if (idx < 0 || it.b >= 0) {
                 const int slot = k % NI;
                 if (lane == 0) {
@@ -680,16 +715,66 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                 if (!ok || idx < 0)
                     break;
             }
-            const int n = it.j1 - it.j0;
-            const int unit = it.b * p.Hkv + it.hk;
-            const int per = p.C / PAGE_SLOTS;
-            if (CHUNK && p.block_table)   // the item's part of the page table into L1
+            if (CHUNK && p.block_table && it.b >= 0) {   // the item's part of the page table into L1
+                const int per = p.C / PAGE_SLOTS;
+                const int32_t *table = p.block_table + (size_t)(it.b * p.Hkv + it.hk) * per;
 #pragma unroll 1
                 for (int i = TK / BOX * it.j0 + 32 * lane; i < min(per, TK / BOX * it.j1); i += 1024)
-                    asm volatile("prefetch.global.L1 [%0];" ::"l"(p.block_table +
-                                                                  (size_t)unit * per + i));
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(table + i));
+            }
+            if (CHUNK && idx == 0 && p.splits > 1) {
+                // once per call, for the merge: ranges out of order cannot be bisected
+                bool bad = false;
+#pragma unroll 1
+                for (int b = lane; b < p.B; b += 32) {
+                    const int c0 = p.cu[b], c1 = p.cu[b + 1];
+                    bad |= c0 < 0 || c1 < c0 || c1 > p.L;
+                }
+                bad = __any_sync(0xffffffffu, bad);
+                if (lane == 0)
+                    *p.broken = bad;
+            }
+            int to = -1;
+            if (lane == 0) {
+                // take over a CTA that has not started
+                ok = it.b < 0 || rest(next, (k - 1) & 1);
+                if (ok) {
+                    clc_request(clc, clc_full);
+                    asked = n_clc;
+                    ok = rest(clc_full, n_clc & 1);
+                }
+                if (ok) {
+                    to = clc_answer(clc);
+                    asked = -1;
+                }
+            }
+            ++n_clc;
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            idx = __shfl_sync(0xffffffffu, to, 0);
+        }
+        // the answer to a request after which a wait ran out has landed before the CTA leaves
+        if (lane == 0 && asked >= 0)
+            mbar_wait(clc_full, asked & 1);
+    } else if (warp == W_TMA) {
+        // ------------------------------------------------ producer
+        if (lane == 0) {
+            prefetch_tmap(&maps.q);
+            prefetch_tmap(&maps.k);
+            prefetch_tmap(&maps.v);
+            prefetch_tmap(&maps.o);
+        }
+        set_up();
+        int n_it = 0, n_q = 0;   // ring slots and query loads
+        bool ok = true;
+        TokItem it;
+        for (int k = 0; ok && feed_get(k, it); ++k) {
+            const int n = it.j1 - it.j0;
+            if (n <= Cfg::LEAD)
+                mbar_arrive_warp(next);
+            const int unit = it.b * p.Hkv + it.hk;
+            const int per = p.C / PAGE_SLOTS;
             if (lane == 0 && n > 0) {
-                const int n_keys = CHUNK ? it.shift + p.cu[it.b + 1] - p.cu[it.b] : 0;
+                const int n_keys = it.keys;
                 auto load = [&](const CUtensorMap *map, int j) {
                     const int st = n_it % NS;
                     if (n_it >= NS)
@@ -749,39 +834,17 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
                     ++n_q;
                 }
                 for (int i = 0; ok && i < n; ++i) {
+                    if (i + Cfg::LEAD == n - 1)
+                        mbar_arrive(next);
                     load(&maps.v, it.j0 + i);
                     if (ok && i + ahead < n)
                         load(&maps.k, it.j0 + i + ahead);
                 }
             }
-            if (CHUNK && idx == 0 && p.splits > 1) {
-                // once per call, for the merge: ranges out of order cannot be bisected
-                bool bad = false;
-#pragma unroll 1
-                for (int b = lane; b < p.B; b += 32) {
-                    const int c0 = p.cu[b], c1 = p.cu[b + 1];
-                    bad |= c0 < 0 || c1 < c0 || c1 > p.L;
-                }
-                bad = __any_sync(0xffffffffu, bad);
-                if (lane == 0)
-                    *p.broken = bad;
-            }
-            int next = -1;
-            if (lane == 0 && ok) {
-                ok = rest(clc_full, n_clc & 1);
-                if (ok) {
-                    next = clc_answer(clc);
-                    asked = -1;
-                }
-            }
             ok = __shfl_sync(0xffffffffu, ok, 0);
-            idx = __shfl_sync(0xffffffffu, next, 0);
         }
-        // every copy, and the answer to a request after which a wait ran out, has landed before
-        // the CTA leaves
+        // every copy has landed before the CTA leaves
         if (lane == 0) {
-            if (asked >= 0)
-                mbar_wait(clc_full, asked & 1);
 #pragma unroll 1
             for (int i = n_it > NS ? n_it - NS : 0; i < n_it; ++i)
                 mbar_wait(&kv_full[i % NS], (i / NS) & 1);
@@ -796,7 +859,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
         const Int<1> T1;
         bool ok = true;
         TokItem it;
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t tm = __shfl_sync(0xffffffffu, set_up(), 0);
         // descriptors differ in the start address alone (bits 0..13, in 16 bytes)
         const uint64_t q_desc = sdesc_k_sw128(smem_u32(sq));
         const uint64_t k_desc = sdesc_k_sw128(smem_u32(ring));
@@ -977,10 +1040,13 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
         commit(mma_done);
         mbar_wait(mma_done, 0);
         __syncwarp();
+    } else {
+        set_up();
     }
     } else {
         // ------------------------------------------------ softmax: a thread per row
         regs_inc<Cfg::REGS_ROW>();
+        const uint32_t tmem = set_up();
         const int t = warp >> 2, quarter = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t o_col = lanes + Cfg::COL_O + D * t;
@@ -1300,7 +1366,7 @@ __global__ void __launch_bounds__(TokCfg<D, TILES>::NTHR, TokCfg<D, TILES>::CTAS
     __syncthreads();
     if (warp == W_MMA) {
         tc_fence_after();
-        tmem_dealloc(tmem, Cfg::TMEM_COLS);
+        tmem_dealloc(*s_tmem, Cfg::TMEM_COLS);
     }
     if (threadIdx.x == 0 && *abort)
         flag_error(p.status, DEV_TIMEOUT);
@@ -1449,6 +1515,10 @@ cudaError_t attend_tokens_impl(TokensLaunch p, cudaStream_t s)
     const long items = ranges * p.Hkv * p.splits;
     if (items > 0x7fffffffL)
         return cudaErrorInvalidValue;
+    // Where all CTAs run at once, no order is better than another, and looking the order up costs
+    // a start 1.2 us (3 x 1 to 130 tokens over 1000 slots, split: 10.5 us without, 11.7 with).
+    p.ordered = CHUNK && p.B > 1 && p.B <= 32 && p.splits == 1 &&
+                items > (long)Cfg::CTAS * sm_count();
     k_attend_tokens<D, TILES, CHUNK, TREE><<<(unsigned)items, Cfg::NTHR, Cfg::SMEM, s>>>(maps, p);
     e = cudaGetLastError();
     if (!CHUNK || e != cudaSuccess || p.splits == 1)
@@ -1489,13 +1559,17 @@ TokensPlan plan_tokens(int T, int B, int Hq, int Hkv, int D, int C, int requeste
 {
     const int tpt = TM / (Hq / Hkv), sms = sm_count();
     const long rows = (long)T * Hq;
-    const int mean = (T + B - 1) / B;
     TokensPlan best{1, 1};
     float least = INFINITY;
     for (int tiles = D == 128 ? 2 : 1; tiles >= 1; --tiles) {
         const int keys = 64 * tiles, slots = sms * (3 - tiles);
         const int blocks = (C + keys - 1) / keys;
-        const long items = (long)B * Hkv * ((mean + tiles * tpt - 1) / (tiles * tpt));
+        // Ranges of tokens: sequences of one length have as many each; of others, half a range is
+        // empty on average.
+        const int range = tiles * tpt;
+        const long ranges = T % B == 0 ? (long)B * ((T / B + range - 1) / range)
+                                       : max((long)B, (T + (long)B * range / 2) / range);
+        const long items = ranges * Hkv;
         for (int s = requested > 0 ? requested : 1;; s += 1 + s / 16) {
             const int splits = s < MAX_SPLITS ? s : MAX_SPLITS;
             const long ctas = items * splits;

@@ -132,6 +132,7 @@ struct TokensLaunch {
     int kv_rows;               // chunk: rows of the K / V arrays (set by the launcher)
     int tiles;                 // chunk: tiles per item
     int splits;                // key ranges per item, merged by a second launch when above 1
+    int ordered;               // chunk: items of long units first (set by the launcher)
     float *part_o;             // [splits, Hkv, D / 4, L * g, 4]: sums of the values, fp32
     float2 *part_ml;           // [splits, Hkv, L * g]: reference and sum
     int *broken;               // whether some sequence's range is bad, for the merge
