@@ -232,11 +232,12 @@ struct Weights {
         keep(x, i0);
         split(x, y, ps, qs);
     }
-    // Sum of the range's weights: whole vectors VER_UNROLL strips of 32 at a time, the others (the
-    // row's ends, the range's last strips, a q of another alignment than p's) one by one.
+    // Sum of the range's weights: whole vectors several strips of 32 at a time, the others (the row's
+    // ends, the range's last strips, a q of another alignment than p's) strip by strip.  The last
+    // strips in a predicated group took 75 us for 512 chains of 128000 tokens instead of 71.
     __device__ __forceinline__ uint64_t sum(int v0, int v1) const
     {
-        constexpr int U = VER_UNROLL;
+        constexpr int U = VER_UNROLL, W = 2 * U;     // as many loads in flight without q
         const int lane = threadIdx.x & 31;
         Sum2 sp, sq;
         int v = v0;
@@ -276,17 +277,17 @@ struct Weights {
             const bool patch = n_gone > 0 && patched(v0, v1);
             const float4 *xs = reinterpret_cast<const float4 *>(p.at - p.off) + lane;
 #pragma unroll 1
-            for (; v + 32 * U <= whole; v += 32 * U) {
-                float4 x[U];
+            for (; v + 32 * W <= whole; v += 32 * W) {
+                float4 x[W];
 #pragma unroll
-                for (int u = 0; u < U; ++u)
+                for (int u = 0; u < W; ++u)
                     x[u] = xs[v + 32 * u];
                 if (patch)
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
+                    for (int u = 0; u < W; ++u)
                         keep(x[u], 4 * (v + 32 * u + lane) - p.off);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
+                for (int u = 0; u < W; ++u) {
                     sp.add(make_float2(clean(x[u].x), clean(x[u].y)));
                     sp.add(make_float2(clean(x[u].z), clean(x[u].w)));
                 }
@@ -590,28 +591,38 @@ __global__ void __launch_bounds__(VER_THREADS, 4) k_draft_verify(const VerifyLau
 // ------------------------------------------------------------------ the accepted path's rows
 
 // A CTA per unit.  Rows move down (path[i] >= i), so a group of rows is read whole before it is
-// written, and the rows that later groups read lie behind it.
-constexpr int COMMIT_THREADS = 128, COMMIT_UNROLL = 4;
+// written, and the rows that later groups read lie behind it.  What bounds it is the chain of
+// loads: range, counts and path together, then the page table, then the rows.
+constexpr int COMMIT_THREADS = 128, COMMIT_UNROLL = 2;
 
 template <int D>
 __global__ void __launch_bounds__(COMMIT_THREADS) k_draft_commit(const CommitLaunch p)
 {
     constexpr int CHUNKS = D / 8;                               // of 16 bytes per row
     constexpr int AT_ONCE = COMMIT_THREADS / (2 * CHUNKS);      // rows of K and V per step
+    __shared__ int s_path[COMMIT_THREADS];                      // the path's first nodes
     const int unit = blockIdx.x, b = unit / p.Hkv;
+    const int32_t *path = p.path + (size_t)b * p.max_path;
     const int start = p.cu[b], end = p.cu[b + 1], count = p.count[b];
     const int n = p.n[unit], seqlen = p.seqlen[b];
+    int x = -1, before = -1;
+    if (threadIdx.x < p.max_path) {
+        x = path[threadIdx.x];
+        before = threadIdx.x ? path[threadIdx.x - 1] : -1;
+    }
+    s_path[threadIdx.x] = x;
     const int m = end - start;
-    const int32_t *path = p.path + (size_t)b * p.max_path;
     bool ok = start >= 0 && start <= end && end <= p.T && count >= 0 && count <= m &&
               count <= p.max_path;
-    if (ok)
-        for (int i = threadIdx.x; i < count; i += COMMIT_THREADS) {
-            const int x = path[i], before = i ? path[i - 1] : -1;
-            ok = ok && x > before && x < m;
-        }
+    const bool refused = ok && m > 0 && p.slot_map &&
+                         p.slot_map[(size_t)start * p.Hkv + unit % p.Hkv] < 0;
+    if (ok) {
+        if (threadIdx.x < count)
+            ok = x > before && x < m;
+        for (int i = threadIdx.x + COMMIT_THREADS; i < count; i += COMMIT_THREADS)
+            ok = ok && path[i] > path[i - 1] && path[i] < m;
+    }
     ok = !__syncthreads_or(!ok);
-    const bool refused = ok && m > 0 && p.slot_map && p.slot_map[(size_t)start * p.Hkv + unit % p.Hkv] < 0;
     const bool fits = n >= m && n <= p.C;
     if (threadIdx.x == 0) {
         if (!ok || (!refused && !fits))
@@ -626,28 +637,33 @@ __global__ void __launch_bounds__(COMMIT_THREADS) k_draft_commit(const CommitLau
     uint16_t *base = (part < CHUNKS ? p.K : p.V) + part % CHUNKS * 8;
     const SlotRows rows{p.table, p.C, p.num_pages};
     for (int i0 = 0; i0 < count; i0 += AT_ONCE * COMMIT_UNROLL) {
-        uint4 x[COMMIT_UNROLL];
-        long to[COMMIT_UNROLL];
+        uint4 y[COMMIT_UNROLL];
+        long from[COMMIT_UNROLL], to[COMMIT_UNROLL];
 #pragma unroll
         for (int u = 0; u < COMMIT_UNROLL; ++u) {
             const int i = i0 + u * AT_ONCE + row;
-            to[u] = -1;
-            if (i < count && path[i] != i) {
-                const long from = rows.row(unit, n - m + path[i]);
-                to[u] = rows.row(unit, n - m + i);
-                if (from < 0 || to[u] < 0) {
-                    flag_error(p.status, DEV_CAPACITY);
-                    to[u] = -1;
-                } else {
-                    x[u] = *reinterpret_cast<const uint4 *>(base + from * D);
+            from[u] = to[u] = -1;
+            if (i < count) {
+                const int node = i < COMMIT_THREADS ? s_path[i] : path[i];
+                if (node != i) {
+                    from[u] = rows.row(unit, n - m + node);
+                    to[u] = rows.row(unit, n - m + i);
+                    if (from[u] < 0 || to[u] < 0) {
+                        flag_error(p.status, DEV_CAPACITY);
+                        to[u] = -1;
+                    }
                 }
             }
         }
+#pragma unroll
+        for (int u = 0; u < COMMIT_UNROLL; ++u)
+            if (to[u] >= 0)
+                y[u] = *reinterpret_cast<const uint4 *>(base + from[u] * D);
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < COMMIT_UNROLL; ++u)
             if (to[u] >= 0)
-                *reinterpret_cast<uint4 *>(base + to[u] * D) = x[u];
+                *reinterpret_cast<uint4 *>(base + to[u] * D) = y[u];
     }
 }
 
@@ -662,9 +678,9 @@ cudaError_t launch_tree_plan(const TreePlanLaunch &p, cudaStream_t s)
 // CTAs per sequence.  A pass over a row costs a cluster barrier and what a CTA reads, and many
 // sequences fill the card by themselves: the more there are, the longer a CTA's part has to be.
 // Measured in a graph, us, with 1 / 2 / 4 / 8 / 16 CTAs (drawn trees of up to 6 nodes): one sequence
-// of 32000 tokens 9.6 / 8.9 / 7.8 / 7.7 / 6.9, of 128000 20.8 / 15.3 / 10.8 / 9.0 / 8.2; 64 sequences
-// of 32000 22.5 / 18.3 / 15.6 / 15.9 / 24.1, of 128000 72 / 47 / 30 / 24 / 30; 512 of 32000
-// 40 / 41 / 48 / 69 / 153, of 128000 94 / 81 / 73 / 84 / 139; 1000 tokens take one CTA at any number.
+// of 32000 tokens 9.4 / 8.7 / 7.7 / 8.3 / 7.0, of 128000 18.3 / 15.5 / 10.9 / 8.8 / 8.1; 64 sequences
+// of 32000 22.6 / 18.5 / 15.6 / 16.1 / 24.2, of 128000 73 / 47 / 31 / 24 / 29; 512 of 32000
+// 41 / 40 / 48 / 78 / 153, of 128000 96 / 80 / 68 / 79 / 133; 1000 tokens take one CTA at any number.
 int verify_ctas(int B, int V)
 {
     const int part = 1900 + 64 * (B < 256 ? B : 256), most = B >= 128 ? 4 : B > 32 ? 8 : MAX_CLUSTER;
