@@ -144,6 +144,51 @@ def test_binding_refuses_wrong_types_and_shapes(kvc):
         kvc.kvc_draft_verify(**args)                   # host tensors
 
 
+class DeviceTensor:
+    """What the binding asks of a CUDA tensor, without a GPU."""
+
+    def __init__(self, dtype, shape, device, address=4096):
+        self.dtype, self.shape, self.index, self.address = dtype, torch.Size(shape), device, address
+        self.is_cuda, self.device, self.nbytes = True, torch.device("cuda", device), 1 << 20
+
+    def data_ptr(self): return self.address
+    def get_device(self): return self.index
+    def is_contiguous(self): return True
+    def numel(self): return self.shape.numel()
+    def stride(self, i=None):
+        st = torch.empty(self.shape, device="meta").stride()
+        return st if i is None else st[i]
+
+
+@pytest.mark.parametrize("wrong", ["cu", "path", "mask", "p", "cache"])
+def test_the_calls_refuse_tensors_of_another_device(kvc, monkeypatch, wrong):
+    """With cuda:1 current, one argument of each call on cuda:0 is refused by name of the device."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(kvc, "_raw_stream", lambda dev: 0)
+    on = lambda name: 0 if name == wrong else 1  # noqa: E731
+    i32 = lambda name, *s: DeviceTensor(torch.int32, s, on(name))  # noqa: E731
+    f32 = lambda name, *s: DeviceTensor(torch.float32, s, on(name))  # noqa: E731
+    f16 = lambda name, *s: DeviceTensor(torch.float16, s, on(name))  # noqa: E731
+    cache = kvc.SlotCache(K=f16("cache", 2, 2, 64, 64), V=f16("cache", 2, 2, 64, 64),
+                          pos=i32("cache", 2, 2, 64), n=i32("cache", 2, 2), seqlen=i32("cache", 2))
+    mask = DeviceTensor(torch.int64, (4, 1), on("mask"))
+    q = f16("q", 4, 4, 64)
+    calls = {
+        "cu": [lambda: kvc.kvc_tree_plan(i32("cu", 3), i32("x", 4), mask),
+               lambda: kvc.kvc_draft_commit(cache, i32("cu", 3), i32("path", 2, 4), i32("x", 2))],
+        "path": [lambda: kvc.kvc_draft_commit(cache, i32("cu", 3), i32("path", 2, 4), i32("x", 2))],
+        "mask": [lambda: kvc.kvc_tree_plan(i32("cu", 3), i32("x", 4), mask),
+                 lambda: kvc.kvc_tree_attend(cache, q, i32("cu", 3), mask, q)],
+        "p": [lambda: kvc.kvc_draft_verify(i32("cu", 3), i32("x", 4), f32("p", 4, 9), f32("x", 4),
+                                           f32("x", 2), i32("path", 2, 4), i32("x", 2), i32("x", 2))],
+        "cache": [lambda: kvc.kvc_tree_attend(cache, q, i32("cu", 3), mask, q),
+                  lambda: kvc.kvc_draft_commit(cache, i32("cu", 3), i32("path", 2, 4), i32("x", 2))],
+    }[wrong]
+    for call in calls:
+        with pytest.raises(ValueError, match="expected the current device cuda:1"):
+            call()
+
+
 def test_masks_worked_by_hand():
     tree = [-1, 0, 0, 1, 3, 2]
     assert lineage(tree) == [1, 0b11, 0b101, 0b1011, 0b11011, 0b100101]
