@@ -767,6 +767,7 @@ KVC_API kvc_status kvc_tree_attend(const kvc_tree_args *args, cudaStream_t strea
  * tokens.  A parent that is neither -1 nor an earlier node sets KVC_DEV_CAPACITY and counts as
  * -1 (its node is then nobody's child); a sequence of more than KVC_TREE_MAX_NODES nodes, or
  * whose range leaves [0, T] or runs backwards, counts as one without nodes and sets it too.
+ * path, count and next_token overlap neither one another nor an input.
  * V is at most KVC_DRAFT_MAX_VOCAB.  One launch, no workspace.
  */
 typedef struct kvc_draft_args {

@@ -1551,7 +1551,10 @@ cudaError_t attend_tokens_impl(TokensLaunch p, cudaStream_t s)
 // tokens each, 512 to 32768 slots).  Against 12 numbers of splits from 1 to 64 on two GPUs the
 // choice was within 1% of the best on all of them but one (3 x 40 tokens over 3008 slots: 9
 // and 10%).  A block's time does not depend on D: shapes of 64 channels are predicted a
-// quarter too slow, which changed no choice in the sweep.  The slots that a unit holds are
+// quarter too slow, which changed no choice in the sweep.  300 batches of trees (4 to 48 sequences of
+// 2 to 100 nodes, 3 to 32 KV heads, 1024 to 8192 slots, equal lengths or from a tenth of that on): the
+// choice was 2.4% above the best of both forms and 7 numbers of splits on average, over 10% above it
+// on 25 of them, 44% at most.  The slots that a unit holds are
 // known on the GPU alone, so the capacity stands for them and every unit gets as many ranges:
 // 64 sequences of 4 tokens, one over 32000 slots and the others over 300 to 610 of 32768, are
 // not split and take 359 us, 88 us with num_splits = 8.
@@ -1559,6 +1562,7 @@ TokensPlan plan_tokens(int T, int B, int Hq, int Hkv, int D, int C, int requeste
 {
     const int tpt = TM / (Hq / Hkv), sms = sm_count();
     const long rows = (long)T * Hq;
+    const bool even = T % B == 0;
     TokensPlan best{1, 1};
     float least = INFINITY;
     for (int tiles = D == 128 ? 2 : 1; tiles >= 1; --tiles) {
@@ -1567,13 +1571,16 @@ TokensPlan plan_tokens(int T, int B, int Hq, int Hkv, int D, int C, int requeste
         // Ranges of tokens: sequences of one length have as many each; of others, half a range is
         // empty on average.
         const int range = tiles * tpt;
-        const long ranges = T % B == 0 ? (long)B * ((T / B + range - 1) / range)
-                                       : max((long)B, (T + (long)B * range / 2) / range);
+        const long ranges = even ? (long)B * ((T / B + range - 1) / range)
+                                 : max((long)B, (T + (long)B * range / 2) / range);
         const long items = ranges * Hkv;
         for (int s = requested > 0 ? requested : 1;; s += 1 + s / 16) {
             const int splits = s < MAX_SPLITS ? s : MAX_SPLITS;
             const long ctas = items * splits;
-            const long rounds = (ctas + slots - 1) / slots;
+            // sequences that bring different numbers of tokens hold different numbers of slots
+            // as a rule, and then the last round's CTAs do not end together
+            const float rounds = even ? (float)((ctas + slots - 1) / slots)
+                                      : fmaxf(1.f, (float)ctas / slots);
             const int per = (blocks + splits - 1) / splits;
             float us = tiles == 2 ? rounds * (1.19f * per + 3.9f)
                                   : rounds * (0.83f * per + 1.5f) * (ctas > sms ? 1.3f : 1.f);
