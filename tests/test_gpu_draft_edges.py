@@ -185,3 +185,122 @@ def test_a_captured_call_and_a_direct_one_do_not_share_state(kvc):
         for got, w in zip(x["out"], want):
             assert (n(got) == w).all()
     assert device_status_clean(kvc)
+
+
+@pytest.mark.parametrize("policy", ["h2o", "stream"])
+def test_steps_over_caches_that_are_evicted(kvc, policy):
+    """Speculative steps over a budget of 48 slots: append, attention, commit, eviction.  Each unit
+    holds what the policy keeps of the certain tokens, with their rows and positions; the nodes'
+    attention was over that and their ancestors; slots behind a unit's have the score 0."""
+    rng, gen = np.random.default_rng(3), _gen(3)
+    B, Hkv, g, D, C, n_first, n_recent = 3, 2, 4, 128, 128, 16, 32
+    cache = kvc.SlotCache.empty(B, Hkv, C, D)
+    scores = torch.zeros(B, Hkv, C, device="cuda")
+    rows_k = [[{} for _ in range(Hkv)] for _ in range(B)]      # of each unit: position -> row
+    rows_v = [[{} for _ in range(Hkv)] for _ in range(B)]
+    k, v = _randn(gen, B, Hkv, 70, D), _randn(gen, B, Hkv, 70, D)
+    kvc.kvc_append(cache, k, v)
+    scores[:, :, :70] = torch.rand(B, Hkv, 70, generator=gen, device="cuda")
+    for b in range(B):
+        for h in range(Hkv):
+            rows_k[b][h] = {i: k[b, h, i] for i in range(70)}
+            rows_v[b][h] = {i: v[b, h, i] for i in range(70)}
+    length = [70] * B
+
+    def evict():
+        table = scores.clone()
+        pos, n = cache.pos.tolist(), cache.n.tolist()
+        if policy == "h2o":
+            kvc.kvc_h2o_evict(cache, scores, n_first, n_recent)
+        else:
+            kvc.kvc_stream_evict(cache, n_first, n_recent)
+        for b in range(B):
+            for h in range(Hkv):
+                held = sorted(rows_k[b][h])
+                recent = [p for p in held if p >= length[b] - n_recent]
+                older = [p for p in held if p < length[b] - n_recent]
+                if policy == "stream":
+                    keep = [p for p in older if p < n_first] + recent
+                else:
+                    s = {pos[b][h][j]: table[b, h, j].item() for j in range(n[b][h])}
+                    keep = sorted(older, key=lambda p: (-s[p], p))[:n_first] + recent
+                for rows in (rows_k, rows_v):
+                    rows[b][h] = {p: rows[b][h][p] for p in keep}
+
+    def check():
+        for b in range(B):
+            assert cache.seqlen[b] == length[b]
+            for h in range(Hkv):
+                n = int(cache.n[b, h])
+                pos = cache.pos[b, h, :n].tolist()
+                assert sorted(pos) == sorted(rows_k[b][h])
+                assert torch.equal(cache.K[b, h, :n], torch.stack([rows_k[b][h][p] for p in pos]))
+                assert torch.equal(cache.V[b, h, :n], torch.stack([rows_v[b][h][p] for p in pos]))
+                if policy == "h2o":
+                    assert (scores[b, h, n:] == 0).all()
+
+    evict()
+    check()
+    for _ in range(5):
+        m = rng.integers(1, 20, B).tolist()
+        trees = [random_tree(rng, x, 4) for x in m]
+        T, cu = sum(m), _cu(m)
+        k, v, q = _randn(gen, T, Hkv, D), _randn(gen, T, Hkv, D), _randn(gen, T, g * Hkv, D)
+        slots = torch.empty(T, Hkv, dtype=torch.int32, device="cuda")
+        mask = torch.zeros(T, 1, dtype=torch.int64, device="cuda")
+        kvc.kvc_tree_plan(cu, _i32(sum(trees, [])), mask)
+        kvc.kvc_append_plan(cache, cu, slots)
+        kvc.kvc_append_packed(cache, k, v, slots)
+        o = torch.empty_like(q)
+        ws = torch.empty(max(kvc.kvc_tree_workspace_size(cache, q) // 4, 4), device="cuda")
+        kvc.kvc_tree_attend(cache, q, cu, mask, o, workspace=ws)
+        paths, t = [], 0
+        for b, tree in enumerate(trees):
+            w, bits = slice(t, t + m[b]), lineage(tree)
+            t += m[b]
+            for h in range(g * Hkv):
+                kk = torch.cat([torch.stack(list(rows_k[b][h // g].values())), k[w, h // g]])
+                vv = torch.cat([torch.stack(list(rows_v[b][h // g].values())), v[w, h // g]])
+                check_rows(o[w, h], None, attend_seen(q[w, h], kk, vv, seen_slots(bits, len(kk), m[b])))
+            path, i = [], int(rng.integers(0, m[b]))
+            while i >= 0:
+                path.append(i)
+                i = tree[i]
+            paths.append(path[::-1])
+            for h in range(Hkv):
+                for d, i in enumerate(paths[b]):
+                    rows_k[b][h][length[b] + d] = k[w][i, h]
+                    rows_v[b][h][length[b] + d] = v[w][i, h]
+            length[b] += len(paths[b])
+        most = max(map(len, paths))
+        kvc.kvc_draft_commit(cache, cu, _i32([p + [-1] * (most - len(p)) for p in paths]),
+                             _i32([len(p) for p in paths]), slot_map=slots)
+        check()
+        scores[:, :, :C] = torch.where(torch.arange(C, device="cuda") < cache.n[..., None],
+                                       scores + torch.rand(scores.shape, generator=gen, device="cuda"), scores)
+        evict()
+        check()
+    assert device_status_clean(kvc)
+
+
+def test_more_sequences_than_a_grid_row_holds(kvc):
+    """70 000 chains of two nodes, a few tokens each."""
+    gen, B, V = _gen(9), 70_000, 5
+    p = torch.softmax(torch.randn(2 * B, V, generator=gen, device="cuda"), 1)
+    tokens = torch.randint(0, V, (2 * B,), generator=gen, device="cuda").int()
+    u, u_next = torch.rand(2 * B, generator=gen, device="cuda"), torch.rand(B, generator=gen, device="cuda")
+    path, count, nxt = (torch.empty(*s, dtype=torch.int32, device="cuda") for s in ((B, 2), (B,), (B,)))
+    cu = torch.arange(0, 2 * B + 1, 2, dtype=torch.int32, device="cuda")
+    mask = torch.zeros(2 * B, 1, dtype=torch.int64, device="cuda")
+    kvc.kvc_tree_plan(cu, _i32([-1, 0] * B), mask)
+    assert (mask[0::2] == 1).all() and (mask[1::2] == 3).all()
+    kvc.kvc_draft_verify(cu, tokens, p, u, u_next, path, count, nxt)
+    px = p.double()[0::2].gather(1, tokens[1::2].long()[:, None])[:, 0]
+    take = u[1::2].double() < px
+    assert torch.equal(count == 2, take) and torch.equal(path[:, 1] == 1, take) and (path[:, 0] == 0).all()
+    w = torch.where(take[:, None], p.double()[1::2], p.double()[0::2])
+    w = torch.where(take[:, None] | (torch.arange(V, device="cuda") != tokens[1::2, None]), w, 0.0)
+    below = w.cumsum(1)
+    want = (below <= u_next.double()[:, None] * below[:, -1:]).sum(1)
+    assert torch.equal(nxt.long(), want)
+    assert device_status_clean(kvc)
