@@ -373,6 +373,9 @@ __global__ void __launch_bounds__(VER_THREADS, 4) k_draft_verify(const VerifyLau
     const int b = blockIdx.x / size, rank = blockIdx.x - b * size;
     const int warp = __shfl_sync(ALL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const bool drawn = p.q != nullptr;
+    if (size > 1)
+        cluster_arrive();        // waited for before the first store to another CTA
+    bool joined = size == 1;
     int start, len;
     node_range(p.cu, b, p.T, MAX_NODES, p.status, start, len);
     if (threadIdx.x == 0 && len > 0)
@@ -391,10 +394,7 @@ __global__ void __launch_bounds__(VER_THREADS, 4) k_draft_verify(const VerifyLau
         s.p[i] = in ? clean(p.p[(start + up) * p.ps + x]) : 0.f;
         s.q[i] = in && drawn ? clean(p.q[(start + up) * p.qs + x]) : 0.f;
     }
-    if (size > 1)
-        cluster_sync_all();      // every CTA of the cluster runs: its shared memory may be written
-    else
-        __syncthreads();
+    __syncthreads();
 
     // The walk is warp 0's; its state waits in shared memory during the passes over a row: for the
     // residual's mass, then for the next token.
@@ -530,6 +530,9 @@ __global__ void __launch_bounds__(VER_THREADS, 4) k_draft_verify(const VerifyLau
             total += s.warp[0][i];
         at = 0;
         if (size > 1) {
+            if (!joined)         // every CTA of the cluster runs: its shared memory may be written
+                cluster_wait();
+            joined = true;
             if (threadIdx.x < size)
                 st_cluster_u64(&s.total[phase][rank], threadIdx.x, total);
             cluster_sync_all();
@@ -586,6 +589,8 @@ __global__ void __launch_bounds__(VER_THREADS, 4) k_draft_verify(const VerifyLau
         for (int i = threadIdx.x; i < p.max_path; i += VER_THREADS)
             p.path[(size_t)b * p.max_path + i] = i < s.count ? s.path[i] : -1;
     }
+    if (!joined)
+        cluster_wait();
 }
 
 // ------------------------------------------------------------------ the accepted path's rows
