@@ -797,9 +797,11 @@ KVC_API kvc_status kvc_draft_verify(const kvc_draft_args *args, cudaStream_t str
  * own until a kvc_append_plan with release; scores of kvc_h2o_evict are not touched (nodes have
  * the score 0, kvc_tree_attend adds nothing to it).
  *   path      [B, max_path] int32, count [B] int32
- *   slot_map  optional [T, Hkv] of the kvc_append_plan that brought the nodes: a unit whose
- *             entry of node 0 is -1 was refused, does not hold the nodes and is left as it is.
- *             Without it such a unit loses its newest slots instead
+ *   slot_map  optional [T, Hkv] of the kvc_append_plan that brought the nodes: with it a unit
+ *             that the append refused, which does not hold the nodes, is left as it is; without
+ *             it such a unit loses its newest slots instead.  Refused is a unit whose entry of
+ *             node 0 is -1, unless each of its nodes with the entry -1 lies on a slot whose
+ *             table entry is no page: such a unit took its nodes
  *   T         tokens in all; the bound of the ranges in cu_new
  *   next      gives the arrays n and seqlen to write: the cache itself, or another one of the
  *             same B and Hkv (then all counts are written); K and V rows move in place

@@ -619,8 +619,20 @@ __global__ void __launch_bounds__(COMMIT_THREADS) k_draft_commit(const CommitLau
     const int m = end - start;
     bool ok = start >= 0 && start <= end && end <= p.T && count >= 0 && count <= m &&
               count <= p.max_path;
-    const bool refused = ok && m > 0 && p.slot_map &&
-                         p.slot_map[(size_t)start * p.Hkv + unit % p.Hkv] < 0;
+    const bool fits = n >= m && n <= p.C;
+    bool refused = ok && m > 0 && p.slot_map &&
+                   p.slot_map[(size_t)start * p.Hkv + unit % p.Hkv] < 0;
+    const SlotRows rows{p.table, p.C, p.num_pages};
+    if (refused && fits && p.table) {
+        // A unit whose first new slot lies on no page has no row for node 0 either, and took its
+        // nodes.  In its case every node without a row is on such a slot; of a refused unit the
+        // slots looked at are older ones, on pages that it holds.
+        bool page = false;
+        for (int i = threadIdx.x; i < m; i += COMMIT_THREADS)
+            page |= p.slot_map[(size_t)(start + i) * p.Hkv + unit % p.Hkv] < 0 &&
+                    rows.row(unit, n - m + i) >= 0;
+        refused = __syncthreads_or(page);
+    }
     if (ok) {
         if (threadIdx.x < count)
             ok = x > before && x < m;
@@ -628,7 +640,6 @@ __global__ void __launch_bounds__(COMMIT_THREADS) k_draft_commit(const CommitLau
             ok = ok && path[i] > path[i - 1] && path[i] < m;
     }
     ok = !__syncthreads_or(!ok);
-    const bool fits = n >= m && n <= p.C;
     if (threadIdx.x == 0) {
         if (!ok || (!refused && !fits))
             flag_error(p.status, DEV_CAPACITY);
@@ -640,7 +651,6 @@ __global__ void __launch_bounds__(COMMIT_THREADS) k_draft_commit(const CommitLau
         return;
     const int row = threadIdx.x / (2 * CHUNKS), part = threadIdx.x % (2 * CHUNKS);
     uint16_t *base = (part < CHUNKS ? p.K : p.V) + part % CHUNKS * 8;
-    const SlotRows rows{p.table, p.C, p.num_pages};
     for (int i0 = 0; i0 < count; i0 += AT_ONCE * COMMIT_UNROLL) {
         uint4 y[COMMIT_UNROLL];
         long from[COMMIT_UNROLL], to[COMMIT_UNROLL];
