@@ -1545,47 +1545,50 @@ cudaError_t attend_tokens_impl(TokensLaunch p, cudaStream_t s)
 
 } // namespace
 
-// Form and splits of a chunk, by what a call takes in microseconds: a start, then each
-// round of CTAs its key blocks and an item's start and end, then the merge.  The numbers
-// are fitted to a sweep of forms and splits over 24 shapes (1 to 32 sequences, 1 to 600
-// tokens each, 512 to 32768 slots).  Against 12 numbers of splits from 1 to 64 on two GPUs the
-// choice was within 1% of the best on all of them but one (3 x 40 tokens over 3008 slots: 9
-// and 10%).  A block's time does not depend on D: shapes of 64 channels are predicted a
-// quarter too slow, which changed no choice in the sweep.  300 batches of trees (4 to 48 sequences of
-// 2 to 100 nodes, 3 to 32 KV heads, 1024 to 8192 slots, equal lengths or from a tenth of that on): the
-// choice was 2.4% above the best of both forms and 7 numbers of splits on average, over 10% above it
-// on 25 of them, 44% at most.  The slots that a unit holds are
-// known on the GPU alone, so the capacity stands for them and every unit gets as many ranges:
-// 64 sequences of 4 tokens, one over 32000 slots and the others over 300 to 610 of 32768, are
-// not split and take 359 us, 88 us with num_splits = 8.
+// Form and splits of a chunk, by what a call takes in microseconds: a start, then each round of
+// CTAs its key blocks and an item's start and end, then the merge.  How many tokens a sequence
+// brings is known on the GPU alone.  So the rounds are a mean of two estimates: of sequences of one
+// length, whose rounds end together and count whole, and, with up to half the weight (one sequence
+// has one length), of sequences a quarter longer or shorter, whose rounds run into one another.
+// Both follow T without regard to what divides it.  The numbers are fitted to 1700 batches of 1 to
+// 96 sequences of 1 to 400 tokens over 128 to 32768 slots, of one length or ragged, over caches of
+// one length or ragged.  On 1110 others (220 of them of 200 to 4096 tokens over up to 65536
+// slots), each with both forms and up to 17 numbers of splits, the choice was 2.5% above the best
+// on average and over 10% above it on 88; by the first estimate alone, with numbers fitted to it,
+// 3.1% and 109, by the second where B does not divide T 4.0% and 150.  Of 48 sequences of 2 to
+// 4 tokens over 1024 slots, 192 items of one tile, the second takes two tiles for 23.4 us, one takes
+// 19.5; of 64 trees of 8 to 24 nodes over 576 slots the first takes two for 49 us, one takes 40.  A
+// block's time does not depend on D.  The slots that a unit holds are known on the GPU alone too:
+// the capacity stands for them and every unit gets as many ranges.  64 sequences of 4 tokens, one
+// over 32000 slots and the others over 300 to 610 of 32768, are not split and take 359 us, 88 us
+// with num_splits = 8.
 TokensPlan plan_tokens(int T, int B, int Hq, int Hkv, int D, int C, int requested)
 {
     const int tpt = TM / (Hq / Hkv), sms = sm_count();
     const long rows = (long)T * Hq;
-    const bool even = T % B == 0;
+    const float weight = 0.5f - 0.5f / B;   // of the uneven estimate
+    auto ceil_div = [](long x, long y) { return (x + y - 1) / y; };
     TokensPlan best{1, 1};
     float least = INFINITY;
     for (int tiles = D == 128 ? 2 : 1; tiles >= 1; --tiles) {
         const int keys = 64 * tiles, slots = sms * (3 - tiles);
         const int blocks = (C + keys - 1) / keys;
-        // Ranges of tokens: sequences of one length have as many each; of others, half a range is
-        // empty on average.
-        const int range = tiles * tpt;
-        const long ranges = even ? (long)B * ((T / B + range - 1) / range)
-                                 : max((long)B, (T + (long)B * range / 2) / range);
-        const long items = ranges * Hkv;
+        const long range = (long)B * tiles * tpt;   // a range of tokens in every sequence
+        const long items = (long)B * Hkv * ceil_div(T, range);
+        const float uneven =
+            0.5f * B * Hkv * (ceil_div(3L * T, 4 * range) + ceil_div(5L * T, 4 * range));
+        // CTAs of the one-tile form share an SM
+        auto shared = [&](float ctas) { return tiles == 1 && ctas > sms ? 1.2f : 1.f; };
         for (int s = requested > 0 ? requested : 1;; s += 1 + s / 16) {
             const int splits = s < MAX_SPLITS ? s : MAX_SPLITS;
             const long ctas = items * splits;
-            // sequences that bring different numbers of tokens hold different numbers of slots
-            // as a rule, and then the last round's CTAs do not end together
-            const float rounds = even ? (float)((ctas + slots - 1) / slots)
-                                      : fmaxf(1.f, (float)ctas / slots);
+            const float more = uneven * splits;
+            const float rounds = (1.f - weight) * ceil_div(ctas, slots) * shared(ctas) +
+                                 weight * fmaxf(1.f, more / slots) * shared(more);
             const int per = (blocks + splits - 1) / splits;
-            float us = tiles == 2 ? rounds * (1.19f * per + 3.9f)
-                                  : rounds * (0.83f * per + 1.5f) * (ctas > sms ? 1.3f : 1.f);
+            float us = rounds * (tiles == 2 ? 1.3f * per + 5.f : 0.7f * per + 3.f);
             if (splits > 1)
-                us += 3.1f + 0.08f * splits + (float)rows * splits * D * 1.35e-6f;
+                us += 2.5f + 0.08f * splits + (float)rows * splits * D * 1.35e-6f;
             if (us < least) {
                 least = us;
                 best = TokensPlan{tiles, splits};
