@@ -755,16 +755,21 @@ KVC_API kvc_status kvc_tree_attend(const kvc_tree_args *args, cudaStream_t strea
  *   parent      [T] int32, or NULL: every sequence is a chain
  *   tokens      [T] int32; a token outside [0, V) is refused (with weight 0)
  *   p, q        rows of V adjacent fp32 entries; p_stride, q_stride elements between rows, at
- *               least V.  Any 4-byte aligned address.  Entries that are NaN or negative count as
- *               0, entries above 1 as 1; rows need to sum to 1 within rounding (of a row that
+ *               least V.  Any 4-byte aligned address; where a row of q begins at another
+ *               place of a 16-byte vector than p's, a pass over both reads entry by entry (512
+ *               chains of 128000 tokens 94 us instead of 71).  Entries that are NaN or negative
+ *               count as 0, entries above 1 as 1; rows need to sum to 1 within rounding (of a row that
  *               does not, the token drawn is unspecified, but a token of positive weight)
  *   u           [T] fp32 (a node that starts the walk needs none), u_next [B] fp32
  *   path        [B, max_path] int32: the accepted nodes, node 0 first, then -1
  *   count       [B] int32: how many (0 for a sequence without nodes)
  *   next_token  [B] int32; -1 for a sequence without nodes, and where p is 0 throughout
- * Sums are 64-bit fixed-point numbers of 2^-52 over entries held exactly, so that the border
- * between two tokens is where 64-bit arithmetic has it and the same inputs always give the same
- * tokens.  A parent that is neither -1 nor an earlier node sets KVC_DEV_CAPACITY and counts as
+ * Sums are 64-bit fixed-point numbers of 2^-52, each thread's part of them a pair of 32-bit ones.
+ * The border between two tokens lies within V 2^-50 (10^-10 at 128000 tokens; V up to 2^19) of
+ * where exact arithmetic has it, as a rule within some 2^-48; with a residual within (1 + a) times
+ * that, and tokens whose p is within 2^-23 p of a q may count or not.  The same call always gives
+ * the same tokens.  How many CTAs share a row follows from B and V, so that with another batch
+ * around a sequence its borders may lie elsewhere within these bounds.  A parent that is neither -1 nor an earlier node sets KVC_DEV_CAPACITY and counts as
  * -1 (its node is then nobody's child); a sequence of more than KVC_TREE_MAX_NODES nodes, or
  * whose range leaves [0, T] or runs backwards, counts as one without nodes and sets it too.
  * path, count and next_token overlap neither one another nor an input.

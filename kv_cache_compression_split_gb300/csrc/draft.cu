@@ -77,8 +77,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tree_plan(const TreePlanLaunch
 // less, and there are V borders: with 32-bit sums (off by 10^-8) one token in a few hundred would
 // be another one than 64-bit arithmetic draws.  64-bit floating point runs at two operations per
 // clock and SM here, so a thread adds in pairs of 32-bit numbers: each addition's exact rounding
-// error (six additions, without a branch) goes into a second sum.  What is lost is 2^-48 of a
-// thread's sum.  The pair becomes one 64-bit number of units 2^-52, and from there on all sums are
+// error (Knuth's two-sum: six additions, without a branch) goes into a second sum, which is
+// rounded itself.  Of a sum of N entries up to N^2 2^-49 of it is lost, 2^-37 at 64, and as a rule
+// some 2^-48; 32-bit sums lose N 2^-25.  The pair becomes one 64-bit number of units 2^-52, and from there on all sums are
 // integers, which add up in any order to the same.  The mass of the residual max(p - a q, 0) is
 // sum p - a sum q over the tokens with p > a q: two such sums, a multiplied in once.  A token
 // that the rounding of a moves across that border has a weight of 2^-24 of its probability.
