@@ -169,3 +169,27 @@ def test_draws_near_a_border_do_not_depend_on_the_batch(kvc, V):
     for B in (16, 64, 200, 520):
         which = torch.arange(B, device="cuda") % 16
         assert _draw(kvc, p[which].contiguous(), u[which]) == [want[i % 16] for i in range(B)]
+
+
+def test_the_largest_vocabulary(kvc):
+    """2^24 tokens: trees with siblings, drawn and given, and the first and last tokens of a row."""
+    gen, V, tree = _gen(24), 1 << 24, [-1, 0, 0]
+    assert V == kvc.DRAFT_MAX_VOCAB
+    p, q = _probs(gen, 3, V)
+    tokens = _drafts(gen, [tree], q, V)
+    for seed in range(4):
+        u = torch.rand(3, generator=gen, device="cuda") ** 0.25
+        u_next = torch.rand(1, generator=gen, device="cuda")
+        for vq in (q, None):
+            got = _verify(kvc, [3], tokens, p, u, u_next, 3, parent=_i32(tree), q=vq)
+            assert device_status_clean(kvc)
+            check_verify(got, [tree], tokens, p, vq, u, u_next, 3)
+    p = torch.zeros(2, V, device="cuda")
+    p[:, 0] = p[:, -1] = 0.5
+    tokens = _i32([0, V - 1])
+    for x, u_next, want in ((0.9, 0.25, [1, 0]), (0.9, 0.75, [1, V - 1]), (0.1, 0.75, [2, V - 1])):
+        _, count, nxt = _verify(kvc, [2], tokens, p, torch.full((2,), x, device="cuda"),
+                                torch.full((1,), u_next, device="cuda"), 2)
+        # a refused last token leaves the first one alone
+        assert count.item() == want[0] and nxt.item() == (0 if x == 0.9 else want[1])
+    assert device_status_clean(kvc)
