@@ -773,7 +773,7 @@ static size_t chunk_bytes(const kvc_chunk_args *a, int splits)
 
 size_t kvc_chunk_workspace_size(const kvc_chunk_args *a)
 {
-    if (check_chunk(a) != KVC_OK)
+    if (check_chunk(a) != KVC_OK || a->T == 0)
         return 0;
     return chunk_bytes(a, chunk_plan(a).splits);
 }
@@ -869,8 +869,10 @@ kvc_status kvc_draft_verify(const kvc_draft_args *a, cudaStream_t stream)
     if (!a || a->B <= 0 || a->T < 0 || a->V <= 0 || a->max_path <= 0 || !a->cu_new || !a->path ||
         !a->count || !a->next_token)
         return KVC_ERR_INVALID_ARG;
-    if (a->T > 0 && (!a->tokens || !a->p || !a->u || !a->u_next || reinterpret_cast<uintptr_t>(a->p) % 4 || reinterpret_cast<uintptr_t>(a->q) % 4 ||
-                     a->p_stride < a->V || (a->q && a->q_stride < a->V)))
+    if (a->T > 0 && (!a->tokens || !a->p || !a->u || !a->u_next ||
+                     reinterpret_cast<uintptr_t>(a->p) % 4 ||
+                     reinterpret_cast<uintptr_t>(a->q) % 4 || a->p_stride < a->V ||
+                     (a->q && a->q_stride < a->V)))
         return KVC_ERR_INVALID_ARG;
     if (a->V > KVC_DRAFT_MAX_VOCAB || a->B > INT_MAX / 16)
         return KVC_ERR_UNSUPPORTED;

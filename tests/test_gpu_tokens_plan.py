@@ -36,3 +36,12 @@ def test_a_batch_that_divides_evenly_is_planned_like_its_neighbours(kvc, B, Hq, 
             continue
         less, here, more = (_splits(kvc, cache, Hq, T + i) for i in (-1, 0, 1))
         assert min(less, more) <= here <= max(less, more), (T, less, here, more)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,D,C", [(8, 64, 8, 128, 16384), (1, 8, 1, 64, 2048), (96, 32, 32, 128, 1024)])
+@pytest.mark.parametrize("splits", [0, 5])
+def test_no_tokens_need_no_workspace(kvc, B, Hq, Hkv, D, C, splits):
+    cache = kvc.SlotCache.empty_paged(B, Hkv, C, D, 64)
+    q = torch.empty(0, Hq, D, dtype=torch.float16, device="cuda")
+    assert kvc.kvc_chunk_workspace_size(cache, q, splits) == 0
+    assert kvc.kvc_tree_workspace_size(cache, q, splits) == 0
