@@ -152,8 +152,8 @@ __device__ __forceinline__ void seq_range(const TokensLaunch &p, int b, int &sta
 // runs while other SMs have nothing left.  So up to 32 sequences, one per lane, whose items do
 // not all run at once are walked in four rounds, those of most slots first (by the first
 // head's): 16 trees over 1000 to 8192 slots of 32 heads 217 us as they come, 215 in this order, 4
-// chunks of 257 to 512 tokens over 2000 to 8192 slots 178 and 155.  Of more sequences the items
-// are many against the CTAs that run.
+// chunks of 257 to 512 tokens over 2000 to 8192 slots 178 and 155.  More than 32 sequences, and
+// the heads of a sequence, are walked as they come.
 struct ItemWalk {
     static constexpr int ROUNDS = 4;
     int b0 = 0, round = 0;
